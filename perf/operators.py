@@ -294,9 +294,9 @@ def _mix(x):
 def _random(first, total, t, device):
     """20 random bits for each element's m and r, from its position, the step and the seed."""
     key = _mix(_mix(torch.tensor(t, dtype=torch.int32, device=device)) ^ SEED)
-    group = torch.arange(first // 16, (first + total) // 16, dtype=torch.int32, device=device)
-    lane = torch.arange(16, dtype=torch.int32, device=device) * (0x9E3779B9 - (1 << 32))
-    s = ((_mix(group ^ key)[:, None] + lane) * (0xBB67AE85 - (1 << 32))).view(-1)
+    a = _mix(torch.arange(first // 16, (first + total) // 16, dtype=torch.int32, device=device) ^ key)
+    lane = torch.arange(16, dtype=torch.int32, device=device)
+    s = (a[:, None] + _mix(a + 0x6A09E667)[:, None] * lane).view(-1)
     return (s >> 12) & 0xFFFFF, ((s & 0xFFFF) << 4) | ((s >> 28) & 0xF)
 
 
@@ -403,8 +403,8 @@ def _exact_random(at, t):
         x = _times(x, 0x9E3779B9)
         return x ^ (x >> 16)
 
-    key = mix(mix(torch.tensor(t, device=at.device)) ^ SEED)
-    return _times((mix((at // 16) ^ key) + (at % 16) * 0x9E3779B9) & word, 0xBB67AE85)
+    a = mix((at // 16) ^ mix(mix(torch.tensor(t, device=at.device)) ^ SEED))
+    return (a + (at % 16) * mix((a + 0x6A09E667) & word)) & word
 
 
 def _times(x, k):
