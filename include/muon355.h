@@ -379,6 +379,164 @@ muon_status_t muon_adamw(const muon_tensor_list_t* tensors, int64_t step, float 
                          float beta2, float eps, float weight_decay, void* stream);
 
 /*
+ * One step's control block, in DEVICE memory (64 bytes, 16-byte aligned,
+ * owned by the caller): muon_grad_norm writes it, and the calls that take a
+ * `control` argument read it when they RUN, not when they are enqueued.  A
+ * captured step that replays therefore clips by its own gradients' norm and
+ * counts its own steps.  Before the first use: lr_factor = 1, the rest 0.
+ */
+typedef struct muon_step_control {
+  float norm;          /* global 2-norm of the gradients */
+  float scale;         /* factor of every gradient: min(1, max_norm / norm) */
+  float lr_factor;     /* factor of lr; written by the caller only */
+  int32_t skip;        /* nonzero: this step changes no parameter and no state */
+  int64_t step;        /* t: steps begun and not skipped */
+  int64_t skipped;     /* steps skipped */
+  int32_t reserved[8]; /* zero */
+} muon_step_control_t;
+
+/* A gradient of a muon_grad_list: numel elements in one contiguous run,
+ * aligned to its element size (16-byte aligned runs are read fastest). */
+typedef struct muon_grad {
+  const void* data;
+  int64_t numel;       /* >= 0 */
+  int64_t first_chunk; /* chunks of the tensors before it in the list */
+  int32_t dtype;       /* muon_dtype_t; the types of a list may differ */
+  int32_t reserved;    /* 0 */
+} muon_grad_t;
+
+#define MUON_GRAD_CHUNK 16384
+
+/* Gradients of any number and types.  Both arrays lie in DEVICE memory and
+ * are only read.  Tensor i takes ceil(numel / MUON_GRAD_CHUNK) chunks, and
+ * chunk_tensor[c] names the tensor of chunk c.  An entry outside [0, count)
+ * or a chunk outside its tensor is passed over, so a wrong table reads
+ * nothing outside the tensors. */
+typedef struct muon_grad_list {
+  int64_t count;               /* tensors, >= 1 */
+  int64_t total_chunks;        /* 0 .. 2^31-1 (0: every tensor is empty) */
+  const muon_grad_t* grads;    /* device array [count] */
+  const int32_t* chunk_tensor; /* device array [total_chunks] */
+} muon_grad_list_t;
+
+/*
+ * Global gradient norm, clip factor and step count:
+ *   norm  = sqrt(sum of g^2 over every element of every tensor)
+ *   scale = min(1, max_norm / norm)   (NaN when norm is NaN)
+ *   skip  = (flags & MUON_SKIP_NONFINITE) and norm is not finite
+ *   step += 1, or skipped += 1 when skip
+ * The gradients are only read: the calls that take `control` multiply by
+ * `scale` as they read them.  Squares and sums are fp64 in an order that
+ * depends on the list alone, so no finite gradient overflows and equal
+ * inputs give equal bits.
+ *
+ * max_norm : > 0; infinity never clips.  flags: 0 or MUON_SKIP_NONFINITE.
+ * workspace: at least muon_grad_norm_workspace bytes, 16-byte aligned; holds
+ *            temporaries of this call alone.
+ */
+#define MUON_SKIP_NONFINITE 1
+
+size_t muon_grad_norm_workspace(int64_t total_chunks);
+muon_status_t muon_grad_norm(const muon_grad_list_t* grads, float max_norm, int flags,
+                             muon_step_control_t* control, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * AdamW ([GUIDE] sections 5 and 6) over many tensors in one launch, whatever
+ * their types, each with its own weight decay and learning-rate factor, and
+ * with its moments in 32 bits or in 8.
+ *
+ * The update, in fp32 (bias corrections from t in double):
+ *   g <- scale * g
+ *   m <- beta1*m + (1-beta1)*g;   v <- beta2*v + (1-beta2)*g^2
+ *   theta <- (1 - l*weight_decay)*theta - l*(m / (1-beta1^t)) / (sqrt(v / (1-beta2^t)) + eps)
+ * with l = lr * lr_factor of the tensor.  A BF16 theta is rounded once to nearest even.
+ *
+ * 32-bit state: m and v are float[numel], zero before step 1.
+ *
+ * 8-bit state: m and r = sqrt(v) are e4m3 codes (OCP: 4 exponent and 3
+ * mantissa bits, largest value 448), one scale each for every 256
+ * consecutive elements: m = scales[2b]*code, r = scales[2b+1]*code for the
+ * elements of block b.  All codes and scales are zero before step 1.  After
+ * the update a block's scale is its largest |m| (or r) / 448, and
+ * y = m / scale (or r / scale) becomes floor(|y|/q + u)*q with y's sign,
+ * where q = 2^(max(floor(log2|y|), -6) - 3) is the code step at |y| and u in
+ * [0, 1) has 20 random bits, so a code's expected value is y.  (Rounded to
+ * nearest, an average with beta2 near 1 would never move: a step changes r by
+ * far less than half a code step.)  A positive r keeps at least the smallest code
+ * 2^-9: with r = 0 beside m > 0 the next update would be m / eps.  A block
+ * whose largest value is below 2^-100 holds zeros.  A non-finite gradient
+ * makes its block's scales non-finite, and with them every moment of the
+ * block.
+ *   The random bits of an element come from `seed`, t and its position
+ * counter + i alone: a = mix(floor(position / 16) ^ mix(mix(t) ^ seed)),
+ * b = mix(a + 0x6A09E667), s = a + (position mod 16) * b mod 2^32 (16 elements
+ * draw from one arithmetic progression with a random step, so any two of them
+ * are independent); m takes the bits 31..12 of s, r the bits 31..12 of s
+ * rotated by 16.  mix(x): x ^= x >> 16; x *= 0xBB67AE85; x ^= x >> 15;
+ * x *= 0x9E3779B9; x ^= x >> 16.
+ * Equal inputs give equal bits on every run.
+ */
+typedef struct muon_param {
+  void* param;          /* theta, in/out */
+  const void* grad;
+  void* m;              /* float[numel], or e4m3 codes [numel], in/out, 16-byte aligned */
+  void* v;              /* v: float[numel], or the codes of r [numel], in/out, 16-byte aligned */
+  float* scales;        /* 8-bit: float[2 * ceil(numel / 256)], 8-byte aligned; 32-bit: NULL */
+  int64_t numel;        /* >= 0; theta and grad are contiguous, aligned to their element size */
+  int64_t counter;      /* 8-bit: position of element 0, a multiple of 256 */
+  int64_t first_chunk;  /* chunks of the tensors before it in the list */
+  float weight_decay;
+  float lr_factor;
+  int32_t param_dtype;  /* muon_dtype_t */
+  int32_t grad_dtype;   /* muon_dtype_t */
+  int32_t state_bits;   /* 32 or 8 */
+  int32_t reserved;     /* 0 */
+} muon_param_t;
+
+#define MUON_PARAM_CHUNK 4096
+#define MUON_STATE_BLOCK 256
+
+/* As muon_grad_list, with chunks of MUON_PARAM_CHUNK elements. */
+typedef struct muon_param_list {
+  int64_t count;
+  int64_t total_chunks;
+  const muon_param_t* params;  /* device array [count] */
+  const int32_t* chunk_tensor; /* device array [total_chunks] */
+} muon_param_list_t;
+
+typedef struct muon_adamw_hyper {
+  double lr, beta1, beta2, eps;
+  uint32_t seed;     /* of the 8-bit states' rounding */
+  uint32_t reserved; /* 0 */
+} muon_adamw_hyper_t;
+
+/* step   : t >= 1, and scale = 1 and nothing is skipped, when control is NULL.
+ * control: with a control block (DEVICE memory), t, the gradients' scale, the
+ *          skip and a further factor of lr are read from it when the kernel
+ *          runs, and `step` is not used; a block whose step is below 1 counts
+ *          as t = 1.
+ * lr finite; beta1, beta2 in [0, 1); eps finite >= 0.
+ * No tensor may appear twice or overlap another in the list. */
+muon_status_t muon_adamw_multi(const muon_param_list_t* params, const muon_adamw_hyper_t* hyper, int64_t step,
+                               const muon_step_control_t* control, void* stream);
+
+/* muon_momentum_packed_grouped and muon_apply_grouped under a control block
+ * (DEVICE memory, not NULL): the momentum reads scale * G in place of G, and
+ * with skip set the momentum leaves M and the apply leaves W as they are (the
+ * Newton-Schulz call between them then works on whatever the workspace held,
+ * and nothing takes its result).  Without skip and with scale = 1 the results
+ * are those of the plain calls bit for bit.  lr is multiplied by the block's
+ * lr_factor. */
+muon_status_t muon_momentum_packed_grouped_controlled(int ngroups, const muon_batch_t* grads,
+                                                      const muon_batch_t* moms, float* const* sumsqs, float beta,
+                                                      int nesterov, int32_t compute, void* workspace,
+                                                      size_t ws_bytes, const muon_step_control_t* control,
+                                                      void* stream);
+muon_status_t muon_apply_grouped_controlled(int ngroups, const muon_batch_t* weights, const muon_batch_t* orthos,
+                                            float lr, float weight_decay, int32_t mode, float coeff,
+                                            const muon_step_control_t* control, void* stream);
+
+/*
  * SOAP: Adam run in the eigenbasis of Shampoo's row and column statistics
  * ([GUIDE] section 11.1 "SOAP: Adam in Shampoo's eigenbasis" and 11.2;
  * [ZH] section 6.2), for `count` same-shape

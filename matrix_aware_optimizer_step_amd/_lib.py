@@ -27,13 +27,19 @@ EXPORTED = ("muon_abi_version", "muon_last_error", "muon_status_string", "muon_m
             "muon_momentum", "muon_momentum_grouped_workspace", "muon_momentum_grouped", "muon_momentum_grouped_noalloc",
             "muon_orthogonalize_workspace", "muon_orthogonalize", "muon_orthogonalize_grouped_workspace",
             "muon_orthogonalize_grouped", "muon_packed_grouped_workspace", "muon_momentum_packed_grouped",
-            "muon_orthogonalize_packed_grouped", "muon_orthogonalize_apply_packed_grouped", "muon_apply", "muon_apply_grouped", "muon_adamw", "soap_statistics",
+            "muon_orthogonalize_packed_grouped", "muon_orthogonalize_apply_packed_grouped", "muon_apply", "muon_apply_grouped", "muon_adamw", "muon_grad_norm_workspace",
+            "muon_grad_norm", "muon_adamw_multi", "muon_momentum_packed_grouped_controlled",
+            "muon_apply_grouped_controlled", "soap_statistics",
             "soap_statistics_grouped", "soap_qr_workspace", "soap_qr", "soap_refresh_workspace", "soap_refresh",
             "soap_refresh_grouped_workspace", "soap_refresh_grouped",
             "soap_precondition_workspace", "soap_precondition", "soap_precondition_grouped_workspace",
             "soap_precondition_grouped")
 
 ADAMW_CHUNK = 4096  # MUON_ADAMW_CHUNK
+GRAD_CHUNK = 16384  # MUON_GRAD_CHUNK
+PARAM_CHUNK = 4096  # MUON_PARAM_CHUNK
+STATE_BLOCK = 256   # MUON_STATE_BLOCK
+SKIP_NONFINITE = 1  # MUON_SKIP_NONFINITE
 
 
 class MuonError(RuntimeError):
@@ -53,6 +59,41 @@ class MuonTensorList(ctypes.Structure):
                 ("grads", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p), ("exp_avg_sq", ctypes.c_void_p),
                 ("numels", ctypes.c_void_p), ("chunk_offsets", ctypes.c_void_p), ("param_dtype", ctypes.c_int32),
                 ("grad_dtype", ctypes.c_int32)]
+
+
+class MuonStepControl(ctypes.Structure):
+    """muon_step_control_t, for its offsets: the block itself lies in device memory."""
+    _fields_ = [("norm", ctypes.c_float), ("scale", ctypes.c_float), ("lr_factor", ctypes.c_float),
+                ("skip", ctypes.c_int32), ("step", ctypes.c_int64), ("skipped", ctypes.c_int64),
+                ("reserved", ctypes.c_int32 * 8)]
+
+
+class MuonGrad(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("first_chunk", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class MuonGradList(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int64), ("total_chunks", ctypes.c_int64), ("grads", ctypes.c_void_p),
+                ("chunk_tensor", ctypes.c_void_p)]
+
+
+class MuonParam(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p), ("numel", ctypes.c_int64), ("counter", ctypes.c_int64),
+                ("first_chunk", ctypes.c_int64), ("weight_decay", ctypes.c_float), ("lr_factor", ctypes.c_float),
+                ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("state_bits", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class MuonParamList(ctypes.Structure):
+    _fields_ = [("count", ctypes.c_int64), ("total_chunks", ctypes.c_int64), ("params", ctypes.c_void_p),
+                ("chunk_tensor", ctypes.c_void_p)]
+
+
+class MuonAdamWHyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("seed", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
 
 
 _lib = None
@@ -98,6 +139,13 @@ def load() -> ctypes.CDLL:
         "muon_apply": (ctypes.c_int, [P, P, f32, f32, i32, f32, vp]),
         "muon_apply_grouped": (ctypes.c_int, [ctypes.c_int, P, P, f32, f32, i32, f32, vp]),
         "muon_adamw": (ctypes.c_int, [ctypes.POINTER(MuonTensorList), i64, f32, f32, f32, f32, f32, vp]),
+        "muon_grad_norm_workspace": (sz, [i64]),
+        "muon_grad_norm": (ctypes.c_int, [ctypes.POINTER(MuonGradList), f32, ctypes.c_int, vp, vp, sz, vp]),
+        "muon_adamw_multi": (ctypes.c_int, [ctypes.POINTER(MuonParamList), ctypes.POINTER(MuonAdamWHyper), i64, vp,
+                                            vp]),
+        "muon_momentum_packed_grouped_controlled": (ctypes.c_int, [ctypes.c_int, P, P, ctypes.POINTER(vp), f32,
+                                                                   ctypes.c_int, i32, vp, sz, vp, vp]),
+        "muon_apply_grouped_controlled": (ctypes.c_int, [ctypes.c_int, P, P, f32, f32, i32, f32, vp, vp]),
         "soap_statistics": (ctypes.c_int, [P, P, P, f32, vp]),
         "soap_statistics_grouped": (ctypes.c_int, [ctypes.c_int, P, ctypes.POINTER(P), ctypes.POINTER(P), f32, vp]),
         "soap_qr_workspace": (sz, [i64, i64]),
@@ -221,6 +269,17 @@ def muon_packed_grouped_workspace(counts, rows, cols, compute: int) -> int:
     return load().muon_packed_grouped_workspace(n, arr(*counts), arr(*rows), arr(*cols), compute)
 
 
+def muon_momentum_packed_grouped_controlled(grads, moms, sumsq_ptrs, beta: float, nesterov: bool, compute: int,
+                                            workspace_ptr: int, ws_bytes: int, control_ptr: int, stream: int) -> None:
+    n = len(grads)
+    if len(moms) != n or len(sumsq_ptrs) != n:
+        raise ValueError("per-group lists differ in length")
+    st = load().muon_momentum_packed_grouped_controlled(
+        n, (MuonBatch * n)(*grads), (MuonBatch * n)(*moms), (ctypes.c_void_p * n)(*sumsq_ptrs), beta,
+        int(bool(nesterov)), compute, workspace_ptr, ws_bytes, control_ptr, stream)
+    _check(st, "muon_momentum_packed_grouped_controlled")
+
+
 def muon_momentum_packed_grouped(grads, moms, sumsq_ptrs, beta: float, nesterov: bool, compute: int,
                                  workspace_ptr: int, ws_bytes: int, stream: int) -> None:
     n = len(grads)
@@ -275,6 +334,32 @@ def muon_adamw(tensors: MuonTensorList, step: int, lr: float, beta1: float, beta
                weight_decay: float, stream: int) -> None:
     st = load().muon_adamw(ctypes.byref(tensors), step, lr, beta1, beta2, eps, weight_decay, stream)
     _check(st, "muon_adamw")
+
+
+def muon_apply_grouped_controlled(weights, orthos, lr: float, weight_decay: float, mode: int, coeff: float,
+                                  control_ptr: int, stream: int) -> None:
+    n = len(weights)
+    if len(orthos) != n:
+        raise ValueError("weights and orthos differ in length")
+    st = load().muon_apply_grouped_controlled(n, (MuonBatch * n)(*weights), (MuonBatch * n)(*orthos), lr, weight_decay,
+                                              mode, coeff, control_ptr, stream)
+    _check(st, "muon_apply_grouped_controlled")
+
+
+def muon_grad_norm_workspace(total_chunks: int) -> int:
+    return load().muon_grad_norm_workspace(total_chunks)
+
+
+def muon_grad_norm(grads: MuonGradList, max_norm: float, flags: int, control_ptr: int, workspace_ptr: int,
+                   ws_bytes: int, stream: int) -> None:
+    st = load().muon_grad_norm(ctypes.byref(grads), max_norm, flags, control_ptr, workspace_ptr, ws_bytes, stream)
+    _check(st, "muon_grad_norm")
+
+
+def muon_adamw_multi(params: MuonParamList, hyper: MuonAdamWHyper, step: int, control_ptr: int | None,
+                     stream: int) -> None:
+    st = load().muon_adamw_multi(ctypes.byref(params), ctypes.byref(hyper), step, control_ptr, stream)
+    _check(st, "muon_adamw_multi")
 
 
 def soap_statistics(grad: MuonBatch, L: MuonBatch | None, R: MuonBatch | None, beta_s: float, stream: int) -> None:

@@ -13,19 +13,17 @@
 #include <cstring>
 #include <vector>
 
+#include "abi_common.h"
 #include "muon_internal.h"
 
 namespace muon {
+
 int elementwise_blocks_per_matrix(int64_t rows, int64_t cols);
-}
 
 namespace {
-
-using namespace muon;
-
 thread_local char g_last_error[512] = "";
+}
 
-muon_status_t fail(muon_status_t st, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 muon_status_t fail(muon_status_t st, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -34,6 +32,35 @@ muon_status_t fail(muon_status_t st, const char* fmt, ...) {
   return st;
 }
 
+muon_status_t ok() {
+  g_last_error[0] = '\0';
+  return MUON_OK;
+}
+
+muon_status_t launch_status(hipError_t e, const char* what) {
+  if (e != hipSuccess) return fail(MUON_ERR_LAUNCH, "%s: %s", what, hipGetErrorString(e));
+  return MUON_OK;
+}
+
+// With MUON355_DEBUG_SYNC=1 in the environment every entry point waits for
+// the work it enqueued and reports a failed kernel as MUON_ERR_LAUNCH naming
+// the call.  A debugging aid only: otherwise the library never synchronizes.
+muon_status_t done(hipStream_t s, const char* what) {
+  const char* v = std::getenv("MUON355_DEBUG_SYNC");
+  if (v && v[0] == '1' && v[1] == '\0') {
+    hipError_t e = hipStreamSynchronize(s);
+    if (e == hipSuccess) e = hipGetLastError();
+    if (e != hipSuccess) return fail(MUON_ERR_LAUNCH, "%s (debug sync): %s", what, hipGetErrorString(e));
+  }
+  return ok();
+}
+
+}  // namespace muon
+
+namespace {
+
+using namespace muon;
+
 // Prefix the current error detail with the group it belongs to.
 muon_status_t in_group(muon_status_t st, int g) {
   if (st == MUON_OK) return st;
@@ -41,11 +68,6 @@ muon_status_t in_group(muon_status_t st, int g) {
   snprintf(tmp, sizeof(tmp), "group %d: %.480s", g, g_last_error);
   memcpy(g_last_error, tmp, sizeof(tmp));
   return st;
-}
-
-muon_status_t ok() {
-  g_last_error[0] = '\0';
-  return MUON_OK;
 }
 
 constexpr int64_t kAlign = 256;
@@ -129,24 +151,6 @@ bool vec_ok(const muon_batch_t* b) {
 }
 
 bool finite(float x) { return std::isfinite(x); }
-
-muon_status_t launch_status(hipError_t e, const char* what) {
-  if (e != hipSuccess) return fail(MUON_ERR_LAUNCH, "%s: %s", what, hipGetErrorString(e));
-  return MUON_OK;
-}
-
-// With MUON355_DEBUG_SYNC=1 in the environment every entry point waits for
-// the work it enqueued and reports a failed kernel as MUON_ERR_LAUNCH naming
-// the call.  A debugging aid only: otherwise the library never synchronizes.
-muon_status_t done(hipStream_t s, const char* what) {
-  const char* v = std::getenv("MUON355_DEBUG_SYNC");
-  if (v && v[0] == '1' && v[1] == '\0') {
-    hipError_t e = hipStreamSynchronize(s);
-    if (e == hipSuccess) e = hipGetLastError();
-    if (e != hipSuccess) return fail(MUON_ERR_LAUNCH, "%s (debug sync): %s", what, hipGetErrorString(e));
-  }
-  return ok();
-}
 
 // ------------------------------------------------------------ NS workspace plan
 
@@ -829,9 +833,16 @@ size_t muon_packed_grouped_workspace(int ngroups, const int64_t* counts, const i
   return static_cast<size_t>(plan.bytes);
 }
 
-muon_status_t muon_momentum_packed_grouped(int ngroups, const muon_batch_t* grads, const muon_batch_t* moms,
-                                           float* const* sumsqs, float beta, int nesterov, int32_t compute,
-                                           void* workspace, size_t ws_bytes, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// muon_momentum_packed_grouped, and with `control` its form under a control
+// block.
+muon_status_t momentum_packed_grouped(int ngroups, const muon_batch_t* grads, const muon_batch_t* moms,
+                                      float* const* sumsqs, float beta, int nesterov, int32_t compute,
+                                      void* workspace, size_t ws_bytes, const muon_step_control_t* control,
+                                      void* stream, const char* name) {
   if (ngroups < 1 || ngroups > kMaxGroups)
     return fail(MUON_ERR_INVALID_VALUE, "ngroups %d outside [1, %d]", ngroups, kMaxGroups);
   if (!grads || !moms || !sumsqs) return fail(MUON_ERR_INVALID_VALUE, "grads, moms and sumsqs must not be NULL");
@@ -890,6 +901,7 @@ muon_status_t muon_momentum_packed_grouped(int ngroups, const muon_batch_t* grad
     a.lo_mat = mn;
     a.LoE = compute == MUON_BF16 ? reinterpret_cast<uint8_t*>(ws + p.xloe) : nullptr;
     a.loe_mat = mn / kLoExpPerCodes;
+    a.control = reinterpret_cast<const StepControl*>(control);
     P.first[g + 1] = P.first[g] + counts[g] * p.pack_tiles;
     F.first[g + 1] = F.first[g] + counts[g];
     F.per[g] = p.pack_tiles;
@@ -903,7 +915,35 @@ muon_status_t muon_momentum_packed_grouped(int ngroups, const muon_batch_t* grad
   if (e != hipSuccess) return launch_status(e, "momentum pack");
   e = launch_sumsq_finalize_grouped(F, s);
   if (e != hipSuccess) return launch_status(e, "sumsq finalize");
-  return done(s, "muon_momentum_packed_grouped");
+  return done(s, name);
+}
+
+muon_status_t check_control(const muon_step_control_t* control) {
+  if (!control || reinterpret_cast<uintptr_t>(control) % 16 != 0)
+    return fail(MUON_ERR_INVALID_VALUE, "control must be a 16-byte aligned device address");
+  return MUON_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status_t muon_momentum_packed_grouped(int ngroups, const muon_batch_t* grads, const muon_batch_t* moms,
+                                           float* const* sumsqs, float beta, int nesterov, int32_t compute,
+                                           void* workspace, size_t ws_bytes, void* stream) {
+  return momentum_packed_grouped(ngroups, grads, moms, sumsqs, beta, nesterov, compute, workspace, ws_bytes, nullptr,
+                                 stream, "muon_momentum_packed_grouped");
+}
+
+muon_status_t muon_momentum_packed_grouped_controlled(int ngroups, const muon_batch_t* grads,
+                                                      const muon_batch_t* moms, float* const* sumsqs, float beta,
+                                                      int nesterov, int32_t compute, void* workspace,
+                                                      size_t ws_bytes, const muon_step_control_t* control,
+                                                      void* stream) {
+  const muon_status_t st = check_control(control);
+  if (st != MUON_OK) return st;
+  return momentum_packed_grouped(ngroups, grads, moms, sumsqs, beta, nesterov, compute, workspace, ws_bytes, control,
+                                 stream, "muon_momentum_packed_grouped_controlled");
 }
 
 muon_status_t muon_orthogonalize_packed_grouped(int ngroups, const float* const* sumsqs, const muon_batch_t* outs,
@@ -943,8 +983,14 @@ muon_status_t muon_apply(const muon_batch_t* weight, const muon_batch_t* ortho, 
   return done(static_cast<hipStream_t>(stream), "muon_apply");
 }
 
-muon_status_t muon_apply_grouped(int ngroups, const muon_batch_t* weights, const muon_batch_t* orthos, float lr,
-                                 float weight_decay, int32_t mode, float coeff, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// muon_apply_grouped, and with `control` its form under a control block.
+muon_status_t apply_grouped(int ngroups, const muon_batch_t* weights, const muon_batch_t* orthos, float lr,
+                            float weight_decay, int32_t mode, float coeff, const muon_step_control_t* control,
+                            void* stream, const char* name) {
   if (ngroups < 1 || ngroups > kMaxGroups)
     return fail(MUON_ERR_INVALID_VALUE, "ngroups %d outside [1, %d]", ngroups, kMaxGroups);
   if (!weights || !orthos) return fail(MUON_ERR_INVALID_VALUE, "weights and orthos must not be NULL");
@@ -955,6 +1001,8 @@ muon_status_t muon_apply_grouped(int ngroups, const muon_batch_t* weights, const
     bool vec;
     const muon_status_t st = prepare_apply(&weights[g], &orthos[g], lr, weight_decay, mode, coeff, &G.g[g], &vec);
     if (st != MUON_OK) return in_group(st, g);
+    G.g[g].lrwd = static_cast<float>(static_cast<double>(lr) * weight_decay);
+    G.g[g].control = reinterpret_cast<const StepControl*>(control);
     G.vec[g] = vec;
     G.blocks_per_mat[g] = elementwise_blocks_per_matrix(weights[g].rows, weights[g].cols);
     G.first[g + 1] = G.first[g] + weights[g].count * G.blocks_per_mat[g];
@@ -963,7 +1011,26 @@ muon_status_t muon_apply_grouped(int ngroups, const muon_batch_t* weights, const
     return fail(MUON_ERR_UNSUPPORTED, "%lld workgroups exceed one launch", (long long)G.first[ngroups]);
   hipError_t e = launch_apply_grouped(G, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return launch_status(e, "apply");
-  return done(static_cast<hipStream_t>(stream), "muon_apply_grouped");
+  return done(static_cast<hipStream_t>(stream), name);
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status_t muon_apply_grouped(int ngroups, const muon_batch_t* weights, const muon_batch_t* orthos, float lr,
+                                 float weight_decay, int32_t mode, float coeff, void* stream) {
+  return apply_grouped(ngroups, weights, orthos, lr, weight_decay, mode, coeff, nullptr, stream,
+                       "muon_apply_grouped");
+}
+
+muon_status_t muon_apply_grouped_controlled(int ngroups, const muon_batch_t* weights, const muon_batch_t* orthos,
+                                            float lr, float weight_decay, int32_t mode, float coeff,
+                                            const muon_step_control_t* control, void* stream) {
+  const muon_status_t st = check_control(control);
+  if (st != MUON_OK) return st;
+  return apply_grouped(ngroups, weights, orthos, lr, weight_decay, mode, coeff, control, stream,
+                       "muon_apply_grouped_controlled");
 }
 
 }  // extern "C"

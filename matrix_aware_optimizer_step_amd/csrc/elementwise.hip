@@ -304,6 +304,15 @@ __device__ __forceinline__ void apply_block(const ApplyArgs& a, int64_t mat, uin
   const int os = a.O.dtype ? 2 : 4;
   const uint32_t total = static_cast<uint32_t>(a.rows) * static_cast<uint32_t>(a.cols);
   const uint32_t base = blk * kElemsPerBlock;
+  float decay = a.decay, step = a.step;
+  if (a.control != nullptr) {
+    if (a.control->skip) return;
+    const float f = a.control->lr_factor;
+    if (f != 1.0f) {  // a factor of 1 leaves the host's rounding of 1 - lr*wd
+      decay = 1.0f - f * a.lrwd;
+      step *= f;
+    }
+  }
   if (VEC) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -316,7 +325,7 @@ __device__ __forceinline__ void apply_block(const ApplyArgs& a, int64_t mat, uin
         load8(wp, a.W.dtype, wv);
         load8(o + (r * a.O.ld + c) * os, a.O.dtype, ov);
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) wv[k] = a.decay * wv[k] - a.step * ov[k];
+        for (int k = 0; k < kVec; ++k) wv[k] = decay * wv[k] - step * ov[k];
         store8(wp, a.W.dtype, wv);
       }
     }
@@ -327,7 +336,7 @@ __device__ __forceinline__ void apply_block(const ApplyArgs& a, int64_t mat, uin
         const uint32_t r = fdiv(a.cdiv, e);
         const uint32_t c = e - r * a.cols;
         char* wp = w + (r * a.W.ld + c) * ws;
-        const float v = a.decay * load1(wp, a.W.dtype) - a.step * load1(o + (r * a.O.ld + c) * os, a.O.dtype);
+        const float v = decay * load1(wp, a.W.dtype) - step * load1(o + (r * a.O.ld + c) * os, a.O.dtype);
         store1(wp, a.W.dtype, v);
       }
     }
@@ -467,6 +476,11 @@ __global__ __launch_bounds__(kThreads) void momentum_pack_kernel(const MomentumP
   const int gsz = a.G.dtype ? 2 : 4;
   const float beta = a.beta;
   const float omb = 1.0f - a.beta;
+  float gs = 1.0f;  // a factor of 1 is exact: the plain call's bits
+  if (a.control != nullptr) {
+    if (a.control->skip) return;
+    gs = a.control->scale;
+  }
   const int q = threadIdx.x & 15;   // 4-element piece of a 64-element row
   const int rq = threadIdx.x >> 4;  // 0..15
   const int esz = a.compute ? 2 : 4;
@@ -487,6 +501,7 @@ __global__ __launch_bounds__(kThreads) void momentum_pack_kernel(const MomentumP
         load4(reinterpret_cast<const char*>(mp), 0, mv);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
+          gv[e] *= gs;
           mv[e] = beta * mv[e] + omb * gv[e];
           nv[e] = a.nesterov ? omb * gv[e] + beta * mv[e] : mv[e];
         }
@@ -495,7 +510,7 @@ __global__ __launch_bounds__(kThreads) void momentum_pack_kernel(const MomentumP
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           if (c + e < a.cols) {
-            const float gv = load1(gp + e * gsz, a.G.dtype);
+            const float gv = gs * load1(gp + e * gsz, a.G.dtype);
             const float mv = beta * mp[e] + omb * gv;
             nv[e] = a.nesterov ? omb * gv + beta * mv : mv;
             mp[e] = mv;

@@ -20,6 +20,14 @@ struct MatBatch {
   int32_t pad_;
 };
 
+// As muon_step_control_t (the C-ABI layer checks that they agree).
+struct StepControl {
+  float norm, scale, lr_factor;
+  int32_t skip;
+  int64_t step, skipped;
+  int32_t reserved[8];
+};
+
 // Fast unsigned 32-bit division by a runtime-constant divisor
 // (round-up multiply-high method of Granlund and Montgomery).
 struct FastDiv {
@@ -203,6 +211,8 @@ struct ApplyArgs {
   FastDiv cdiv;
   float decay;           // 1 - lr*wd
   float step;            // lr * s
+  float lrwd;            // lr * wd, for a control block's lr_factor
+  const StepControl* control;  // device, or null: its skip and lr_factor apply
 };
 hipError_t launch_apply(const ApplyArgs& a, int64_t count, bool vec,
                         hipStream_t stream);
@@ -290,6 +300,7 @@ struct MomentumPackArgs {
   char* T; int64_t t_mat;
   int8_t* Lo; int64_t lo_mat;
   uint8_t* LoE; int64_t loe_mat;
+  const StepControl* control;  // device, or null: G is read times its scale; with skip nothing is written
 };
 struct MomentumPackGroups {
   int32_t ngroups;
@@ -328,6 +339,59 @@ struct AdamWArgs {
   float lr, decay;                // decay = 1 - lr*wd
 };
 hipError_t launch_adamw(const AdamWArgs& a, int64_t total_chunks, hipStream_t stream);
+
+// ------------------------------------------------------------ step control, many-tensor AdamW
+
+// GradTensor and ParamTensor are muon_grad_t and muon_param_t (the C-ABI
+// layer checks that they agree).
+struct GradTensor {
+  const char* data;
+  int64_t numel, first_chunk;
+  int32_t dtype, reserved;
+};
+
+constexpr int64_t kGradChunk = 16384;  // MUON_GRAD_CHUNK
+constexpr int kGradMaxBlocks = 2048;   // workgroups of the norm, one partial sum each
+
+struct GradNormArgs {
+  int64_t count, total_chunks;
+  const GradTensor* grads;        // device [count]
+  const int32_t* chunk_tensor;    // device [total_chunks]
+  double* partials;               // device [blocks]
+  int32_t blocks;
+  int32_t skip_nonfinite;
+  float max_norm;
+  int32_t pad_;
+  StepControl* control;           // device
+};
+hipError_t launch_grad_norm(const GradNormArgs& a, hipStream_t stream);
+
+struct ParamTensor {
+  char* param;
+  const char* grad;
+  char* m;
+  char* v;
+  float* scales;
+  int64_t numel, counter, first_chunk;
+  float weight_decay, lr_factor;
+  int32_t param_dtype, grad_dtype, state_bits, reserved;
+};
+
+constexpr int64_t kParamChunk = 4096;  // elements per workgroup; MUON_PARAM_CHUNK
+constexpr int kStateBlock = 256;       // elements per scale; MUON_STATE_BLOCK
+
+struct AdamWMultiArgs {
+  int64_t count;
+  const ParamTensor* params;      // device [count]
+  const int32_t* chunk_tensor;    // device [total_chunks]
+  const StepControl* control;     // device, or null
+  double lr, log_b1, log_b2;      // log_b1, log_b2: natural logarithms of the betas
+  int64_t step;                   // t when control is null
+  float b1, omb1, b2, omb2, eps;  // omb = 1 - beta, rounded once
+  float c1, c2;                   // 1/(1-beta1^t), 1/(1-beta2^t) when control is null
+  uint32_t seed;
+};
+hipError_t launch_adamw_multi(const AdamWMultiArgs& a, int64_t total_chunks, hipStream_t stream);
 
 // ------------------------------------------------------------ SOAP
 

@@ -9,6 +9,7 @@ steps 1-4).  It does no arithmetic on the tensors.
 
 from __future__ import annotations
 
+import math
 from dataclasses import dataclass, field
 
 import torch
@@ -208,14 +209,22 @@ class MuonStep:
     applied by the last Newton-Schulz step
     (muon_orthogonalize_apply_packed_grouped): O is never stored, and
     ``ortho_buffers`` raises.
+
+    ``control`` (a ``StepControl``): the gradients are read times its clip
+    factor, its skip flag leaves momentum and weights unchanged, and its
+    ``lr_factor`` multiplies ``lr``, all read on the device when the step runs.
+    It needs the packed path with the update as its own kernel.
     """
 
     def __init__(self, groups, *, compute: int = L.MUON_BF16, beta: float = 0.95, nesterov: bool = True,
                  steps: int = 5, coeffs=QUINTIC, eps: float = EPS, lr: float = 3e-4,
                  weight_decay: float = 0.1, mode: int = L.MUON_SCALE_MATCH_RMS, coeff: float = 0.2,
-                 packed: bool = True, fused_apply: bool = False):
+                 packed: bool = True, fused_apply: bool = False, control=None):
         if not groups:
             raise ValueError("no parameter groups")
+        if control is not None and (not packed or fused_apply or steps < 1):
+            raise ValueError("a control block needs packed=True, fused_apply=False and steps >= 1")
+        self.control = control
         self.compute, self.beta, self.nesterov = compute, beta, nesterov
         self.steps, self.coeffs, self.eps = steps, coeffs, eps
         self.lr, self.weight_decay, self.mode, self.coeff = lr, weight_decay, mode, coeff
@@ -316,6 +325,8 @@ class MuonStep:
         st = stream if stream is not None else torch.cuda.current_stream()
         s = _stream(st)
         packed = self.packed and self.steps >= 1
+        if self.control is not None and not packed:
+            raise ValueError("a control block needs steps >= 1")
         if not packed:
             self._unpacked_buffers()
         if not (packed and self.fused_apply):
@@ -327,8 +338,12 @@ class MuonStep:
             sums = [self.ss[i].data_ptr() for i in ch]
             if packed:
                 ws = self.pws[k]
-                L.muon_momentum_packed_grouped([self.g[i].desc for i in ch], [self.m[i].desc for i in ch], sums,
-                                               self.beta, self.nesterov, self.compute, ws.data_ptr(), ws.numel(), s)
+                args = ([self.g[i].desc for i in ch], [self.m[i].desc for i in ch], sums, self.beta, self.nesterov,
+                        self.compute, ws.data_ptr(), ws.numel())
+                if self.control is None:
+                    L.muon_momentum_packed_grouped(*args, s)
+                else:
+                    L.muon_momentum_packed_grouped_controlled(*args, self.control.data_ptr(), s)
             else:
                 ws = self.mws[k]
                 L.muon_momentum_grouped([self.g[i].desc for i in ch], [self.m[i].desc for i in ch],
@@ -355,8 +370,12 @@ class MuonStep:
         if events is not None:
             events[2].record(st)
         for ch in (self.chunks if not (packed and self.fused_apply) else []):
-            L.muon_apply_grouped([self.w[i].desc for i in ch], [self.o[i].desc for i in ch], self.lr,
-                                 self.weight_decay, self.mode, self.coeff, s)
+            args = ([self.w[i].desc for i in ch], [self.o[i].desc for i in ch], self.lr, self.weight_decay, self.mode,
+                    self.coeff)
+            if self.control is None:
+                L.muon_apply_grouped(*args, s)
+            else:
+                L.muon_apply_grouped_controlled(*args, self.control.data_ptr(), s)
         if events is not None:
             events[3].record(st)
 
@@ -484,11 +503,26 @@ class OptimizerStep:
     for tensors of two or more dimensions (embeddings, head) and an undecayed
     one for norms and biases, each split by dtype.  ``routing`` records the
     name of every parameter and where it went.
+
+    ``max_grad_norm``: every gradient is clipped by their global norm, on the
+    device (infinity: the norm is taken but clips nothing).  ``skip_nonfinite``:
+    a step whose norm is not finite changes nothing.  Either makes a
+    ``GradClip`` that runs first, and the updates read its ``control`` block,
+    whose step count then is the AdamW step number: such a step can be captured
+    in a graph and replayed.  ``adam_state_bits=8`` keeps the AdamW moments of
+    the decayed tensors in 8 bits (norms and biases stay in 32).  With any of
+    these the AdamW tensors are one ``AdamWMulti``, one launch for all types.
     """
 
     def __init__(self, named_params, *, compute: int = L.MUON_BF16, muon_lr: float = 3e-4,
                  muon_weight_decay: float = 0.1, adam_lr: float = 3e-4, adam_betas=(0.9, 0.999),
-                 adam_eps: float = 1e-8, adam_weight_decay: float = 0.1, is_muon=is_muon_param):
+                 adam_eps: float = 1e-8, adam_weight_decay: float = 0.1, is_muon=is_muon_param,
+                 max_grad_norm: float | None = None, skip_nonfinite: bool = False, adam_state_bits: int = 32,
+                 seed: int = 0):
+        from .multi import AdamWMulti, GradClip  # multi imports this module's helpers
+        if adam_state_bits not in (8, 32):
+            raise ValueError("adam_state_bits must be 8 or 32")
+        named_params = list(named_params)
         shapes = {}
         adam = {}
         self.routing = {}
@@ -502,15 +536,29 @@ class OptimizerStep:
                 decay = p.dim() >= 2
                 adam.setdefault((decay, p.dtype, g.dtype), []).append((p, g))
                 self.routing[name] = "adamw" if decay else "adamw_no_decay"
-        self.muon = None
+        self.clip = self.muon = control = None
+        if max_grad_norm is not None or skip_nonfinite:
+            self.clip = GradClip([g for _, _, g in named_params if g is not None],
+                                 max_norm=math.inf if max_grad_norm is None else max_grad_norm,
+                                 skip_nonfinite=skip_nonfinite)
+            control = self.clip.control
         if shapes:
             groups = [([p for p, _ in v], [g for _, g in v]) for v in shapes.values()]
-            self.muon = MuonStep(groups, compute=compute, lr=muon_lr, weight_decay=muon_weight_decay)
+            self.muon = MuonStep(groups, compute=compute, lr=muon_lr, weight_decay=muon_weight_decay, control=control)
+        if control is not None or adam_state_bits == 8:
+            flat = [(p, g, decay) for (decay, _, _), v in adam.items() for p, g in v]
+            self.adamw = [AdamWMulti([p for p, _, _ in flat], [g for _, g, _ in flat], lr=adam_lr, betas=adam_betas,
+                                     eps=adam_eps, weight_decay=[adam_weight_decay if d else 0.0 for _, _, d in flat],
+                                     state_bits=[adam_state_bits if d else 32 for _, _, d in flat], seed=seed,
+                                     control=control)] if flat else []
+            return
         self.adamw = [AdamW([p for p, _ in v], [g for _, g in v], lr=adam_lr, betas=adam_betas, eps=adam_eps,
                             weight_decay=adam_weight_decay if decay else 0.0)
                       for (decay, _, _), v in adam.items()]
 
     def step(self, stream=None) -> None:
+        if self.clip is not None:
+            self.clip.step(stream=stream)
         if self.muon is not None:
             self.muon.step(stream=stream)
         for group in self.adamw:
