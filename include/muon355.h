@@ -384,6 +384,7 @@ muon_status_t muon_adamw(const muon_tensor_list_t* tensors, int64_t step, float 
  * `control` argument read it when they RUN, not when they are enqueued.  A
  * captured step that replays therefore clips by its own gradients' norm and
  * counts its own steps.  Before the first use: lr_factor = 1, the rest 0.
+ * Calls that share a block must be ordered, as calls that share a workspace.
  */
 typedef struct muon_step_control {
   float norm;          /* global 2-norm of the gradients */
@@ -392,7 +393,7 @@ typedef struct muon_step_control {
   int32_t skip;        /* nonzero: this step changes no parameter and no state */
   int64_t step;        /* t: steps begun and not skipped */
   int64_t skipped;     /* steps skipped */
-  int32_t reserved[8]; /* zero */
+  int32_t reserved[8]; /* the library's; back at zero after every call */
 } muon_step_control_t;
 
 /* A gradient of a muon_grad_list: numel elements in one contiguous run,
@@ -451,7 +452,7 @@ muon_status_t muon_grad_norm(const muon_grad_list_t* grads, float max_norm, int 
  *   theta <- (1 - l*weight_decay)*theta - l*(m / (1-beta1^t)) / (sqrt(v / (1-beta2^t)) + eps)
  * with l = lr * lr_factor of the tensor.  A BF16 theta is rounded once to nearest even.
  *
- * 32-bit state: m and v are float[numel], zero before step 1.
+ * 32-bit state: m and v are floats, zero before step 1.
  *
  * 8-bit state: m and r = sqrt(v) are e4m3 codes (OCP: 4 exponent and 3
  * mantissa bits, largest value 448), one scale each for every 256
@@ -475,12 +476,17 @@ muon_status_t muon_grad_norm(const muon_grad_list_t* grads, float max_norm, int 
  * rotated by 16.  mix(x): x ^= x >> 16; x *= 0xBB67AE85; x ^= x >> 15;
  * x *= 0x9E3779B9; x ^= x >> 16.
  * Equal inputs give equal bits on every run.
+ *
+ * State arrays hold numel rounded up to a multiple of MUON_STATE_BLOCK
+ * elements; those past numel are zero before step 1 and stay zero (for finite
+ * gradients).  theta and the gradients end at numel: nothing past it is read
+ * or written.
  */
 typedef struct muon_param {
   void* param;          /* theta, in/out */
   const void* grad;
-  void* m;              /* float[numel], or e4m3 codes [numel], in/out, 16-byte aligned */
-  void* v;              /* v: float[numel], or the codes of r [numel], in/out, 16-byte aligned */
+  void* m;              /* m as float, or its e4m3 codes, in/out, 16-byte aligned */
+  void* v;              /* v as float, or the codes of r, in/out, 16-byte aligned */
   float* scales;        /* 8-bit: float[2 * ceil(numel / 256)], 8-byte aligned; 32-bit: NULL */
   int64_t numel;        /* >= 0; theta and grad are contiguous, aligned to their element size */
   int64_t counter;      /* 8-bit: position of element 0, a multiple of 256 */

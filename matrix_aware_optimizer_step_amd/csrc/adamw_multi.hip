@@ -8,8 +8,7 @@
 // A workgroup owns one chunk of kParamChunk elements of one tensor; the
 // chunk table names the tensor.  The 8-bit state keeps m and r = sqrt(v) as
 // e4m3 codes with a scale per 256 elements (include/muon355.h gives the
-// format): a thread holds 16 consecutive elements, so a block is 16 lanes of
-// one wave and its maximum four lane exchanges.
+// format).
 
 #include "muon_internal.h"
 
@@ -18,90 +17,162 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPer = kParamChunk / kThreads;  // 16 elements per thread
+constexpr int kPiece = 8;                     // contiguous elements of a thread
 static_assert(kStateBlock == 16 * kPer, "a block of the 8-bit state is 16 lanes");
 
 constexpr float kTop = 448.0f;                      // largest e4m3 value
 constexpr float kLeast = 0.001953125f;              // 2^-9, smallest e4m3 value above zero
 constexpr float kTiny = 7.888609052210118e-31f;     // 2^-100
 
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) { return __builtin_bit_cast(float, w & 0xffff0000u); }
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-// two values rounded to nearest even, the first in the low half
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){lo, hi}, bf16x2));
-}
 
-// 8 values starting at element e of p, all of them inside (vec) or the first n.
+// A piece of a tensor: 8 values of bf16 or fp32 as they lie in memory.  Whole
+// pieces move 16 bytes per access whatever the tensor's alignment: the
+// hardware takes vector accesses at any address, so views that start anywhere
+// in a flat buffer need no path of their own.
 template <bool BF16>
-__device__ __forceinline__ void load8(const char* p, bool vec, int n, float* x) {
-  if (vec) {
-    if (BF16) {
-      const uint4 u = *reinterpret_cast<const uint4*>(p);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        x[2 * k] = bf16_lo(w[k]);
-        x[2 * k + 1] = bf16_hi(w[k]);
-      }
-    } else {
-      const float4 a = reinterpret_cast<const float4*>(p)[0];
-      const float4 b = reinterpret_cast<const float4*>(p)[1];
-      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-      x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      x[k] = 0.0f;
-      if (k < n)
-        x[k] = BF16 ? bf16_lo(reinterpret_cast<const uint16_t*>(p)[k]) : reinterpret_cast<const float*>(p)[k];
-    }
-  }
-}
+struct Piece {
+  uint32_t w[BF16 ? kPiece / 2 : kPiece];
 
-template <bool BF16>
-__device__ __forceinline__ void store8(char* p, bool vec, int n, const float* x) {
-  if (vec) {
-    if (BF16) {
-      uint4 u;
-      u.x = bf16_pair(x[0], x[1]);
-      u.y = bf16_pair(x[2], x[3]);
-      u.z = bf16_pair(x[4], x[5]);
-      u.w = bf16_pair(x[6], x[7]);
-      *reinterpret_cast<uint4*>(p) = u;
-    } else {
-      reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-    }
-  } else {
+  __device__ __forceinline__ void load(const char* p) { __builtin_memcpy(w, p, sizeof(w)); }
+  // the first n >= 1 of them, then zeros (element 0 is read in their place and
+  // dropped: no branch between the loads)
+  __device__ __forceinline__ void load_first(const char* p, int n) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (k < n) {
-        if (BF16) {
-          reinterpret_cast<uint16_t*>(p)[k] = static_cast<uint16_t>(bf16_pair(x[k], 0.0f));
-        } else {
-          reinterpret_cast<float*>(p)[k] = x[k];
-        }
+    for (int k = 0; k < kPiece; ++k) {
+      const int i = k < n ? k : 0;
+      if (BF16) {
+        const uint32_t h = reinterpret_cast<const uint16_t*>(p)[i], x = k < n ? h : 0;
+        w[k / 2] = k % 2 ? w[k / 2] | (x << 16) : x;
+      } else {
+        const uint32_t x = reinterpret_cast<const uint32_t*>(p)[i];
+        w[k] = k < n ? x : 0;
       }
     }
   }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (uint32_t& x : w) x = 0;
+  }
+  __device__ __forceinline__ float get(int k) const {
+    if (!BF16) return __builtin_bit_cast(float, w[k]);
+    return __builtin_bit_cast(float, k % 2 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
+  }
+  // bf16 rounds to nearest even
+  __device__ __forceinline__ void set(const float* x) {
+#pragma unroll
+    for (int k = 0; k < kPiece; k += 2) {
+      if (BF16) {
+        w[k / 2] = __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){x[k], x[k + 1]}, bf16x2));
+      } else {
+        w[k] = __builtin_bit_cast(uint32_t, x[k]);
+        w[k + 1] = __builtin_bit_cast(uint32_t, x[k + 1]);
+      }
+    }
+  }
+  __device__ __forceinline__ void store(char* p) const { __builtin_memcpy(p, w, sizeof(w)); }
+  __device__ __forceinline__ void store_first(char* p, int n) const {
+#pragma unroll
+    for (int k = 0; k < kPiece; ++k) {
+      if (k >= n) continue;
+      if (BF16) {
+        reinterpret_cast<uint16_t*>(p)[k] = static_cast<uint16_t>(w[k / 2] >> (k % 2 * 16));
+      } else {
+        reinterpret_cast<uint32_t*>(p)[k] = w[k];
+      }
+    }
+  }
+};
+
+// The same at element e of a tensor's chunk of len elements; `full`: the
+// chunk is whole (uniform).
+template <bool BF16>
+__device__ __forceinline__ void load(Piece<BF16>& x, const char* base, int e, int len, bool full) {
+  const char* p = base + e * (BF16 ? 2 : 4);
+  if (full || len - e >= kPiece) {
+    x.load(p);
+  } else if (len - e > 0) {
+    x.load_first(p, len - e);
+  } else {
+    x.clear();
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ void store(const Piece<BF16>& x, char* base, int e, int len, bool full) {
+  char* p = base + e * (BF16 ? 2 : 4);
+  if (full || len - e >= kPiece) {
+    x.store(p);
+  } else if (len - e > 0) {
+    x.store_first(p, len - e);
+  }
 }
 
-// What one step does to one element, after g has been scaled.
+// What one step does to one element.  Every product and sum of the moments is
+// rounded by itself (no contraction): both moments then round as the formula
+// is written, whichever way the compiler schedules it, and it costs nothing
+// beside the memory traffic (1.90 ms either way for 1.05e9 elements with
+// 8-bit states).
 struct Rule {
   float gs, b1, omb1, b2, omb2, sc2, eps, decay, lr;  // sc2 = sqrt(c2); lr includes c1
 
-  // m and v in, m, v and r = sqrt(v) out, theta updated
-  __device__ __forceinline__ void operator()(float& p, float g, float& m, float& v, float& r) const {
-    g *= gs;
-    m = b1 * m + omb1 * g;
-    v = b2 * v + omb2 * g * g;
-    r = sqrtf(v);
-    p = decay * p - lr * m / (r * sc2 + eps);
+  __device__ __forceinline__ float first(float m, float g) const {
+    return __fadd_rn(__fmul_rn(b1, m), __fmul_rn(omb1, g));
+  }
+  __device__ __forceinline__ float second(float v, float g) const {
+    return __fadd_rn(__fmul_rn(b2, v), __fmul_rn(omb2, __fmul_rn(g, g)));
+  }
+  // v_rcp_f32 (off by 1.5 ulp, a 1e-7 of the step): the IEEE division took 7 %
+  // of the time with 8-bit states
+  __device__ __forceinline__ float theta(float p, float m, float r) const {
+    return decay * p - lr * m * __builtin_amdgcn_rcpf(r * sc2 + eps);
   }
 };
+
+// 32-bit moments: two pieces per thread, 256 pieces apart, so that a wave's
+// access covers one contiguous run.  The state is padded, so only the
+// parameter and the gradient end inside a piece.
+template <bool PB, bool GB>
+__device__ __forceinline__ void chunk32(const ParamTensor& t, const Rule& rule, int64_t start, int len, bool full) {
+  constexpr int N = kPer / kPiece;
+  char* P = t.param + start * (PB ? 2 : 4);
+  const char* G = t.grad + start * (GB ? 2 : 4);
+  char* M = t.m + start * 4;
+  char* V = t.v + start * 4;
+  Piece<PB> p[N];
+  Piece<GB> g[N];
+  Piece<false> m[N], v[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const int e = (q * kThreads + threadIdx.x) * kPiece;
+    load(p[q], P, e, len, full);
+    load(g[q], G, e, len, full);
+    if (full || e < len) {
+      m[q].load(M + e * 4);
+      v[q].load(V + e * 4);
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const int e = (q * kThreads + threadIdx.x) * kPiece;
+    float np[kPiece], nm[kPiece], nv[kPiece];
+#pragma unroll
+    for (int k = 0; k < kPiece; ++k) {
+      const float x = rule.gs * g[q].get(k);
+      nm[k] = rule.first(m[q].get(k), x);
+      nv[k] = rule.second(v[q].get(k), x);
+      np[k] = rule.theta(p[q].get(k), nm[k], sqrtf(nv[k]));
+    }
+    p[q].set(np);
+    m[q].set(nm);
+    v[q].set(nv);
+    store(p[q], P, e, len, full);
+    if (full || e < len) {
+      m[q].store(M + e * 4);
+      v[q].store(V + e * 4);
+    }
+  }
+}
 
 __device__ __forceinline__ uint32_t mix(uint32_t x) {
   x ^= x >> 16;
@@ -116,67 +187,25 @@ __device__ __forceinline__ float max_abs(float a, float b) {
   return __builtin_elementwise_maximum(__builtin_fabsf(a), __builtin_fabsf(b));
 }
 
-template <bool PB, bool GB>
-__device__ __forceinline__ void chunk32(const ParamTensor& t, const Rule& rule, int64_t start, int len, bool aligned) {
-  char* P = t.param + start * (PB ? 2 : 4);
-  const char* G = t.grad + start * (GB ? 2 : 4);
-  char* M = t.m + start * 4;
-  char* V = t.v + start * 4;
-#pragma unroll
-  for (int u = 0; u < kPer / 8; ++u) {
-    const int e = (u * kThreads + threadIdx.x) * 8;
-    const int n = len - e;
-    if (n <= 0) continue;
-    const bool full = n >= 8, vec = full && aligned;
-    float p[8], g[8], m[8], v[8];
-    load8<PB>(P + e * (PB ? 2 : 4), vec, n, p);
-    load8<GB>(G + e * (GB ? 2 : 4), vec, n, g);
-    load8<false>(M + e * 4, full, n, m);
-    load8<false>(V + e * 4, full, n, v);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float r;
-      rule(p[k], g[k], m[k], v[k], r);
-    }
-    store8<PB>(P + e * (PB ? 2 : 4), vec, n, p);
-    store8<false>(M + e * 4, full, n, m);
-    store8<false>(V + e * 4, full, n, v);
-  }
+// The largest of x >= 0 over a row of 16 lanes, in every one of them, by
+// rotations inside the row.  Such floats order as their bits, a NaN above all.
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_rotated(uint32_t x) {
+  const uint32_t y = __builtin_amdgcn_update_dpp(x, x, CTRL, 0xf, 0xf, false);
+  return x > y ? x : y;
+}
+__device__ __forceinline__ float row_max(float x) {
+  uint32_t u = __builtin_bit_cast(uint32_t, x);
+  u = max_rotated<0x128>(u);  // by 8, 4, 2 and 1 lanes
+  u = max_rotated<0x124>(u);
+  u = max_rotated<0x122>(u);
+  u = max_rotated<0x121>(u);
+  return __builtin_bit_cast(float, u);
 }
 
-// 16 codes of one lane (four words), the first n inside the tensor.
-__device__ __forceinline__ void load_codes(const char* p, int n, uint32_t* w) {
-  if (n >= 16) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = 0;
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (k < n) w[k / 4] |= static_cast<uint32_t>(reinterpret_cast<const uint8_t*>(p)[k]) << (8 * (k & 3));
-  }
-}
-
-__device__ __forceinline__ void store_codes(char* p, int n, const uint32_t* w) {
-  if (n >= 16) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (k < n) reinterpret_cast<uint8_t*>(p)[k] = static_cast<uint8_t>(w[k / 4] >> (8 * (k & 3)));
-  }
-}
-
-__device__ __forceinline__ void decode4(uint32_t w, float s, float* x) {
-  x[0] = s * __builtin_amdgcn_cvt_f32_fp8(w, 0);
-  x[1] = s * __builtin_amdgcn_cvt_f32_fp8(w, 1);
-  x[2] = s * __builtin_amdgcn_cvt_f32_fp8(w, 2);
-  x[3] = s * __builtin_amdgcn_cvt_f32_fp8(w, 3);
-}
-
-// v_cvt_sr_fp8_f32 is floor(|y|/q + (seed >> 12) / 2^20) * q with y's sign,
-// for normal and subnormal codes (checked on the hardware over the range).
+// Four values to codes.  v_cvt_sr_fp8_f32 is floor(|y|/q + (seed >> 12) / 2^20) * q
+// with y's sign, for normal and subnormal codes (checked on the hardware over
+// the range).
 __device__ __forceinline__ uint32_t encode4(const float* y, const uint32_t* rnd) {
   uint32_t w = 0;
   w = __builtin_amdgcn_cvt_sr_fp8_f32(y[0], rnd[0], w, 0);
@@ -185,88 +214,123 @@ __device__ __forceinline__ uint32_t encode4(const float* y, const uint32_t* rnd)
   return __builtin_amdgcn_cvt_sr_fp8_f32(y[3], rnd[3], w, 3);
 }
 
+// 8-bit moments.  A block of 256 elements is a row of 16 lanes; lane j holds
+// the pieces at 8j and 128 + 8j of it, so every access of a wave is
+// contiguous within a block (16 elements in one run were 11 % slower with
+// fp32 tensors, 88 against 80 us for 25e6 elements, and equal with bf16).
+// Everything between the loads and the stores stays in registers: the
+// block's maxima are four lane rotations, the codes come and go through the
+// e4m3 conversions.  The codes are padded to whole blocks, so only the
+// parameter and the gradient end inside a piece; the gap's codes are zero and
+// stay zero, and add nothing to a maximum.
+//
+// What bounds it is HBM traffic at the rate that three read and three written
+// streams reach: without its arithmetic the kernel takes the same time.  The
+// first version spent 67 vector instructions on an element and was bound by
+// those (2.44 ms where this takes 1.95, for 1.05e9 bf16 elements): what went
+// is the step's IEEE division, lane exchanges through LDS, and bounds checks
+// in whole chunks.  Whole and partial chunks share their arithmetic: as two
+// instantiations the kernel was 118 KB of code and not 53, and a launch of
+// 300,000 elements in 40 tensors of both types took 10.3 us and not 6.1.
 template <bool PB, bool GB>
-__device__ __forceinline__ void chunk8(const ParamTensor& t, const Rule& rule, int64_t start, int len, bool aligned,
+__device__ __forceinline__ void chunk8(const ParamTensor& t, const Rule& rule, int64_t start, int len, bool full,
                                        uint32_t key) {
-  const int e = threadIdx.x * kPer;
-  const int n = len - e;  // <= 0: a lane of the last block past the tensor's end, or a block past it
-  const bool vec = n >= kPer && aligned;
-  char* P = t.param + (start + e) * (PB ? 2 : 4);
-  const char* G = t.grad + (start + e) * (GB ? 2 : 4);
+  constexpr int N = kPer / kPiece;
+  const int row = (threadIdx.x >> 4) * kStateBlock;
+  const int e = row + (threadIdx.x & 15) * kPiece;
+  const bool inside = full || row < len;  // the row's block has elements of this tensor
+  char* P = t.param + start * (PB ? 2 : 4);
+  const char* G = t.grad + start * (GB ? 2 : 4);
   char* CM = t.m + start + e;
   char* CR = t.v + start + e;
-  float2* S = reinterpret_cast<float2*>(t.scales) + (start + e) / kStateBlock;
-  float p[16], m[16], r[16];
-  float am = 0.0f, ar = 0.0f;
+  float2* S = reinterpret_cast<float2*>(t.scales) + (start + row) / kStateBlock;
+  Piece<PB> p[N];
+  Piece<GB> g[N];
+  uint2 wm[N], wr[N];
+  float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-  for (int k = 0; k < 16; ++k) p[k] = m[k] = r[k] = 0.0f;
-  if (n > 0) {
-    float g[16];
-    uint32_t wm[4], wr[4];
-    const float2 s = *S;
-    load8<PB>(P, vec, n, p);
-    load8<PB>(P + 8 * (PB ? 2 : 4), vec, n - 8, p + 8);
-    load8<GB>(G, vec, n, g);
-    load8<GB>(G + 8 * (GB ? 2 : 4), vec, n - 8, g + 8);
-    load_codes(CM, n, wm);
-    load_codes(CR, n, wr);
+  for (int q = 0; q < N; ++q) wm[q] = wr[q] = make_uint2(0, 0);
+  if (inside) {
+    s = *S;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      decode4(wm[k], s.x, m + 4 * k);
-      decode4(wr[k], s.y, r + 4 * k);
-    }
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      float v = r[k] * r[k];
-      rule(p[k], g[k], m[k], v, r[k]);
-    }
-    if (n < kPer) {
-#pragma unroll
-      for (int k = 0; k < 16; ++k)
-        if (k >= n) m[k] = r[k] = 0.0f;  // an element past the end has no part in the block's maximum
-    }
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      am = max_abs(am, m[k]);
-      ar = max_abs(ar, r[k]);
+    for (int q = 0; q < N; ++q) {
+      const int o = q * 16 * kPiece;
+      wm[q] = *reinterpret_cast<const uint2*>(CM + o);
+      wr[q] = *reinterpret_cast<const uint2*>(CR + o);
     }
   }
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) {
-    am = max_abs(am, __shfl_xor(am, o, 16));
-    ar = max_abs(ar, __shfl_xor(ar, o, 16));
+  for (int q = 0; q < N; ++q) {
+    load(p[q], P, e + q * 16 * kPiece, len, full);
+    load(g[q], G, e + q * 16 * kPiece, len, full);
   }
-  if (n <= 0) return;
-  const float im = am < kTiny ? 0.0f : kTop / am;
-  const float ir = ar < kTiny ? 0.0f : kTop / ar;
-  const uint32_t ra = mix(static_cast<uint32_t>((t.counter + start + e) >> 4) ^ key);
-  const uint32_t rb = mix(ra + 0x6A09E667u);
-  uint32_t wm[4], wr[4];
+  float m[kPer], v[kPer];
+  float am = 0.0f, av = 0.0f;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    float ym[4], yr[4];
-    uint32_t rm[4], rr[4];
+  for (int z = 0; z < kPer; z += 2) {
+    const int q = z / kPiece, k = z % kPiece;
+    const uint32_t a = k < 4 ? wm[q].x : wm[q].y, b = k < 4 ? wr[q].x : wr[q].y;
+    const f32x2 cm = (k & 2) ? __builtin_amdgcn_cvt_pk_f32_fp8(a, true) : __builtin_amdgcn_cvt_pk_f32_fp8(a, false);
+    const f32x2 cr = (k & 2) ? __builtin_amdgcn_cvt_pk_f32_fp8(b, true) : __builtin_amdgcn_cvt_pk_f32_fp8(b, false);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t x = ra + (4 * q + k) * rb;
-      rm[k] = x;
-      rr[k] = (x << 16) | (x >> 16);
-      // the scaled maximum may round past 448; a NaN stays in the scale
-      ym[k] = fminf(fmaxf(m[4 * q + k] * im, -kTop), kTop);
-      const float y = r[4 * q + k] * ir;
-      yr[k] = y == 0.0f ? 0.0f : fminf(fmaxf(y, kLeast), kTop);
+    for (int j = 0; j < 2; ++j) {
+      const float x = rule.gs * g[q].get(k + j);
+      const float r = __fmul_rn(s.y, cr[j]);
+      m[z + j] = rule.first(__fmul_rn(s.x, cm[j]), x);
+      v[z + j] = rule.second(__fmul_rn(r, r), x);
     }
-    wm[q] = encode4(ym, rm);
-    wr[q] = encode4(yr, rr);
+    am = max_abs(am, max_abs(m[z], m[z + 1]));
+    av = max_abs(av, max_abs(v[z], v[z + 1]));
   }
-  store8<PB>(P, vec, n, p);
-  store8<PB>(P + 8 * (PB ? 2 : 4), vec, n - 8, p + 8);
-  store_codes(CM, n, wm);
-  store_codes(CR, n, wr);
-  if ((threadIdx.x & 15) == 0)
-    *S = make_float2(am < kTiny ? 0.0f : am / kTop, ar < kTiny ? 0.0f : ar / kTop);
+  am = row_max(am);
+  av = row_max(av);
+  const float ar = sqrtf(av);
+  // 448 * (1 / largest) and largest * (1 / 448), as tensor code computes such
+  // quotients: plain elementwise operations give the same codes and scales
+  const float im = am < kTiny ? 0.0f : kTop * (1.0f / am);
+  const float ir = ar < kTiny ? 0.0f : kTop * (1.0f / ar);
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const int o = q * 16 * kPiece;
+    const int64_t pos = t.counter + start + e + o;
+    const uint32_t ra = mix(static_cast<uint32_t>(pos >> 4) ^ key);
+    const uint32_t rb = mix(ra + 0x6A09E667u);
+    uint32_t rnd = ra + (static_cast<uint32_t>(pos) & 15u) * rb;
+    uint32_t cm[2], cr[2];
+    float np[kPiece];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float ym[4], yr[4];
+      uint32_t rm[4], rr[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int z = q * kPiece + 4 * i + k;
+        const float r = sqrtf(v[z]);
+        np[4 * i + k] = rule.theta(p[q].get(4 * i + k), m[z], r);
+        rm[k] = rnd;
+        rr[k] = (rnd << 16) | (rnd >> 16);
+        rnd += rb;
+        // the scaled maximum may round past 448; a NaN is in the scale
+        ym[k] = __builtin_amdgcn_fmed3f(m[z] * im, -kTop, kTop);
+        const float y = __builtin_amdgcn_fmed3f(r * ir, kLeast, kTop);
+        yr[k] = v[z] > 0.0f ? y : 0.0f;
+      }
+      cm[i] = encode4(ym, rm);
+      cr[i] = encode4(yr, rr);
+    }
+    p[q].set(np);
+    store(p[q], P, e + o, len, full);
+    if (inside) {
+      *reinterpret_cast<uint2*>(CM + o) = make_uint2(cm[0], cm[1]);
+      *reinterpret_cast<uint2*>(CR + o) = make_uint2(cr[0], cr[1]);
+    }
+  }
+  if (inside && (threadIdx.x & 15) == 0)
+    *S = make_float2(am < kTiny ? 0.0f : am * (1.0f / kTop), ar < kTiny ? 0.0f : ar * (1.0f / kTop));
 }
 
+// One workgroup per chunk beat workgroups that take several (2 to 8 in turn,
+// or a grid of 1024 to 16384 that walks the table: 4 to 16 % slower).
 __global__ __launch_bounds__(kThreads) void adamw_multi_kernel(const AdamWMultiArgs a) {
   const int64_t chunk = blockIdx.x;
   const int64_t i = a.chunk_tensor[chunk];
@@ -293,24 +357,17 @@ __global__ __launch_bounds__(kThreads) void adamw_multi_kernel(const AdamWMultiA
   rule.decay = static_cast<float>(1.0 - lr * static_cast<double>(t.weight_decay));
   rule.lr = static_cast<float>(lr) * c1;
 
-  const bool aligned = ((reinterpret_cast<uintptr_t>(t.param) | reinterpret_cast<uintptr_t>(t.grad)) & 15) == 0;
-  if (t.state_bits == 8) {
-    const uint32_t key = mix(mix(static_cast<uint32_t>(step)) ^ a.seed);
-    if (t.param_dtype) {
-      t.grad_dtype ? chunk8<true, true>(t, rule, start, len, aligned, key)
-                   : chunk8<true, false>(t, rule, start, len, aligned, key);
-    } else {
-      t.grad_dtype ? chunk8<false, true>(t, rule, start, len, aligned, key)
-                   : chunk8<false, false>(t, rule, start, len, aligned, key);
-    }
-  } else {
-    if (t.param_dtype) {
-      t.grad_dtype ? chunk32<true, true>(t, rule, start, len, aligned)
-                   : chunk32<true, false>(t, rule, start, len, aligned);
-    } else {
-      t.grad_dtype ? chunk32<false, true>(t, rule, start, len, aligned)
-                   : chunk32<false, false>(t, rule, start, len, aligned);
-    }
+  const uint32_t key = mix(mix(static_cast<uint32_t>(step)) ^ a.seed);
+  const bool full = len == kParamChunk;
+  switch ((t.state_bits == 8) * 4 + t.param_dtype * 2 + t.grad_dtype) {
+    case 0: chunk32<false, false>(t, rule, start, len, full); break;
+    case 1: chunk32<false, true>(t, rule, start, len, full); break;
+    case 2: chunk32<true, false>(t, rule, start, len, full); break;
+    case 3: chunk32<true, true>(t, rule, start, len, full); break;
+    case 4: chunk8<false, false>(t, rule, start, len, full, key); break;
+    case 5: chunk8<false, true>(t, rule, start, len, full, key); break;
+    case 6: chunk8<true, false>(t, rule, start, len, full, key); break;
+    case 7: chunk8<true, true>(t, rule, start, len, full, key); break;
   }
 }
 

@@ -351,7 +351,8 @@ struct GradTensor {
 };
 
 constexpr int64_t kGradChunk = 16384;  // MUON_GRAD_CHUNK
-constexpr int kGradMaxBlocks = 2048;   // workgroups of the norm, one partial sum each
+constexpr int kGradMaxBlocks = 512;    // workgroups of the norm, one partial sum each
+constexpr int kGradOneLaunch = 256;    // up to this many need no second launch
 
 struct GradNormArgs {
   int64_t count, total_chunks;

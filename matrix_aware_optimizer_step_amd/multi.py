@@ -22,6 +22,11 @@ import torch
 from . import _lib as L
 from .muon import _stream, _stream_object, dtype_code, workspace
 
+# The raw handle of the current stream without a Stream object around it
+# (1.7 us less in a call that takes 6); the public way where torch lacks it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: int(torch.cuda.current_stream(index).cuda_stream))
+
 MAX_POSITIONS = 1 << 36  # positions of the 8-bit states' random bits: 2^32 groups of 16 elements
 
 
@@ -79,7 +84,7 @@ class _OnDevice:
         if self.device.type != "cuda":
             raise RuntimeError("the tensors are not on a GPU (there is no CPU path)")
         if stream is None:
-            return int(torch.cuda.current_stream(self.device).cuda_stream)
+            return _raw_stream(self.device.index)
         raw = _stream(stream)
         if raw not in self._seen:
             obj = _stream_object(stream)

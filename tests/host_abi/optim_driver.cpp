@@ -32,7 +32,7 @@ int main() {
   const float inf = std::numeric_limits<float>::infinity(), nan = std::numeric_limits<float>::quiet_NaN();
   auto* control = reinterpret_cast<muon_step_control_t*>(fake + 4096);
 
-  for (int64_t chunks : {int64_t{0}, int64_t{1}, int64_t{2047}, int64_t{2048}, int64_t{1} << 20, (int64_t{1} << 31) - 1}) {
+  for (int64_t chunks : {int64_t{0}, int64_t{1}, int64_t{511}, int64_t{512}, int64_t{1} << 20, (int64_t{1} << 31) - 1}) {
     muon_grad_list_t l{3, chunks, reinterpret_cast<const muon_grad_t*>(fake), reinterpret_cast<const int32_t*>(fake + 64)};
     const size_t need = muon_grad_norm_workspace(chunks);
     optim_stub_workspace(fake + 8192, need);
