@@ -465,8 +465,8 @@ muon_status_t muon_grad_norm(const muon_grad_list_t* grads, float max_norm, int 
  * nearest, an average with beta2 near 1 would never move: a step changes r by
  * far less than half a code step.)  A positive r keeps at least the smallest code
  * 2^-9: with r = 0 beside m > 0 the next update would be m / eps.  A block
- * whose largest value is below 2^-100 holds zeros.  A non-finite gradient
- * makes its block's scales non-finite, and with them every moment of the
+ * whose largest value is below 2^-100 holds zeros.  A gradient that is not
+ * finite, or whose square is not, makes its block's scales non-finite, and with them every moment of the
  * block.
  *   The random bits of an element come from `seed`, t and its position
  * counter + i alone: a = mix(floor(position / 16) ^ mix(mix(t) ^ seed)),

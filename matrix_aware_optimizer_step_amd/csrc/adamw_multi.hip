@@ -330,9 +330,12 @@ __device__ __forceinline__ void chunk8(const ParamTensor& t, const Rule& rule, i
 }
 
 // One workgroup per chunk beat workgroups that take several (2 to 8 in turn,
-// or a grid of 1024 to 16384 that walks the table: 4 to 16 % slower).
+// or a grid of 1024 to 16384 that walks the table: 4 to 16 % slower).  The
+// chunks run from the last to the first: a norm before the step reads the
+// gradients first to last, and what it read last is still in the cache
+// (clipped steps over 60e6 to 300e6 elements 0.3 to 3.6 % faster, others equal).
 __global__ __launch_bounds__(kThreads) void adamw_multi_kernel(const AdamWMultiArgs a) {
-  const int64_t chunk = blockIdx.x;
+  const int64_t chunk = static_cast<int64_t>(gridDim.x) - 1 - blockIdx.x;
   const int64_t i = a.chunk_tensor[chunk];
   if (i < 0 || i >= a.count) return;  // a wrong chunk table: nothing to do here
   const ParamTensor t = a.params[i];

@@ -13,6 +13,7 @@ and counts its own steps.
 
 from __future__ import annotations
 
+import bisect
 import ctypes
 import math
 
@@ -45,12 +46,21 @@ def _check_dense(t: torch.Tensor, what: str) -> None:
     dtype_code(t)  # bfloat16 or float32
 
 
-def _check_apart(tensors, what: str) -> None:
-    """No two tensors share memory: they are updated in one launch."""
-    spans = sorted((t.data_ptr(), t.numel() * t.element_size()) for t in tensors if t.numel())
-    for (a, n), (b, _) in zip(spans, spans[1:]):
-        if a + n > b:
-            raise ValueError(f"two {what} overlap in memory (list a tied parameter once)")
+def _check_apart(params, grads) -> None:
+    """No parameter shares memory with another or with a gradient: all are
+    updated in one launch."""
+    def spans(tensors):
+        return [(t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in tensors if t.numel()]
+
+    written = sorted(spans(params))
+    for (_, end), (start, _) in zip(written, written[1:]):
+        if end > start:
+            raise ValueError("two parameters overlap in memory (list a tied parameter once)")
+    starts = [a for a, _ in written]
+    for a, b in spans(grads):
+        k = bisect.bisect_left(starts, b) - 1  # the last parameter that starts before the gradient's end
+        if k >= 0 and written[k][1] > a:
+            raise ValueError("a gradient overlaps a parameter in memory")
 
 
 def _table(structs, device) -> torch.Tensor:
@@ -200,7 +210,7 @@ class AdamWMulti(_OnDevice):
     With ``control`` the gradients' clip factor, the skip flag, the step number
     and the lr factor are read on the device (see ``StepControl``): run the
     ``GradClip`` that shares it before each step.  Otherwise ``t`` counts the
-    steps.
+    steps, and a step cannot be captured (every replay would repeat its t).
 
     State buffers, each tensor starting on a multiple of 256 elements: ``exp_avg`` and
     ``exp_avg_sq`` (fp32) of the 32-bit tensors, ``codes_m``, ``codes_r``
@@ -223,10 +233,7 @@ class AdamWMulti(_OnDevice):
             _check_dense(g, "gradients")
             if p.device != device or g.device != device:
                 raise ValueError("all tensors must be on one device")
-        _check_apart(params, "parameters")
-        for p, g in ((p, g) for p, g in zip(params, grads) if p.numel()):
-            if p.data_ptr() == g.data_ptr():
-                raise ValueError("a parameter and its gradient are the same memory")
+        _check_apart(params, grads)
         if control is not None and control.device != device:
             raise ValueError("control is on another device than the parameters")
         if not 0 <= int(seed) < 1 << 32:
@@ -282,9 +289,10 @@ class AdamWMulti(_OnDevice):
         h = self.hyper
         h.lr, h.eps = self.lr, self.eps
         h.beta1, h.beta2 = self.betas
-        control = self.control
-        self._call(L.muon_adamw_multi, self.desc, h, self.t + 1, None if control is None else control.data_ptr(),
-                   self._on(stream))
+        control, raw = self.control, self._on(stream)
+        if control is None and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("capturing a step needs a control block: its replays would all use the same t")
+        self._call(L.muon_adamw_multi, self.desc, h, self.t + 1, None if control is None else control.data_ptr(), raw)
         if control is None:
             self.t += 1
 

@@ -465,6 +465,22 @@ def test_captured_step_replays_as_the_eager_one(mx):
         assert torch.equal(eager.scales, graphed.scales) and torch.equal(eager.exp_avg_sq, graphed.exp_avg_sq)
 
 
+def test_capture_without_control_is_refused_and_empty_lists_run(mx):
+    p, g = torch.ones(300, device="cuda"), torch.ones(300, device="cuda")
+    opt = mx.AdamWMulti([p], [g])
+    opt.step()
+    with torch.cuda.graph(torch.cuda.CUDAGraph()):
+        with pytest.raises(RuntimeError, match="control"):
+            opt.step()
+    opt.step()
+    torch.cuda.synchronize()
+    assert opt.t == 2
+    for bits in (8, 32):
+        none = mx.AdamWMulti([p[:0], p[:0]], [g[:0], g[:0]], state_bits=bits)
+        none.step()
+        assert none.t == 1 and none.moments(0)[0].shape == (0,)
+
+
 def test_moments_and_resume(mx, tmp_path):
     def build():
         params, grads, _ = make(MIXED, SIZES, 17)

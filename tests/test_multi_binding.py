@@ -56,8 +56,10 @@ def test_adamw_multi_refuses_shared_memory():
         mx.AdamWMulti([p, p], [z(100), z(100)])           # a tied parameter listed twice
     with pytest.raises(ValueError, match="overlap"):
         mx.AdamWMulti([p[:60], p[50:]], [z(60), z(50)])
-    with pytest.raises(ValueError, match="same memory"):
+    with pytest.raises(ValueError, match="gradient overlaps"):
         mx.AdamWMulti([p], [p])
+    with pytest.raises(ValueError, match="gradient overlaps"):
+        mx.AdamWMulti([p[:40], p[60:]], [z(40), p[20:60]])  # another tensor's parameter
     mx.AdamWMulti([p[:50], p[50:], p[:0]], [z(50), z(50), z(0)])  # neighbours and an empty one are fine
 
 
