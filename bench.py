@@ -117,13 +117,14 @@ def measured_traffic(profile, source, key):
 
 ADAM_LR, ADAM_WD, ADAM_BETAS, ADAM_EPS = 3e-4, 0.1, (0.9, 0.999), 1e-8
 ADAMW_BYTES = 2 + 2 + 2 + 8 + 8  # per element: bf16 theta read+write, bf16 grad, fp32 m and v read+write
+ADAMW8_BYTES = 2 + 2 + 2 + 2 + 2 + 16 / 256  # the same with one byte each of m and v, and a block's two scales
 
 
-def make_adamw_step(mx, names, params, grads):
+def make_adamw_step(mx, names, params, grads, **kw):
     """The AdamW leg this benchmark times: the routing helper over the 8B-style
     model's non-matrix parameters (every one goes to AdamW)."""
     opt = mx.OptimizerStep(list(zip(names, params, grads)), adam_lr=ADAM_LR, adam_betas=ADAM_BETAS,
-                           adam_eps=ADAM_EPS, adam_weight_decay=ADAM_WD)
+                           adam_eps=ADAM_EPS, adam_weight_decay=ADAM_WD, **kw)
     assert opt.muon is None
     return opt
 
@@ -156,8 +157,14 @@ def bench_adamw(args):
     shapes = synth.adamw_workload()
     names = [n for n, _ in shapes]
     params, grads = synth.adamw_tensors(shapes, step=1, device=dev)
-    opt = make_adamw_step(mx, names, params, grads)
+    bits, clip = args.adam_state_bits, args.max_grad_norm
+    opt = make_adamw_step(mx, names, params, grads, adam_state_bits=bits, max_grad_norm=clip)
     elems = sum(g.elements for g in opt.adamw)
+    # with 8-bit states the norm weights (one dimension, undecayed) keep 32 bits
+    step_bytes = sum(p.numel() * (ADAMW8_BYTES if bits == 8 and p.dim() > 1 else ADAMW_BYTES) for p in params)
+    if clip is not None:
+        step_bytes += elems * 2  # the norm reads the gradients before the step does
+    plain = bits == 32 and clip is None
     log(f"[bench] AdamW over {len(shapes)} tensors, {elems / 1e6:.1f} M elements")
     if args.copy_calibration:
         calibration_copy(dev)
@@ -173,7 +180,7 @@ def bench_adamw(args):
     torch.cuda.synchronize()
     wall = time.perf_counter() - t0
     ms = e0.elapsed_time(e1) / args.steps
-    gbs = elems * ADAMW_BYTES / (ms * 1e-3) / 1e9
+    gbs = step_bytes / (ms * 1e-3) / 1e9
     cpu = None
     if not args.no_cpu_baseline:
         from oracle import adamw as OA
@@ -196,12 +203,14 @@ def bench_adamw(args):
            "vs_baseline": None, "dtype": "f32", "data": "synthetic",
            "config": {"workload": f"AdamW leg: embedding and head {synth.ADAMW_VOCAB}x{synth.ADAMW_HIDDEN} bf16, "
                                   f"65 RMSNorm weights of {synth.ADAMW_HIDDEN}", "elements": elems,
-                      "bytes_per_element": ADAMW_BYTES, "parallelism": "single GPU",
+                      "bytes_per_element": step_bytes / elems, "state_bits": bits, "max_grad_norm": clip,
+                      "parallelism": "single GPU",
                       "hyperparameters": {"lr": ADAM_LR, "betas": list(ADAM_BETAS), "eps": ADAM_EPS,
                                           "weight_decay": ADAM_WD}},
            "roofline": {"bound": "hbm", "achieved": gbs, "peak": PEAK_HBM_GBS, "unit": "GB/s",
-                        "frac": gbs / PEAK_HBM_GBS, "kernel": "adamw_kernel",
-                        "traffic": measured_traffic("adamw_kernel_8b_nonmatrix_params.md", "adamw.hip", "bytes_per_step")},
+                        "frac": gbs / PEAK_HBM_GBS, "kernel": "adamw_kernel" if plain else "adamw_multi_kernel",
+                        "traffic": measured_traffic("adamw_kernel_8b_nonmatrix_params.md", "adamw.hip",
+                                                    "bytes_per_step") if plain else None},
            "cpu_baseline": cpu}
     print(json.dumps(out), flush=True)
 
@@ -385,6 +394,10 @@ def main():
     ap.add_argument("--part", default="muon", choices=["muon", "adamw", "soap"],
                     help="muon: the Muon step of --workload (default); adamw: the AdamW step over the 8B-style "
                          "model's embeddings, head and norms; soap: SOAP steps over --workload's matrices")
+    ap.add_argument("--adam-state-bits", type=int, default=32, choices=[8, 32],
+                    help="--part adamw: width of the matrices' moments")
+    ap.add_argument("--max-grad-norm", type=float, default=None,
+                    help="--part adamw: clip by the global gradient norm, taken in every step")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--separate-apply", action="store_true",
                     help="apply the update with its own kernel (muon_apply_grouped) instead of in the last "

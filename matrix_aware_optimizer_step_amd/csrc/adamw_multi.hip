@@ -117,10 +117,14 @@ struct Rule {
   float gs, b1, omb1, b2, omb2, sc2, eps, decay, lr;  // sc2 = sqrt(c2); lr includes c1
 
   __device__ __forceinline__ float first(float m, float g) const {
-    return __fadd_rn(__fmul_rn(b1, m), __fmul_rn(omb1, g));
+#pragma clang fp contract(off)
+    const float old = b1 * m, add = omb1 * g;
+    return old + add;
   }
   __device__ __forceinline__ float second(float v, float g) const {
-    return __fadd_rn(__fmul_rn(b2, v), __fmul_rn(omb2, __fmul_rn(g, g)));
+#pragma clang fp contract(off)
+    const float old = b2 * v, add = omb2 * (g * g);
+    return old + add;
   }
   // v_rcp_f32 (off by 1.5 ulp, a 1e-7 of the step): the IEEE division took 7 %
   // of the time with 8-bit states
@@ -275,9 +279,9 @@ __device__ __forceinline__ void chunk8(const ParamTensor& t, const Rule& rule, i
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const float x = rule.gs * g[q].get(k + j);
-      const float r = __fmul_rn(s.y, cr[j]);
-      m[z + j] = rule.first(__fmul_rn(s.x, cm[j]), x);
-      v[z + j] = rule.second(__fmul_rn(r, r), x);
+      const float r = s.y * cr[j];
+      m[z + j] = rule.first(s.x * cm[j], x);
+      v[z + j] = rule.second(r * r, x);
     }
     am = max_abs(am, max_abs(m[z], m[z + 1]));
     av = max_abs(av, max_abs(v[z], v[z + 1]));

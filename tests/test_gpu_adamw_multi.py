@@ -261,6 +261,39 @@ def test_codes_are_unbiased(mx):
         assert np.all(np.abs(f64(total[k]) / seeds - want) <= 6 * q / 2 / math.sqrt(seeds) + 8 * U * want)
 
 
+def test_moments_are_those_of_elementwise_tensor_code(mx):
+    """m, v, the codes and the scales bit for bit as separate tensor operations
+    give them (each product and sum rounded by itself), over several steps."""
+    n, b1, b2 = 256 * 40, 0.9, 0.999
+    gen = torch.Generator("cuda").manual_seed(5)
+    wide, narrow = (mx.AdamWMulti([torch.zeros(n, device="cuda")], [torch.zeros(n, device="cuda")], betas=(b1, b2),
+                                  state_bits=bits, seed=77) for bits in (32, 8))
+    m = torch.zeros(n, device="cuda")
+    v = torch.zeros_like(m)
+    dm, dr = torch.zeros_like(m), torch.zeros_like(m)  # what the codes stand for
+    for t in range(1, 6):
+        g = torch.randn(n, generator=gen, device="cuda") * torch.exp(torch.randn(n, generator=gen, device="cuda"))
+        for opt in (wide, narrow):
+            opt.grads[0].copy_(g)
+            opt.step()
+        m = m * b1 + g * (1 - b1)
+        v = v * b2 + g * g * (1 - b2)
+        assert torch.equal(wide.exp_avg, m) and torch.equal(wide.exp_avg_sq, v)
+        m8, r8 = dm * b1 + g * (1 - b1), (dr.square() * b2 + g * g * (1 - b2)).sqrt()
+        decoded = []
+        for x, bits, least, got, k in zip((m8, r8), OM.random_bits(np.arange(n), t, 77), (0.0, OM.LEAST),
+                                          (narrow.codes_m, narrow.codes_r), (0, 1)):
+            top = x.view(-1, 256).abs().amax(1, keepdim=True)
+            s = top / 448.0
+            y = (x.view(-1, 256) * (448.0 / top)).view(-1).cpu().numpy()
+            a = np.where(y == 0, 0.0, np.clip(np.abs(y.astype(np.float64)), least, OM.TOP))
+            want = torch.from_numpy(np.copysign(OM.round_code(a, bits), y)).to(torch.float32).cuda()
+            assert torch.equal(got.float(), want)
+            assert torch.equal(narrow.scales[:, k], s.view(-1))
+            decoded.append((want.view(-1, 256) * s).view(-1))
+        dm, dr = decoded
+
+
 def test_more_than_2_to_31_elements(mx):
     """One tensor longer than 32-bit offsets reach: its last blocks against the
     oracle, and the positions of the random bits with them."""
