@@ -83,24 +83,23 @@ class _OnDevice:
     def _own(self, device, buffers) -> None:
         self.device = device
         self._buffers = [b for b in buffers if b is not None]
-        self._seen = set()
+        self._seen = set()  # streams that the allocator knows these buffers are used on
         if device.type == "cuda":
             # the buffers are filled: any stream may use them from here on
             torch.cuda.current_stream(device).synchronize()
+            self._seen.add(_raw_stream(device.index))
 
     def _on(self, stream):
-        """Raw stream of a call.  A stream given by the caller is recorded on
-        the buffers once, so that their memory outlives its kernels."""
+        """Raw stream of a call (None: the current one).  A stream other than
+        the one the buffers were made on is recorded on them once, so that
+        their memory outlives its kernels."""
         if self.device.type != "cuda":
             raise RuntimeError("the tensors are not on a GPU (there is no CPU path)")
-        if stream is None:
-            return _raw_stream(self.device.index)
-        raw = _stream(stream)
+        raw = _raw_stream(self.device.index) if stream is None else _stream(stream)
         if raw not in self._seen:
-            obj = _stream_object(stream)
+            used = torch.cuda.current_stream(self.device) if stream is None else _stream_object(stream)
             for b in self._buffers:
-                if b.is_cuda:
-                    b.record_stream(obj)
+                b.record_stream(used)
             self._seen.add(raw)
         return raw
 

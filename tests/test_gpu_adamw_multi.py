@@ -438,6 +438,29 @@ def test_equal_inputs_give_equal_bits_on_any_stream(mx):
     assert torch.equal(a[1].exp_avg, b[1].exp_avg) and torch.equal(a[2].control.norm, b[2].control.norm)
 
 
+@pytest.mark.parametrize("explicit", [True, False])
+def test_dropped_objects_outlive_their_kernels(mx, explicit):
+    """The optimizer is dropped while its step still waits on a side stream:
+    its state's memory must not go to the next allocation before the step ran."""
+    n = 1 << 20
+    p, twin, g = torch.ones(n, device="cuda"), torch.ones(n, device="cuda"), torch.randn(n, device="cuda")
+    one = mx.AdamWMulti([twin], [g], lr=1e-2)
+    one.step()
+    opt = mx.AdamWMulti([p], [g], lr=1e-2)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+        if not explicit:
+            opt.step()
+    if explicit:
+        opt.step(stream=side)
+    del opt
+    junk = [torch.full((n,), 1e30, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(p, twin) and len(junk) == 8
+
+
 def test_two_steps_at_once_on_two_streams(mx):
     """Two optimizers with their own control blocks and workspaces, interleaved on two streams."""
     def build(k):
