@@ -279,19 +279,21 @@ class AdamWMulti(_OnDevice):
         tensors = _table((L.MuonParam * n)(*rows), device)
         chunks = torch.from_numpy(chunk_tensor).to(device)
         self.desc = L.MuonParamList(n, first[-1], tensors.data_ptr(), chunks.data_ptr())
-        self.hyper = L.MuonAdamWHyper(0.0, 0.0, 0.0, 0.0, self.seed, 0)
+        self.hyper, self._now = L.MuonAdamWHyper(0.0, 0.0, 0.0, 0.0, self.seed, 0), None
         self.elements = sum(numels)
         self._own(device, [self.exp_avg, self.exp_avg_sq, codes, self.scales, tensors, chunks,
                            None if control is None else control.block])
 
     def step(self, stream=None) -> None:
-        h = self.hyper
-        h.lr, h.eps = self.lr, self.eps
-        h.beta1, h.beta2 = self.betas
+        now = (self.lr, self.eps, *self.betas)
+        if now != self._now:  # they may be set between steps
+            h = self.hyper
+            h.lr, h.eps, h.beta1, h.beta2 = now
+            self._now = now
         control, raw = self.control, self._on(stream)
         if control is None and torch.cuda.is_current_stream_capturing():
             raise RuntimeError("capturing a step needs a control block: its replays would all use the same t")
-        self._call(L.muon_adamw_multi, self.desc, h, self.t + 1, None if control is None else control.data_ptr(), raw)
+        self._call(L.muon_adamw_multi, self.desc, self.hyper, self.t + 1, None if control is None else control.data_ptr(), raw)
         if control is None:
             self.t += 1
 
