@@ -446,11 +446,12 @@ muon_status_t muon_grad_norm(const muon_grad_list_t* grads, float max_norm, int 
  * their types, each with its own weight decay and learning-rate factor, and
  * with its moments in 32 bits or in 8.
  *
- * The update, in fp32 (bias corrections from t in double):
+ * The update, in fp32:
  *   g <- scale * g
  *   m <- beta1*m + (1-beta1)*g;   v <- beta2*v + (1-beta2)*g^2
  *   theta <- (1 - l*weight_decay)*theta - l*(m / (1-beta1^t)) / (sqrt(v / (1-beta2^t)) + eps)
- * with l = lr * lr_factor of the tensor.  A BF16 theta is rounded once to nearest even.
+ * with l = lr * lr_factor of the tensor.  A BF16 theta is rounded once to
+ * nearest even.
  *
  * 32-bit state: m and v are floats, zero before step 1.
  *
@@ -463,11 +464,11 @@ muon_status_t muon_grad_norm(const muon_grad_list_t* grads, float max_norm, int 
  * where q = 2^(max(floor(log2|y|), -6) - 3) is the code step at |y| and u in
  * [0, 1) has 20 random bits, so a code's expected value is y.  (Rounded to
  * nearest, an average with beta2 near 1 would never move: a step changes r by
- * far less than half a code step.)  A positive r keeps at least the smallest code
- * 2^-9: with r = 0 beside m > 0 the next update would be m / eps.  A block
+ * far less than half a code step.)  A positive r keeps at least the smallest
+ * code 2^-9: with r = 0 beside m > 0 the next update would be m / eps.  A block
  * whose largest value is below 2^-100 holds zeros.  A gradient that is not
- * finite, or whose square is not, makes its block's scales non-finite, and with them every moment of the
- * block.
+ * finite, or whose square is not, makes its block's scales non-finite, and
+ * with them every moment of the block.
  *   The random bits of an element come from `seed`, t and its position
  * counter + i alone: a = mix(floor(position / 16) ^ mix(mix(t) ^ seed)),
  * b = mix(a + 0x6A09E667), s = a + (position mod 16) * b mod 2^32 (16 elements
@@ -495,7 +496,7 @@ typedef struct muon_param {
   float lr_factor;
   int32_t param_dtype;  /* muon_dtype_t */
   int32_t grad_dtype;   /* muon_dtype_t */
-  int32_t state_bits;   /* 32 or 8 */
+  int32_t state_bits;   /* 32 or 8; a tensor with another value is left alone */
   int32_t reserved;     /* 0 */
 } muon_param_t;
 
