@@ -119,7 +119,8 @@ class StepControl:
     reading them with ``.item()`` waits for the device, using them in further
     device work does not.  ``lr_factor`` multiplies the learning rate of every
     call that reads the block; write it with ``lr_factor.fill_(x)``, also
-    between replays of a captured step.
+    between replays of a captured step.  Calls that share a block must be
+    ordered: on one stream, or by events.
     """
 
     def __init__(self, device="cuda", step: int = 0):
