@@ -334,9 +334,13 @@ class AdamWMulti(_OnDevice):
         if list(state.get("bits", [])) != list(self.bits) or len(state["state"]) != len(mine) or any(
                 len(a) != len(b) or any(x.shape != y.shape for x, y in zip(a, b)) for a, b in zip(state["state"], mine)):
             raise ValueError("the state was saved for differently shaped tensors or other state widths")
-        for saved, own in zip(state["state"], mine):
+        for i, (saved, own) in enumerate(zip(state["state"], mine)):
             for x, y in zip(saved, own):
                 (y.view(torch.uint8) if y.dtype == torch.float8_e4m3fn else y).copy_(x)
+            # a block's maximum covers the codes behind the tensor too: none may stay from before
+            end, n = self._at[i] + self.params[i].numel(), -self.params[i].numel() % L.STATE_BLOCK
+            for buf in (self.exp_avg, self.exp_avg_sq) if self.bits[i] == 32 else (self.codes_m, self.codes_r):
+                (buf.view(torch.uint8) if buf.dtype == torch.float8_e4m3fn else buf)[end:end + n].zero_()
         h = state["hyper"]
         self.lr, self.betas, self.eps = h["lr"], tuple(h["betas"]), h["eps"]
         self.seed = self.hyper.seed = int(h["seed"])

@@ -1,0 +1,37 @@
+"""CPU checks of what the many-tensor operators save, restore and refuse on the
+host (nothing touches a GPU)."""
+
+import pytest
+import torch
+
+import matrix_aware_optimizer_step_amd as mx
+
+
+def z(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def raw(buffer):
+    return buffer.view(torch.uint8) if buffer.element_size() == 1 else buffer
+
+
+def buffers(opt):
+    return [raw(b) for b in (opt.exp_avg, opt.exp_avg_sq, opt.codes_m, opt.codes_r)]
+
+
+def test_load_clears_what_lies_behind_the_tensors():
+    """The state is padded to whole blocks, and a block's maximum is taken over
+    its padding too: nothing there may outlive a load."""
+    def build():
+        return mx.AdamWMulti([z(300), z(5), z(1)], [z(300), z(5), z(1)], state_bits=[8, 32, 8])
+
+    a, b = build(), build()
+    a.codes_m.view(torch.uint8)[:300] = 0x30
+    a.exp_avg[:5] = 2.0
+    for buf in buffers(b):
+        buf.fill_(0xFE if buf.dtype == torch.uint8 else float("nan"))
+    b.scales.fill_(float("nan"))
+    b.load_state_dict(a.state_dict())
+    for x, y in zip(buffers(a), buffers(b)):
+        assert torch.equal(x, y)
+    assert torch.equal(a.scales, b.scales)
