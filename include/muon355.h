@@ -479,9 +479,8 @@ muon_status_t muon_grad_norm(const muon_grad_list_t* grads, float max_norm, int 
  * Equal inputs give equal bits on every run.
  *
  * State arrays hold numel rounded up to a multiple of MUON_STATE_BLOCK
- * elements; those past numel are zero before step 1 and stay zero (for finite
- * gradients).  theta and the gradients end at numel: nothing past it is read
- * or written.
+ * elements; those past numel are zero before step 1 and stay zero.  theta
+ * and the gradients end at numel: nothing past it is read or written.
  */
 typedef struct muon_param {
   void* param;          /* theta, in/out */

@@ -166,6 +166,7 @@ __device__ __forceinline__ void chunk32(const ParamTensor& t, const Rule& rule, 
       nm[k] = rule.first(m[q].get(k), x);
       nv[k] = rule.second(v[q].get(k), x);
       np[k] = rule.theta(p[q].get(k), nm[k], sqrtf(nv[k]));
+      if (!full && e + k >= len) nm[k] = nv[k] = 0.0f;  // behind the tensor, also where the clip factor is a NaN
     }
     p[q].set(np);
     m[q].set(nm);
@@ -226,7 +227,7 @@ __device__ __forceinline__ uint32_t encode4(const float* y, const uint32_t* rnd)
 // block's maxima are four lane rotations, the codes come and go through the
 // e4m3 conversions.  The codes are padded to whole blocks, so only the
 // parameter and the gradient end inside a piece; the gap's codes are zero and
-// stay zero, and add nothing to a maximum.
+// stay zero whatever the block holds, and add nothing to a maximum.
 //
 // What bounds it is HBM traffic at the rate that three read and three written
 // streams reach: without its arithmetic the kernel takes the same time.  The
@@ -282,6 +283,8 @@ __device__ __forceinline__ void chunk8(const ParamTensor& t, const Rule& rule, i
       const float r = s.y * cr[j];
       m[z + j] = rule.first(s.x * cm[j], x);
       v[z + j] = rule.second(r * r, x);
+      // behind the tensor, also where the block's scale or the clip factor is a NaN
+      if (!full && e + q * 16 * kPiece + k + j >= len) m[z + j] = v[z + j] = 0.0f;
     }
     am = max_abs(am, max_abs(m[z], m[z + 1]));
     av = max_abs(av, max_abs(v[z], v[z + 1]));
@@ -318,6 +321,7 @@ __device__ __forceinline__ void chunk8(const ParamTensor& t, const Rule& rule, i
         ym[k] = __builtin_amdgcn_fmed3f(m[z] * im, -kTop, kTop);
         const float y = __builtin_amdgcn_fmed3f(r * ir, kLeast, kTop);
         yr[k] = v[z] > 0.0f ? y : 0.0f;
+        if (!full && e + o + 4 * i + k >= len) ym[k] = 0.0f;  // 0 times a NaN's scale
       }
       cm[i] = encode4(ym, rm);
       cr[i] = encode4(yr, rr);
