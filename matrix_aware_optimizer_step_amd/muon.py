@@ -241,6 +241,8 @@ class MuonStep:
             self.m.append(batch(torch.zeros(shape, dtype=torch.float32, device=dev)))
             self.ss.append(torch.empty(w.count, dtype=torch.float32, device=dev))
         self.device = dev
+        if control is not None and control.device != dev:
+            raise ValueError("control is on another device than the weights")
         # each stage runs the groups together, at most 8 per grouped launch
         self.chunks = [list(range(i, min(i + 8, len(self.w)))) for i in range(0, len(self.w), 8)]
         self.packed = bool(packed)

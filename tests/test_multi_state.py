@@ -35,3 +35,17 @@ def test_load_clears_what_lies_behind_the_tensors():
     for x, y in zip(buffers(a), buffers(b)):
         assert torch.equal(x, y)
     assert torch.equal(a.scales, b.scales)
+
+
+def muon(control=None, **kw):
+    w, g = z(1, 64, 64), z(1, 64, 64)
+    return mx.MuonStep([(w, g)], control=control, **kw)
+
+
+def test_muon_step_refuses_a_control_block_on_another_device():
+    muon(mx.StepControl("cpu"))
+    block = mx.StepControl("cpu")
+    for elsewhere in ("cuda:0", "meta"):
+        block.device = torch.device(elsewhere)
+        with pytest.raises(ValueError, match="another device"):
+            muon(block)
