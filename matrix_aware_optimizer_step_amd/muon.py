@@ -327,8 +327,8 @@ class MuonStep:
         st = stream if stream is not None else torch.cuda.current_stream()
         s = _stream(st)
         packed = self.packed and self.steps >= 1
-        if self.control is not None and not packed:
-            raise ValueError("a control block needs steps >= 1")
+        if self.control is not None and (not packed or self.fused_apply):
+            raise ValueError("a control block needs packed=True, fused_apply=False and steps >= 1")
         if not packed:
             self._unpacked_buffers()
         if not (packed and self.fused_apply):

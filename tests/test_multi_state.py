@@ -49,3 +49,42 @@ def test_muon_step_refuses_a_control_block_on_another_device():
         block.device = torch.device(elsewhere)
         with pytest.raises(ValueError, match="another device"):
             muon(block)
+
+
+class Recorded:
+    """Stands in for a library call and keeps its arguments."""
+
+    def __init__(self, log, name):
+        self.log, self.name = log, name
+
+    def __call__(self, *args):
+        self.log.append((self.name, args))
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """MuonStep's library calls, recorded in order, on no device."""
+    from matrix_aware_optimizer_step_amd import muon as mu
+    log = []
+    for name in ("muon_momentum_packed_grouped", "muon_momentum_packed_grouped_controlled",
+                 "muon_orthogonalize_packed_grouped", "muon_orthogonalize_apply_packed_grouped", "muon_apply_grouped",
+                 "muon_apply_grouped_controlled"):
+        monkeypatch.setattr(mu.L, name, Recorded(log, name))
+    return log
+
+
+def test_muon_step_checks_its_path_before_every_step(calls):
+    """The folded apply does not follow a control block, also when it is asked
+    for after construction."""
+    step = muon(mx.StepControl("cpu"))
+    step.step(stream=7)
+    assert [name for name, _ in calls] == ["muon_momentum_packed_grouped_controlled", "muon_orthogonalize_packed_grouped",
+                                           "muon_apply_grouped_controlled"]
+    calls.clear()
+    for name, value in (("fused_apply", True), ("packed", False), ("steps", 0)):
+        old = getattr(step, name)
+        setattr(step, name, value)
+        with pytest.raises(ValueError, match="control block"):
+            step.step(stream=7)
+        setattr(step, name, old)
+    assert calls == []
