@@ -402,7 +402,7 @@ typedef struct muon_grad {
   const void* data;
   int64_t numel;       /* >= 0 */
   int64_t first_chunk; /* chunks of the tensors before it in the list */
-  int32_t dtype;       /* muon_dtype_t; the types of a list may differ */
+  int32_t dtype;       /* muon_dtype_t; the types of a list may differ, another value adds nothing */
   int32_t reserved;    /* 0 */
 } muon_grad_t;
 
@@ -493,9 +493,9 @@ typedef struct muon_param {
   int64_t first_chunk;  /* chunks of the tensors before it in the list */
   float weight_decay;
   float lr_factor;
-  int32_t param_dtype;  /* muon_dtype_t */
+  int32_t param_dtype;  /* muon_dtype_t; a tensor with another value here or below is left alone */
   int32_t grad_dtype;   /* muon_dtype_t */
-  int32_t state_bits;   /* 32 or 8; a tensor with another value is left alone */
+  int32_t state_bits;   /* 32 or 8 */
   int32_t reserved;     /* 0 */
 } muon_param_t;
 

@@ -370,8 +370,7 @@ __global__ __launch_bounds__(kThreads) void adamw_multi_kernel(const AdamWMultiA
 
   const uint32_t key = mix(mix(static_cast<uint32_t>(step)) ^ a.seed);
   const bool full = len == kParamChunk;
-  const int width = t.state_bits == 8 ? 4 : t.state_bits == 32 ? 0 : 8;
-  switch (width + t.param_dtype * 2 + t.grad_dtype) {
+  switch (param_form(t.state_bits, t.param_dtype, t.grad_dtype)) {
     case 0: chunk32<false, false>(t, rule, start, len, full); break;
     case 1: chunk32<false, true>(t, rule, start, len, full); break;
     case 2: chunk32<true, false>(t, rule, start, len, full); break;

@@ -115,7 +115,7 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const GradNormArgs 
     if (t < 0 || t >= a.count) continue;
     const GradTensor g = a.grads[t];
     const int64_t start = (c - g.first_chunk) * kGradChunk;
-    if (start < 0 || start >= g.numel) continue;
+    if (start < 0 || start >= g.numel || !known_type(g.dtype)) continue;
     const int len = static_cast<int>(g.numel - start < kGradChunk ? g.numel - start : kGradChunk);
     acc = g.dtype ? chunk_sumsq<true>(g.data + start * 2, len, acc) : chunk_sumsq<false>(g.data + start * 4, len, acc);
   }

@@ -350,6 +350,10 @@ struct GradTensor {
   int32_t dtype, reserved;
 };
 
+// Descriptors lie in device memory, where no call can check them: a kernel
+// passes over a tensor whose type is none.
+__host__ __device__ constexpr bool known_type(int32_t dtype) { return static_cast<uint32_t>(dtype) <= 1u; }
+
 constexpr int64_t kGradChunk = 16384;  // MUON_GRAD_CHUNK
 constexpr int kGradMaxBlocks = 512;    // workgroups of the norm, one partial sum each
 constexpr int kGradOneLaunch = 256;    // up to this many need no second launch
@@ -377,6 +381,13 @@ struct ParamTensor {
   float weight_decay, lr_factor;
   int32_t param_dtype, grad_dtype, state_bits, reserved;
 };
+
+// The form of the update that a tensor takes: 0 to 3 with 32-bit states, 4 to 7
+// with 8-bit ones, by parameter and gradient type; -1 for none of them.
+__host__ __device__ constexpr int param_form(int32_t state_bits, int32_t param_dtype, int32_t grad_dtype) {
+  if ((state_bits != 8 && state_bits != 32) || !known_type(param_dtype) || !known_type(grad_dtype)) return -1;
+  return (state_bits == 8 ? 4 : 0) + param_dtype * 2 + grad_dtype;
+}
 
 constexpr int64_t kParamChunk = 4096;  // elements per workgroup; MUON_PARAM_CHUNK
 constexpr int kStateBlock = 256;       // elements per scale; MUON_STATE_BLOCK

@@ -86,3 +86,41 @@ def test_restoring_after_a_bad_step_resumes_bit_for_bit(mx, bits):
         assert torch.equal(p, q)
         for x, y in zip(used._state(i), fresh._state(i)):
             assert torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
+
+
+def table(obj, struct, count):
+    """The descriptors of a list as int32 words in device memory, a row each."""
+    import ctypes
+    size = ctypes.sizeof(struct)
+    (rows,) = [b for b in obj._buffers if b.data_ptr() == (obj.desc.params if hasattr(obj.desc, "params") else obj.desc.grads)]
+    return rows[:count * size].view(torch.int32).view(count, size // 4)
+
+
+@pytest.mark.parametrize("field,value", [("param_dtype", 2), ("param_dtype", -1), ("grad_dtype", 2), ("grad_dtype", 1 << 20),
+                                         ("state_bits", 4), ("state_bits", 0)])
+@pytest.mark.parametrize("bits", [8, 32])
+def test_descriptors_of_no_type_are_left_alone(mx, field, value, bits):
+    L = mx._lib
+    opt, twin = build(mx, bits), build(mx, bits)
+    table(opt, L.MuonParam, len(SIZES))[3, getattr(L.MuonParam, field).offset // 4] = value
+    before = [opt.params[3].clone()] + [x.clone() for x in opt._state(3)]
+    for o in (opt, twin):
+        o.step()
+    torch.cuda.synchronize()
+    for x, y in zip(before, [opt.params[3]] + opt._state(3)):
+        assert torch.equal(x.view(torch.uint8), y.contiguous().view(torch.uint8))
+    for i in (0, 1, 2, 4):
+        assert torch.equal(opt.params[i], twin.params[i])
+
+
+@pytest.mark.parametrize("value", [2, -1, 1 << 20])
+def test_gradients_of_no_type_add_nothing(mx, value):
+    L = mx._lib
+    grads = build(mx, 32).grads
+    clip, rest = mx.GradClip(grads), mx.GradClip([g for i, g in enumerate(grads) if i != 3])
+    table(clip, L.MuonGrad, len(grads))[3, L.MuonGrad.dtype.offset // 4] = value
+    clip.step()
+    rest.step()
+    torch.cuda.synchronize()
+    # the chunks go to workgroups in another grouping: two fp64 sums, rounded once
+    assert abs(float(clip.control.norm) - float(rest.control.norm)) <= 2.0 ** -23 * float(rest.control.norm)

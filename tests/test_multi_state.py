@@ -1,10 +1,17 @@
 """CPU checks of what the many-tensor operators save, restore and refuse on the
 host (nothing touches a GPU)."""
 
+import os
+import shutil
+import subprocess
+
 import pytest
 import torch
 
 import matrix_aware_optimizer_step_amd as mx
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "matrix_aware_optimizer_step_amd", "csrc")
 
 
 def z(*shape, dtype=torch.float32):
@@ -88,3 +95,44 @@ def test_muon_step_checks_its_path_before_every_step(calls):
             step.step(stream=7)
         setattr(step, name, old)
     assert calls == []
+
+
+FORMS = """
+#include <cstdio>
+#include "muon_internal.h"
+int main() {
+  const int bits[] = {-8, 0, 1, 4, 8, 16, 31, 32, 33, 64, 264};
+  const int types[] = {-2147483647, -1, 0, 1, 2, 3, 4, 256, 2147483647};
+  for (int b : bits)
+    for (int p : types)
+      for (int g : types) std::printf("%d %d %d %d\\n", b, p, g, muon::param_form(b, p, g));
+  for (int g : types) std::printf("%d %d\\n", g, muon::known_type(g));
+}
+"""
+
+
+def test_only_the_eight_forms_are_taken(tmp_path):
+    """A type code or a state width that is none never picks a form (a 32-bit
+    tensor has no scales for the 8-bit form to read)."""
+    gxx = shutil.which("g++")
+    if gxx is None or not os.path.isdir("/opt/rocm/include"):
+        pytest.skip("needs g++ and the ROCm headers")
+    (tmp_path / "forms.cpp").write_text(FORMS)
+    exe = tmp_path / "forms"
+    res = subprocess.run([gxx, "-std=c++17", "-Wall", "-Werror", "-D__HIP_PLATFORM_AMD__", "-I/opt/rocm/include", "-I", CSRC,
+                          str(tmp_path / "forms.cpp"), "-o", str(exe)], capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr[-3000:]
+    lines = [tuple(map(int, line.split())) for line in subprocess.run([str(exe)], capture_output=True, text=True).stdout.split("\n") if line]
+    assert len(lines) == 11 * 9 * 9 + 9
+    seen = set()
+    for row in lines:
+        if len(row) == 2:
+            assert row[1] == (row[0] in (0, 1)), row
+            continue
+        bits, p, g, form = row
+        if bits in (8, 32) and p in (0, 1) and g in (0, 1):
+            assert form == (4 if bits == 8 else 0) + 2 * p + g, row
+            seen.add(form)
+        else:
+            assert form == -1, row
+    assert seen == set(range(8))
