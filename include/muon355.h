@@ -505,7 +505,7 @@ typedef struct muon_param {
 /* As muon_grad_list, with chunks of MUON_PARAM_CHUNK elements. */
 typedef struct muon_param_list {
   int64_t count;
-  int64_t total_chunks;
+  int64_t total_chunks;        /* 0 .. 2^24-1 */
   const muon_param_t* params;  /* device array [count] */
   const int32_t* chunk_tensor; /* device array [total_chunks] */
 } muon_param_list_t;

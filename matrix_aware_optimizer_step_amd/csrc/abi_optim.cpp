@@ -16,6 +16,8 @@ namespace {
 using namespace muon;
 
 constexpr int64_t kMaxChunks = (int64_t{1} << 31) - 1;
+// AdamW takes a workgroup of 256 for a chunk, and a launch has fewer than 2^32 work-items.
+constexpr int64_t kMaxParamChunks = (int64_t{1} << 24) - 1;
 
 static_assert(sizeof(StepControl) == sizeof(muon_step_control_t) && sizeof(StepControl) == 64, "control block");
 static_assert(offsetof(StepControl, skip) == offsetof(muon_step_control_t, skip) &&
@@ -91,6 +93,8 @@ muon_status_t muon_adamw_multi(const muon_param_list_t* l, const muon_adamw_hype
   if (!l) return fail(MUON_ERR_INVALID_VALUE, "parameter list is NULL");
   const muon_status_t st = check_list(l->count, l->total_chunks, l->params, l->chunk_tensor);
   if (st != MUON_OK) return st;
+  if (l->total_chunks > kMaxParamChunks)
+    return fail(MUON_ERR_INVALID_VALUE, "total_chunks %lld outside [0, 2^24-1]", (long long)l->total_chunks);
   if (!h) return fail(MUON_ERR_INVALID_VALUE, "hyperparameters are NULL");
   if (h->reserved != 0) return fail(MUON_ERR_INVALID_VALUE, "reserved field must be 0");
   if (!(h->beta1 >= 0.0 && h->beta1 < 1.0) || !(h->beta2 >= 0.0 && h->beta2 < 1.0))

@@ -136,3 +136,13 @@ def test_only_the_eight_forms_are_taken(tmp_path):
         else:
             assert form == -1, row
     assert seen == set(range(8))
+
+
+def test_adamw_multi_refuses_more_chunks_than_one_launch_holds():
+    """A launch has fewer than 2^32 work-items, 256 of them to a chunk."""
+    L = mx._lib
+    hyper = L.MuonAdamWHyper(1e-3, 0.9, 0.999, 1e-8, 0, 0)
+    for chunks in (1 << 24, (1 << 31) - 1, 1 << 31):
+        with pytest.raises(L.MuonError, match="total_chunks") as e:
+            L.muon_adamw_multi(L.MuonParamList(1, chunks, 0x10000, 0x10000), hyper, 1, None, 0)
+        assert e.value.status == 1
