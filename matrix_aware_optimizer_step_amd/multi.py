@@ -103,6 +103,13 @@ class _OnDevice:
             self._seen.add(raw)
         return raw
 
+    def _capturing(self, stream) -> bool:
+        """Whether the stream of a call (None: the current one) is being captured."""
+        if stream is None and self.device.index == torch.cuda.current_device():
+            return torch.cuda.is_current_stream_capturing()
+        with torch.cuda.stream(torch.cuda.current_stream(self.device) if stream is None else _stream_object(stream)):
+            return torch.cuda.is_current_stream_capturing()
+
     def _call(self, fn, *args) -> None:
         """Runs fn with this object's device current."""
         if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
@@ -292,7 +299,7 @@ class AdamWMulti(_OnDevice):
             h.lr, h.eps, h.beta1, h.beta2 = now
             self._now = now
         control, raw = self.control, self._on(stream)
-        if control is None and torch.cuda.is_current_stream_capturing():
+        if control is None and self._capturing(stream):
             raise RuntimeError("capturing a step needs a control block: its replays would all use the same t")
         self._call(L.muon_adamw_multi, self.desc, self.hyper, self.t + 1, None if control is None else control.data_ptr(), raw)
         if control is None:

@@ -124,3 +124,32 @@ def test_gradients_of_no_type_add_nothing(mx, value):
     torch.cuda.synchronize()
     # the chunks go to workgroups in another grouping: two fp64 sums, rounded once
     assert abs(float(clip.control.norm) - float(rest.control.norm)) <= 2.0 ** -23 * float(rest.control.norm)
+
+
+def test_only_the_calls_own_stream_decides_about_a_capture(mx):
+    """Without a control block a step refuses a stream that is being captured,
+    whichever stream is current, and takes one that is not."""
+    opt, twin = build(mx, 8), build(mx, 8)
+    captured, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    keep = torch.zeros(64, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=captured):
+        keep.add_(1.0)
+        opt.step(stream=other)
+        with torch.cuda.stream(other):
+            for stream in (captured, captured.cuda_stream):
+                with pytest.raises(RuntimeError, match="control"):
+                    opt.step(stream=stream)
+            opt.step()
+            opt.step(stream=other.cuda_stream)
+        with pytest.raises(RuntimeError, match="control"):
+            opt.step()
+    assert opt.t == 3
+    for _ in range(3):
+        twin.step()
+    torch.cuda.synchronize()
+    graph.replay()
+    torch.cuda.synchronize()
+    for p, q in zip(opt.params, twin.params):
+        assert torch.equal(p, q)
