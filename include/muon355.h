@@ -521,7 +521,8 @@ typedef struct muon_adamw_hyper {
  *          skip and a further factor of lr are read from it when the kernel
  *          runs, and `step` is not used; a block whose step is below 1 counts
  *          as t = 1.
- * lr finite; beta1, beta2 in [0, 1); eps finite >= 0.
+ * lr finite; beta1, beta2 in [0, 1); eps 0 or in [2^-126, 2^125] (with eps 0
+ * an element that has had no gradient yet becomes 0 / 0).
  * No tensor may appear twice or overlap another in the list. */
 muon_status_t muon_adamw_multi(const muon_param_list_t* params, const muon_adamw_hyper_t* hyper, int64_t step,
                                const muon_step_control_t* control, void* stream);

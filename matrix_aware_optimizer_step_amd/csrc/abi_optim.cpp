@@ -99,7 +99,9 @@ muon_status_t muon_adamw_multi(const muon_param_list_t* l, const muon_adamw_hype
   if (h->reserved != 0) return fail(MUON_ERR_INVALID_VALUE, "reserved field must be 0");
   if (!(h->beta1 >= 0.0 && h->beta1 < 1.0) || !(h->beta2 >= 0.0 && h->beta2 < 1.0))
     return fail(MUON_ERR_INVALID_VALUE, "betas must lie in [0, 1)");
-  if (!std::isfinite(h->eps) || h->eps < 0.0) return fail(MUON_ERR_INVALID_VALUE, "eps must be finite and >= 0");
+  // the kernel's reciprocal flushes what is below fp32's normal range, on either side
+  if (h->eps != 0.0 && !(h->eps >= 0x1p-126 && h->eps <= 0x1p125))
+    return fail(MUON_ERR_INVALID_VALUE, "eps must be 0 or lie in [2^-126, 2^125]");
   if (!std::isfinite(h->lr)) return fail(MUON_ERR_INVALID_VALUE, "lr must be finite");
   if (!control && step < 1) return fail(MUON_ERR_INVALID_VALUE, "step %lld < 1", (long long)step);
   if (control && !aligned16(control))

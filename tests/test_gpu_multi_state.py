@@ -153,3 +153,22 @@ def test_only_the_calls_own_stream_decides_about_a_capture(mx):
     torch.cuda.synchronize()
     for p, q in zip(opt.params, twin.params):
         assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("eps", [2.0 ** -126, 1e-30, 2.0 ** 125])
+@pytest.mark.parametrize("bits", [8, 32])
+def test_smallest_and_largest_eps(mx, bits, eps):
+    """Elements that never had a gradient stay as they are, and the others
+    follow m / (r + eps)."""
+    n = 600
+    p, g = torch.full((n,), 0.75, device="cuda"), torch.zeros(n, device="cuda")
+    g[::3] = 2.0
+    opt = mx.AdamWMulti([p], [g], lr=2.0 ** -4, betas=(0.5, 0.75), eps=eps, state_bits=bits)
+    opt.step()
+    torch.cuda.synchronize()
+    # m = 1, v = 1, both corrected to 2 and 4: the step is 2^-4 * 2 / (2 + eps), with at most 8 roundings of its own
+    want = 0.75 - 2.0 ** -4 * 2.0 / (2.0 + eps)
+    assert torch.all((p[::3].double() - want).abs() <= 2.0 ** -24 * want + 8 * 2.0 ** -24 * 2.0 ** -4)
+    rest = torch.ones(n, dtype=torch.bool, device="cuda")
+    rest[::3] = False
+    assert torch.all(p[rest] == 0.75)

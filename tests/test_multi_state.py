@@ -146,3 +146,13 @@ def test_adamw_multi_refuses_more_chunks_than_one_launch_holds():
         with pytest.raises(L.MuonError, match="total_chunks") as e:
             L.muon_adamw_multi(L.MuonParamList(1, chunks, 0x10000, 0x10000), hyper, 1, None, 0)
         assert e.value.status == 1
+
+
+@pytest.mark.parametrize("eps", [2.0 ** -149, 1e-40, 2.0 ** -126 * (1 - 2.0 ** -24), 2.0 ** 125 * (1 + 2.0 ** -23), 1e39])
+def test_adamw_multi_refuses_an_eps_that_its_reciprocal_loses(eps):
+    """The hardware's reciprocal of a denominator below 2^-126 is infinite, and
+    above 2^126 zero."""
+    L = mx._lib
+    with pytest.raises(L.MuonError, match="eps") as e:
+        L.muon_adamw_multi(L.MuonParamList(1, 1, 0x10000, 0x10000), L.MuonAdamWHyper(1e-3, 0.9, 0.999, eps, 0, 0), 1, None, 0)
+    assert e.value.status == 1
