@@ -149,6 +149,16 @@ class StepControl:
     def data_ptr(self) -> int:
         return self.block.data_ptr()
 
+    def state_dict(self) -> dict:
+        """What the next step goes on from: both counts and the lr factor."""
+        return {"step": int(self.step.item()), "skipped": int(self.skipped.item()),
+                "lr_factor": float(self.lr_factor.item())}
+
+    def load_state_dict(self, state: dict) -> None:
+        self.step.fill_(int(state["step"]))
+        self.skipped.fill_(int(state["skipped"]))
+        self.lr_factor.fill_(float(state["lr_factor"]))
+
 
 class GradClip(_OnDevice):
     """Global norm of a list of gradients, and the factor that clips it.
@@ -324,7 +334,9 @@ class AdamWMulti(_OnDevice):
 
     def state_dict(self) -> dict:
         """The step count, every tensor's state (host copies: m and v, or the
-        codes of m and r as uint8 and their scales) and the hyperparameters."""
+        codes of m and r as uint8 and their scales) and the hyperparameters.  Of
+        a control block it holds the step count; ``StepControl.state_dict()``
+        has the rest."""
         def host(x):
             x = x.view(torch.uint8) if x.dtype == torch.float8_e4m3fn else x
             return x.detach().to("cpu", copy=True)

@@ -568,10 +568,12 @@ class OptimizerStep:
 
     def state_dict(self) -> dict:
         """Everything a resumed run needs besides the weights: the Muon
-        momentum, every AdamW group's moments and step count, the
-        hyperparameters and the routing they belong to."""
+        momentum, every AdamW group's moments and step count, the control
+        block's counts and lr factor, the hyperparameters and the routing they
+        belong to."""
         return {"routing": dict(self.routing), "muon": None if self.muon is None else self.muon.state_dict(),
-                "adamw": [g.state_dict() for g in self.adamw]}
+                "adamw": [g.state_dict() for g in self.adamw],
+                "control": None if self.clip is None else self.clip.control.state_dict()}
 
     def load_state_dict(self, state: dict) -> None:
         if state["routing"] != self.routing or len(state["adamw"]) != len(self.adamw) or \
@@ -581,3 +583,5 @@ class OptimizerStep:
             self.muon.load_state_dict(state["muon"])
         for g, s in zip(self.adamw, state["adamw"]):
             g.load_state_dict(s)
+        if self.clip is not None and state.get("control") is not None:
+            self.clip.control.load_state_dict(state["control"])

@@ -156,3 +156,49 @@ def test_adamw_multi_refuses_an_eps_that_its_reciprocal_loses(eps):
     with pytest.raises(L.MuonError, match="eps") as e:
         L.muon_adamw_multi(L.MuonParamList(1, 1, 0x10000, 0x10000), L.MuonAdamWHyper(1e-3, 0.9, 0.999, eps, 0, 0), 1, None, 0)
     assert e.value.status == 1
+
+
+MODEL = [("embed_tokens.weight", (24, 16)), ("layers.0.attn.wq", (16, 16)), ("layers.0.norm.weight", (16,))]
+MUON_ONLY = [("layers.0.attn.wq", (16, 16)), ("layers.0.attn.wk", (16, 16))]
+
+
+def model_step(spec, **kw):
+    return mx.OptimizerStep([(name, z(*shape), z(*shape)) for name, shape in spec], **kw)
+
+
+@pytest.mark.parametrize("spec", [MODEL, MUON_ONLY])
+def test_a_whole_step_saves_its_control_block(spec, tmp_path):
+    a, b = model_step(spec, max_grad_norm=1.0), model_step(spec, max_grad_norm=1.0)
+    a.clip.control.step.fill_(41)
+    a.clip.control.skipped.fill_(3)
+    a.clip.control.lr_factor.fill_(0.25)
+    torch.save(a.state_dict(), tmp_path / "s.pt")
+    b.load_state_dict(torch.load(tmp_path / "s.pt", weights_only=True))
+    c = b.clip.control
+    assert (int(c.step), int(c.skipped), float(c.lr_factor)) == (41, 3, 0.25)
+
+
+def test_states_with_and_without_a_control_block():
+    """A step without clipping takes a clipped one's state, and the reverse
+    keeps the block's lr factor; so does a state saved without the block."""
+    clipped, plain = model_step(MODEL, max_grad_norm=1.0, adam_state_bits=8), model_step(MODEL, adam_state_bits=8)
+    clipped.clip.control.step.fill_(9)
+    plain.load_state_dict(clipped.state_dict())
+    assert plain.adamw[0].t == 9
+    clipped.clip.control.lr_factor.fill_(0.5)
+    plain.adamw[0].t = 12
+    clipped.load_state_dict(plain.state_dict())
+    assert int(clipped.clip.control.step) == 12 and float(clipped.clip.control.lr_factor) == 0.5
+    old = clipped.state_dict()
+    del old["control"]
+    clipped.clip.control.step.fill_(0)
+    clipped.load_state_dict(old)
+    assert int(clipped.clip.control.step) == 12
+
+
+def test_a_control_block_by_itself():
+    a, b = mx.StepControl("cpu", step=5), mx.StepControl("cpu")
+    a.lr_factor.fill_(0.125)
+    a.skipped.fill_(2)
+    b.load_state_dict(a.state_dict())
+    assert (int(b.step), int(b.skipped), float(b.lr_factor)) == (5, 2, 0.125)
