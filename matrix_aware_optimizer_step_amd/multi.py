@@ -154,7 +154,13 @@ class StepControl:
         return {"step": int(self.step.item()), "skipped": int(self.skipped.item()),
                 "lr_factor": float(self.lr_factor.item())}
 
+    def check_state(self, state: dict) -> None:
+        """Raises where load_state_dict() would refuse the state."""
+        if not {"step", "skipped", "lr_factor"} <= set(state):
+            raise ValueError("the state was saved for something else than a control block")
+
     def load_state_dict(self, state: dict) -> None:
+        self.check_state(state)
         self.step.fill_(int(state["step"]))
         self.skipped.fill_(int(state["skipped"]))
         self.lr_factor.fill_(float(state["lr_factor"]))
@@ -346,13 +352,18 @@ class AdamWMulti(_OnDevice):
                 "bits": list(self.bits),
                 "hyper": {"lr": self.lr, "betas": list(self.betas), "eps": self.eps, "seed": self.seed}}
 
-    def load_state_dict(self, state: dict) -> None:
-        """Restores state_dict()'s state (weight decays and lr factors are the
-        constructor's).  With a control block its step count is set too."""
+    def check_state(self, state: dict) -> None:
+        """Raises where load_state_dict() would refuse the state."""
         mine = [self._state(i) for i in range(len(self.params))]
         if list(state.get("bits", [])) != list(self.bits) or len(state["state"]) != len(mine) or any(
                 len(a) != len(b) or any(x.shape != y.shape for x, y in zip(a, b)) for a, b in zip(state["state"], mine)):
             raise ValueError("the state was saved for differently shaped tensors or other state widths")
+
+    def load_state_dict(self, state: dict) -> None:
+        """Restores state_dict()'s state (weight decays and lr factors are the
+        constructor's).  With a control block its step count is set too."""
+        self.check_state(state)
+        mine = [self._state(i) for i in range(len(self.params))]
         for i, (saved, own) in enumerate(zip(state["state"], mine)):
             for x, y in zip(saved, own):
                 (y.view(torch.uint8) if y.dtype == torch.float8_e4m3fn else y).copy_(x)

@@ -309,10 +309,15 @@ class MuonStep:
                           "coeffs": [float(x) for x in self.coeffs], "eps": self.eps, "lr": self.lr,
                           "weight_decay": self.weight_decay, "mode": self.mode, "coeff": self.coeff}}
 
-    def load_state_dict(self, state: dict) -> None:
+    def check_state(self, state: dict) -> None:
+        """Raises where load_state_dict() would refuse the state."""
         mom = state["momentum"]
         if len(mom) != len(self.m) or any(tuple(t.shape) != tuple(m.keep[0].shape) for m, t in zip(self.m, mom)):
             raise ValueError("the state was saved for differently shaped groups")
+
+    def load_state_dict(self, state: dict) -> None:
+        self.check_state(state)
+        mom = state["momentum"]
         for m, t in zip(self.m, mom):
             m.keep[0].copy_(t)
         h = state["hyper"]
@@ -446,10 +451,14 @@ class AdamW:
                 "exp_avg_sq": [v.detach().to("cpu", copy=True) for v in self.exp_avg_sq],
                 "hyper": {"lr": self.lr, "betas": list(self.betas), "eps": self.eps, "weight_decay": self.weight_decay}}
 
-    def load_state_dict(self, state: dict) -> None:
+    def check_state(self, state: dict) -> None:
+        """Raises where load_state_dict() would refuse the state."""
         for key, own in (("exp_avg", self.exp_avg), ("exp_avg_sq", self.exp_avg_sq)):
-            if len(state[key]) != len(own) or any(t.shape != o.shape for t, o in zip(state[key], own)):
+            if len(state.get(key, [])) != len(own) or any(t.shape != o.shape for t, o in zip(state[key], own)):
                 raise ValueError("the state was saved for differently shaped tensors")
+
+    def load_state_dict(self, state: dict) -> None:
+        self.check_state(state)
         # copied into the existing buffers: the device pointer tables stay valid
         for key, own in (("exp_avg", self.exp_avg), ("exp_avg_sq", self.exp_avg_sq)):
             for o, t in zip(own, state[key]):
@@ -579,9 +588,11 @@ class OptimizerStep:
         if state["routing"] != self.routing or len(state["adamw"]) != len(self.adamw) or \
                 (state["muon"] is None) != (self.muon is None):
             raise ValueError("the state was saved for a different set of parameters")
-        if self.muon is not None:
-            self.muon.load_state_dict(state["muon"])
-        for g, s in zip(self.adamw, state["adamw"]):
-            g.load_state_dict(s)
+        parts = [] if self.muon is None else [(self.muon, state["muon"])]
+        parts += zip(self.adamw, state["adamw"])
         if self.clip is not None and state.get("control") is not None:
-            self.clip.control.load_state_dict(state["control"])
+            parts.append((self.clip.control, state["control"]))
+        for own, saved in parts:  # all of them before any is changed
+            own.check_state(saved)
+        for own, saved in parts:
+            own.load_state_dict(saved)

@@ -202,3 +202,28 @@ def test_a_control_block_by_itself():
     a.skipped.fill_(2)
     b.load_state_dict(a.state_dict())
     assert (int(b.step), int(b.skipped), float(b.lr_factor)) == (5, 2, 0.125)
+
+
+def test_a_refused_state_changes_nothing():
+    """Every part is checked before any is copied, whichever does not fit."""
+    one_type, many = model_step(MODEL[1:]), model_step(MODEL[1:], max_grad_norm=1.0)
+    for own, other in ((one_type, many), (many, one_type)):
+        other.muon.momentum_buffers[0].fill_(3.0)
+        own.muon.lr = 0.75
+        with pytest.raises(ValueError, match="saved for"):
+            own.load_state_dict(other.state_dict())
+        assert torch.all(own.muon.momentum_buffers[0] == 0.0) and own.muon.lr == 0.75
+        other.muon.momentum_buffers[0].zero_()
+    bad = many.state_dict()
+    bad["control"] = {"step": 7}
+    many.muon.momentum_buffers[0].fill_(5.0)
+    with pytest.raises(ValueError, match="saved for"):
+        many.load_state_dict(bad)
+    assert torch.all(many.muon.momentum_buffers[0] == 5.0)
+    bad = many.state_dict()
+    bad["muon"]["momentum"][0] = z(1, 16, 17)
+    many.clip.control.step.fill_(4)
+    many.adamw[0].exp_avg.fill_(2.0)
+    with pytest.raises(ValueError, match="saved for"):
+        many.load_state_dict(bad)
+    assert int(many.clip.control.step) == 4 and torch.all(many.adamw[0].exp_avg == 2.0)
