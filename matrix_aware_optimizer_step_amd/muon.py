@@ -229,6 +229,7 @@ class MuonStep:
         self.steps, self.coeffs, self.eps = steps, coeffs, eps
         self.lr, self.weight_decay, self.mode, self.coeff = lr, weight_decay, mode, coeff
         self.w, self.g, self.m, self.n, self.o, self.ss = [], [], [], [], [], []
+        self._seen = set()  # streams that the allocator knows the buffers of this object are used on
         dev = None
         for weights, grads in groups:
             w, g = batch(weights), batch(grads)
@@ -263,6 +264,7 @@ class MuonStep:
         when the update is folded into the last step, which needs none."""
         if self.o:
             return
+        self._seen.clear()
         for w in self.w:
             self.o.append(batch(torch.empty((w.count, w.rows, w.cols), dtype=w.keep[-1].dtype, device=self.device)))
 
@@ -273,6 +275,7 @@ class MuonStep:
         separate calls; made on first use."""
         if self.mws:
             return
+        self._seen.clear()
         for g in self.g:
             self.n.append(batch(torch.empty((g.count, g.rows, g.cols), dtype=torch.float32, device=self.device)))
         for ch in self.chunks:
@@ -282,6 +285,18 @@ class MuonStep:
             need = L.muon_orthogonalize_grouped_workspace([self.g[i].count for i in ch], [self.g[i].rows for i in ch],
                                                           [self.g[i].cols for i in ch], self.compute)
             self.ows.append(workspace(need, self.device))
+
+    def _outlive(self, stream, raw: int) -> None:
+        """The memory that this object allocated, and the control block's,
+        outlives the kernels it sends to a stream."""
+        if raw in self._seen:
+            return
+        made = [b.keep[0] for b in self.m + self.n + self.o]
+        made += self.ss + self.pws + self.mws + self.ows + _owned(self.w + self.g)
+        if self.control is not None:
+            made.append(self.control.block)
+        _record_on(_stream_object(stream) if self.device.type == "cuda" else stream, made)
+        self._seen.add(raw)
 
     @property
     def momentum_buffers(self):
@@ -338,6 +353,7 @@ class MuonStep:
             self._unpacked_buffers()
         if not (packed and self.fused_apply):
             self._ortho()
+        self._outlive(st, s)
         a, b, c = self.coeffs
         if events is not None:
             events[0].record(st)

@@ -172,3 +172,27 @@ def test_smallest_and_largest_eps(mx, bits, eps):
     rest = torch.ones(n, dtype=torch.bool, device="cuda")
     rest[::3] = False
     assert torch.all(p[rest] == 0.75)
+
+
+@pytest.mark.parametrize("explicit", [True, False])
+def test_a_dropped_muon_step_outlives_its_kernels(mx, explicit):
+    """MuonStep and its control block are dropped while the step still waits on
+    a side stream: their memory must not go to new tensors before it ran."""
+    gen = torch.Generator().manual_seed(2)
+    g = torch.randn(2, 256, 320, generator=gen).cuda()
+    w = torch.randn(2, 256, 320, generator=gen).cuda()
+    twin = w.clone()
+    mx.MuonStep([(twin, g)], lr=0.01, control=mx.StepControl("cuda")).step()
+    step = mx.MuonStep([(w, g)], lr=0.01, control=mx.StepControl("cuda"))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+        if not explicit:
+            step.step()
+    if explicit:
+        step.step(stream=side)
+    del step
+    junk = [torch.full((n,), 2, dtype=torch.uint8, device="cuda") for n in [64] * 64 + [1 << 20] * 16]
+    torch.cuda.synchronize()
+    assert torch.equal(w, twin) and len(junk) == 80

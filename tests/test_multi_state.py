@@ -227,3 +227,31 @@ def test_a_refused_state_changes_nothing():
     with pytest.raises(ValueError, match="saved for"):
         many.load_state_dict(bad)
     assert int(many.clip.control.step) == 4 and torch.all(many.adamw[0].exp_avg == 2.0)
+
+
+def test_muon_step_holds_its_memory_on_every_stream(calls, monkeypatch):
+    """What a MuonStep allocated, and the control block it reads, are recorded
+    once on each stream that its kernels go to."""
+    from matrix_aware_optimizer_step_amd import muon as mu
+    log = []
+    monkeypatch.setattr(mu, "_record_on", lambda s, ts: log.append((s, [t.data_ptr() for t in ts])))
+    for name in ("muon_momentum_grouped", "muon_orthogonalize_grouped"):
+        monkeypatch.setattr(mu.L, name, Recorded(calls, name))
+    control = mx.StepControl("cpu")
+    step = mx.MuonStep([([z(16, 16), z(16, 16)], [z(16, 16), z(16, 16)]), (z(1, 8, 8), z(1, 8, 8))], control=control)
+    for stream in (7, 7, 8, 7):
+        step.step(stream=stream)
+    assert [s for s, _ in log] == [7, 8]
+    mine = [control.block, *step.momentum_buffers, *step.ortho_buffers, *step.sumsq_buffers, *step.pws,
+            *(t for b in step.w + step.g for t in b.owned)]
+    assert len(mine) == 1 + 3 * 2 + 1 + 2
+    assert all(sorted(ptrs) == sorted(t.data_ptr() for t in mine) for _, ptrs in log)
+    # buffers made by a later step are recorded too
+    log.clear()
+    folded = mx.MuonStep([(z(1, 16, 16), z(1, 16, 16))], fused_apply=True)
+    folded.step(stream=7)
+    folded.packed = False
+    folded.step(stream=7)
+    assert [s for s, _ in log] == [7, 7]
+    late = [*(b.keep[0] for b in folded.n + folded.o), *folded.mws, *folded.ows]
+    assert len(late) == 4 and {t.data_ptr() for t in late} <= set(log[1][1])
