@@ -97,9 +97,10 @@ class _OnDevice:
             raise RuntimeError("the tensors are not on a GPU (there is no CPU path)")
         raw = _raw_stream(self.device.index) if stream is None else _stream(stream)
         if raw not in self._seen:
-            used = torch.cuda.current_stream(self.device) if stream is None else _stream_object(stream)
-            for b in self._buffers:
-                b.record_stream(used)
+            with torch.cuda.device(self.device):  # a raw handle is a stream of the current device
+                used = torch.cuda.current_stream() if stream is None else _stream_object(stream)
+                for b in self._buffers:
+                    b.record_stream(used)
             self._seen.add(raw)
         return raw
 
@@ -107,8 +108,9 @@ class _OnDevice:
         """Whether the stream of a call (None: the current one) is being captured."""
         if stream is None and self.device.index == torch.cuda.current_device():
             return torch.cuda.is_current_stream_capturing()
-        with torch.cuda.stream(torch.cuda.current_stream(self.device) if stream is None else _stream_object(stream)):
-            return torch.cuda.is_current_stream_capturing()
+        with torch.cuda.device(self.device):
+            with torch.cuda.stream(torch.cuda.current_stream() if stream is None else _stream_object(stream)):
+                return torch.cuda.is_current_stream_capturing()
 
     def _call(self, fn, *args) -> None:
         """Runs fn with this object's device current."""

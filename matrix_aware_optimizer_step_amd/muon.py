@@ -344,6 +344,9 @@ class MuonStep:
         """Enqueue one step.  ``events``, if given, is four torch.cuda.Event
         objects recorded before momentum, before orthogonalization, before
         apply and after apply (phase timing on the same stream)."""
+        if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
+            with torch.cuda.device(self.device):
+                return self.step(stream, events)
         st = stream if stream is not None else torch.cuda.current_stream()
         s = _stream(st)
         packed = self.packed and self.steps >= 1

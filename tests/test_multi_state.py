@@ -255,3 +255,33 @@ def test_muon_step_holds_its_memory_on_every_stream(calls, monkeypatch):
     assert [s for s, _ in log] == [7, 7]
     late = [*(b.keep[0] for b in folded.n + folded.o), *folded.mws, *folded.ows]
     assert len(late) == 4 and {t.data_ptr() for t in late} <= set(log[1][1])
+
+
+def test_muon_step_runs_on_its_own_device(calls, monkeypatch):
+    """The norm goes to its tensors' device whichever is current; Muon under
+    the same block has to follow it there, onto that device's stream."""
+    import contextlib
+    current = [0]
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], torch.device(d).index
+        yield
+        current[0] = before
+
+    class Stream:
+        def __init__(self, index):
+            self.cuda_stream = 100 + index
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: Stream(current[0]))
+    monkeypatch.setattr(mx.muon, "_record_on", lambda *a: None)
+    step = muon(mx.StepControl("cpu"))
+    step.device = torch.device("cuda:1")  # the library's calls are stand-ins
+    for now in (0, 1):
+        current[0] = now
+        calls.clear()
+        step.step()
+        assert len(calls) == 3 and all(args[-1] == 101 for _, args in calls)
+        assert current[0] == now
