@@ -311,10 +311,10 @@ class AdamWMulti(_OnDevice):
                            None if control is None else control.block])
 
     def step(self, stream=None) -> None:
-        now = (self.lr, self.eps, *self.betas)
+        now = (self.seed, self.lr, self.eps, *self.betas)
         if now != self._now:  # they may be set between steps
             h = self.hyper
-            h.lr, h.eps, h.beta1, h.beta2 = now
+            h.seed, h.lr, h.eps, h.beta1, h.beta2 = now
             self._now = now
         control, raw = self.control, self._on(stream)
         if control is None and self._capturing(stream):

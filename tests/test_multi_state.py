@@ -285,3 +285,15 @@ def test_muon_step_runs_on_its_own_device(calls, monkeypatch):
         step.step()
         assert len(calls) == 3 and all(args[-1] == 101 for _, args in calls)
         assert current[0] == now
+
+
+def test_hyperparameters_set_between_steps_reach_the_next(monkeypatch):
+    opt = mx.AdamWMulti([z(300)], [z(300)], state_bits=8, seed=3)
+    seen = []
+    monkeypatch.setattr(opt, "_on", lambda stream: 0)
+    monkeypatch.setattr(opt, "_capturing", lambda stream: False)
+    monkeypatch.setattr(mx._lib, "muon_adamw_multi", lambda desc, h, *a: seen.append((h.lr, h.beta1, h.beta2, h.eps, h.seed)))
+    opt.step()
+    opt.lr, opt.betas, opt.eps, opt.seed = 0.5, (0.25, 0.75), 1e-6, 9
+    opt.step()
+    assert seen == [(1e-3, 0.9, 0.999, 1e-8, 3), (0.5, 0.25, 0.75, 1e-6, 9)] and opt.t == 2
