@@ -471,11 +471,14 @@ muon_status_t muon_grad_norm(const muon_grad_list_t* grads, float max_norm, int 
  * with them every moment of the block.
  *   The random bits of an element come from `seed`, t and its position
  * counter + i alone: a = mix(floor(position / 16) ^ mix(mix(t) ^ seed)),
- * b = mix(a + 0x6A09E667), s = a + (position mod 16) * b mod 2^32 (16 elements
- * draw from one arithmetic progression with a random step, so any two of them
- * are independent); m takes the bits 31..12 of s, r the bits 31..12 of s
- * rotated by 16.  mix(x): x ^= x >> 16; x *= 0xBB67AE85; x ^= x >> 15;
- * x *= 0x9E3779B9; x ^= x >> 16.
+ * b = mix(a + 0x6A09E667), s = a + (position mod 16) * b mod 2^32; m takes the
+ * bits 31..12 of s, r the bits 31..12 of s rotated by 16.  mix(x):
+ * x ^= x >> 16; x *= 0xBB67AE85; x ^= x >> 15; x *= 0x9E3779B9; x ^= x >> 16.
+ * 16 elements draw from one arithmetic progression with a random step: any two
+ * of them have independent bits for m, and for r independent leading 13 bits
+ * (of the bits 4 to 6 of r's 20, the first k are equal in elements whose
+ * distance 2^k divides).  m and r of one element have independent leading 16
+ * bits (the leading four of each are the last four of the other).
  * Equal inputs give equal bits on every run.
  *
  * State arrays hold numel rounded up to a multiple of MUON_STATE_BLOCK
