@@ -464,7 +464,9 @@ muon_status_t muon_grad_norm(const muon_grad_list_t* grads, float max_norm, int 
  * where q = 2^(max(floor(log2|y|), -6) - 3) is the code step at |y| and u in
  * [0, 1) has 20 random bits, so a code's expected value is y.  (Rounded to
  * nearest, an average with beta2 near 1 would never move: a step changes r by
- * far less than half a code step.)  A positive r keeps at least the smallest
+ * far less than half a code step.)  The mean of y is kept, not that of
+ * y^2: v comes out high by r's variance, 5 to 6 % of it with Gaussian
+ * gradients.  A positive r keeps at least the smallest
  * code 2^-9: with r = 0 beside m > 0 the next update would be m / eps.  A block
  * whose largest value is below 2^-100 holds zeros.  A gradient that is not
  * finite, or whose square is not, makes its block's scales non-finite, and

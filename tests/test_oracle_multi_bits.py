@@ -1,6 +1,6 @@
-"""CPU pins of how far the 8-bit states' random bits are independent: which
-bits two elements of a group of 16 share, which bits one element's m and r
-share, and that what they do not share looks independent."""
+"""CPU pins of the 8-bit states' rounding: which random bits two elements of a
+group of 16 share, which bits one element's m and r share, that what they do
+not share looks independent, and by how much v = r^2 is high."""
 
 import math
 
@@ -53,3 +53,25 @@ def test_m_and_r_of_one_element(drawn):
     for a in (17, 10, 4):  # the 16 leading bits of each
         for b in (17, 10, 4):
             table_is_flat((m >> np.uint64(a)) & np.uint64(7), (r >> np.uint64(b)) & np.uint64(7))
+
+
+def test_v_is_high_by_the_variance_of_r():
+    """A code's mean is r, so its square is high by the code's variance, and
+    the average collects the excess of 1/(1 - beta2) steps.  A step that moves
+    r by d (small beside the code step q) rounds with variance q*|d|; for
+    Gaussian gradients |d| is (1 - beta2)/2 * r * 0.97 in the mean, so the excess
+    is 0.48 * q/r of v: 3 to 6 % for q/r between 1/16 and 1/8, and the blocks'
+    scales, which move too, add to it.  2 to 10 % is asked."""
+    n, beta2 = 4096, 0.99
+    rng = np.random.default_rng(1)
+    values = OM.code_value(np.arange(127))
+    codes, scales, zeros = np.zeros(n, dtype=np.uint8), np.zeros((n // 256, 2)), np.zeros(n, dtype=np.uint8)
+    v, high = np.zeros(n), []
+    for t in range(1, 801):
+        g = rng.standard_normal(n)
+        v = beta2 * v + (1 - beta2) * g * g
+        got = OM.adamw8_step(np.zeros(n), g, zeros, codes, scales, t, 0.0, 0.0, beta2, 1e-8, 0.0, seed=5)
+        codes, scales = np.searchsorted(values, got["codes_r"]).astype(np.uint8), got["scales"]
+        if t > 400 and t % 20 == 0:
+            high.append(np.mean((got["codes_r"] * OM.per_block(scales[:, 1], n)) ** 2) / np.mean(v) - 1)
+    assert 0.02 <= np.mean(high) <= 0.10
