@@ -428,8 +428,9 @@ typedef struct muon_grad_list {
  *   step += 1, or skipped += 1 when skip
  * The gradients are only read: the calls that take `control` multiply by
  * `scale` as they read them.  Squares and sums are fp64 in an order that
- * depends on the list alone, so no finite gradient overflows and equal
- * inputs give equal bits.
+ * depends on the list alone: none overflows, and equal inputs give equal bits.
+ * The norm itself is a float: finite gradients whose norm is past the largest
+ * float have an infinite one, and scale 0 (1 when max_norm is infinite).
  *
  * max_norm : > 0; infinity never clips.  flags: 0 or MUON_SKIP_NONFINITE.
  * workspace: at least muon_grad_norm_workspace bytes, 16-byte aligned; holds

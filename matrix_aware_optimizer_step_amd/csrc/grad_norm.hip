@@ -13,8 +13,8 @@
 // Bound by HBM: 1.05e9 bf16 gradients in 316 us, 6.6 TB/s.  Two workgroups
 // per compute unit with eight 16-byte loads in flight per thread; 4, 8 or 1
 // per unit took 340, 353 and 420 us.  Squares are formed and added in fp64
-// (v_fma_f64 has fp32's rate here), so the largest finite gradients do not
-// overflow and no length loses bits.
+// (v_fma_f64 has fp32's rate here), so no sum of finite gradients overflows
+// and no length loses bits; the norm itself is a float and can be infinite.
 
 #include "muon_internal.h"
 

@@ -196,3 +196,15 @@ def test_a_dropped_muon_step_outlives_its_kernels(mx, explicit):
     junk = [torch.full((n,), 2, dtype=torch.uint8, device="cuda") for n in [64] * 64 + [1 << 20] * 16]
     torch.cuda.synchronize()
     assert torch.equal(w, twin) and len(junk) == 80
+
+
+def test_a_norm_past_the_largest_float(mx):
+    """Finite gradients whose norm no float holds: an infinite norm, which
+    counts as not finite, and nothing of the gradients is taken."""
+    g = torch.full((3000,), 3e38, device="cuda")
+    for max_norm, scale in ((1.0, 0.0), (math.inf, 1.0)):
+        for skip in (False, True):
+            c = mx.GradClip([g], max_norm=max_norm, skip_nonfinite=skip)
+            c.step()
+            c = c.control
+            assert (float(c.norm), float(c.scale), int(c.skip), int(c.step)) == (math.inf, scale, skip, not skip)
