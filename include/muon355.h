@@ -535,9 +535,9 @@ muon_status_t muon_adamw_multi(const muon_param_list_t* params, const muon_adamw
 
 /* muon_momentum_packed_grouped and muon_apply_grouped under a control block
  * (DEVICE memory, not NULL): the momentum reads scale * G in place of G, and
- * with skip set the momentum leaves M and the apply leaves W as they are (the
- * Newton-Schulz call between them then works on whatever the workspace held,
- * and nothing takes its result).  Without skip and with scale = 1 the results
+ * with skip set the momentum leaves M and the apply leaves W as they are (sumsqs
+ * and the Newton-Schulz call between them then come from whatever the workspace
+ * held, and nothing takes their results).  Without skip and with scale = 1 the results
  * are those of the plain calls bit for bit.  lr is multiplied by the block's
  * lr_factor. */
 muon_status_t muon_momentum_packed_grouped_controlled(int ngroups, const muon_batch_t* grads,

@@ -111,8 +111,7 @@ __device__ __forceinline__ void store(const Piece<BF16>& x, char* base, int e, i
 // What one step does to one element.  Every product and sum of the moments is
 // rounded by itself (no contraction): both moments then round as the formula
 // is written, whichever way the compiler schedules it, and it costs nothing
-// beside the memory traffic (1.90 ms either way for 1.05e9 elements with
-// 8-bit states).
+// beside the memory accesses (equal times for 1.05e9 elements with 8-bit states).
 struct Rule {
   float gs, b1, omb1, b2, omb2, sc2, eps, decay, lr;  // sc2 = sqrt(c2); lr includes c1
 
@@ -229,14 +228,16 @@ __device__ __forceinline__ uint32_t encode4(const float* y, const uint32_t* rnd)
 // parameter and the gradient end inside a piece; the gap's codes are zero and
 // stay zero whatever the block holds, and add nothing to a maximum.
 //
-// What bounds it is HBM traffic at the rate that three read and three written
-// streams reach: without its arithmetic the kernel takes the same time.  The
+// What bounds it is its memory accesses, 5.4 TB/s over three read and three
+// written streams (1.94 ms for 1.05e9 bf16 elements): without its arithmetic the
+// kernel takes the same time.  Its pointers come out of a descriptor, so the
+// accesses are flat ones; what global ones would take is not measured.  The
 // first version spent 67 vector instructions on an element and was bound by
-// those (2.44 ms where this takes 1.95, for 1.05e9 bf16 elements): what went
-// is the step's IEEE division, lane exchanges through LDS, and bounds checks
-// in whole chunks.  Whole and partial chunks share their arithmetic: as two
-// instantiations the kernel was 118 KB of code and not 53, and a launch of
-// 300,000 elements in 40 tensors of both types took 10.3 us and not 6.1.
+// those (2.44 ms): what went is the step's IEEE division, lane exchanges through
+// LDS, and bounds checks in whole chunks.  Whole and partial chunks share their
+// arithmetic: as two instantiations the kernel had twice the code (now 58 KB),
+// and a launch of 300,000 elements in 40 tensors of both types took 10.3 us
+// and not 6.1.
 template <bool PB, bool GB>
 __device__ __forceinline__ void chunk8(const ParamTensor& t, const Rule& rule, int64_t start, int len, bool full,
                                        uint32_t key) {

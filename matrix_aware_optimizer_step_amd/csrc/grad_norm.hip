@@ -6,9 +6,12 @@
 // At most kGradMaxBlocks workgroups walk the list's chunks, workgroup b taking
 // the chunks b, b + grid, ..., and each leaves one fp64 sum; the sums are then
 // added in a fixed order.  Up to kGradOneLaunch workgroups the one that draws
-// the last ticket does that (65 norm weights of 4096: 5.1 us a call against
-// 7.0 with a second launch); with more of them the tickets queue up on one
-// address (1371 workgroups: 25 us against 14), so a second launch does it.
+// the last ticket does that; with more of them a second launch does it, since
+// the tickets are drawn one after another.  One launch against two, us a call
+// among others, bf16: 16 workgroups 5.2 and 7.1, 65 5.9 and 7.1, 128 6.7 and
+// 7.1, 160 7.1 and 7.2, 200 7.7 and 7.3, 256 8.5 and 7.1, 384 10.6 and 7.6,
+// 512 12.7 and 8.7.  The two meet at 160, so between that and 256 a second
+// launch would be the faster, by 1.4 us at most.
 //
 // Bound by HBM: 1.05e9 bf16 gradients in 316 us, 6.6 TB/s.  Two workgroups
 // per compute unit with eight 16-byte loads in flight per thread; 4, 8 or 1

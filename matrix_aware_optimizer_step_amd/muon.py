@@ -541,7 +541,10 @@ class OptimizerStep:
     whose step count then is the AdamW step number: such a step can be captured
     in a graph and replayed.  ``adam_state_bits=8`` keeps the AdamW moments of
     the decayed tensors in 8 bits (norms and biases stay in 32).  With any of
-    these the AdamW tensors are one ``AdamWMulti``, one launch for all types.
+    these the AdamW tensors are one ``AdamWMulti``, one launch for all types,
+    whose update rounds a little differently from ``AdamW``'s (a reciprocal, off
+    by 1e-7 of the step, for the division).  The norm takes contiguous gradients
+    only; without it Muon's may have rows further apart.
     """
 
     def __init__(self, named_params, *, compute: int = L.MUON_BF16, muon_lr: float = 3e-4,

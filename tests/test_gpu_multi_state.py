@@ -200,7 +200,7 @@ def test_a_dropped_muon_step_outlives_its_kernels(mx, explicit):
 
 def test_a_norm_past_the_largest_float(mx):
     """Finite gradients whose norm no float holds: an infinite norm, which
-    counts as not finite, and nothing of the gradients is taken."""
+    counts as not finite, and a finite bound takes nothing of the gradients."""
     g = torch.full((3000,), 3e38, device="cuda")
     for max_norm, scale in ((1.0, 0.0), (math.inf, 1.0)):
         for skip in (False, True):
