@@ -104,21 +104,25 @@ class _OnDevice:
             self._seen.add(raw)
         return raw
 
-    def _capturing(self, stream) -> bool:
+    def _here(self) -> bool:
+        """Whether this object's device is current (asked once a call)."""
+        return self.device.type != "cuda" or self.device.index == torch.cuda.current_device()
+
+    def _capturing(self, stream, here: bool) -> bool:
         """Whether the stream of a call (None: the current one) is being captured."""
-        if stream is None and self.device.index == torch.cuda.current_device():
+        if stream is None and here:
             return torch.cuda.is_current_stream_capturing()
         with torch.cuda.device(self.device):
             with torch.cuda.stream(torch.cuda.current_stream() if stream is None else _stream_object(stream)):
                 return torch.cuda.is_current_stream_capturing()
 
-    def _call(self, fn, *args) -> None:
+    def _call(self, here: bool, fn, *args) -> None:
         """Runs fn with this object's device current."""
-        if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
+        if here:
+            fn(*args)
+        else:
             with torch.cuda.device(self.device):
                 fn(*args)
-        else:
-            fn(*args)
 
 
 class StepControl:
@@ -207,8 +211,10 @@ class GradClip(_OnDevice):
         self._own(device, [tensors, chunks, self.ws, control.block])
 
     def step(self, stream=None) -> None:
-        self._call(L.muon_grad_norm, self.desc, self.max_norm, L.SKIP_NONFINITE if self.skip_nonfinite else 0,
-                   self.control.data_ptr(), self.ws.data_ptr(), self.ws.numel(), self._on(stream))
+        raw = self._on(stream)
+        self._call(self._here(), L.muon_grad_norm, self.desc, self.max_norm,
+                   L.SKIP_NONFINITE if self.skip_nonfinite else 0, self.control.data_ptr(), self.ws.data_ptr(),
+                   self.ws.numel(), raw)
 
 
 def _per_tensor(x, n, what):
@@ -316,10 +322,10 @@ class AdamWMulti(_OnDevice):
             h = self.hyper
             h.seed, h.lr, h.eps, h.beta1, h.beta2 = now
             self._now = now
-        control, raw = self.control, self._on(stream)
-        if control is None and self._capturing(stream):
+        control, raw, here = self.control, self._on(stream), self._here()
+        if control is None and self._capturing(stream, here):
             raise RuntimeError("capturing a step needs a control block: its replays would all use the same t")
-        self._call(L.muon_adamw_multi, self.desc, self.hyper, self.t + 1, None if control is None else control.data_ptr(), raw)
+        self._call(here, L.muon_adamw_multi, self.desc, self.hyper, self.t + 1, None if control is None else control.data_ptr(), raw)
         if control is None:
             self.t += 1
 

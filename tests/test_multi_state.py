@@ -291,7 +291,7 @@ def test_hyperparameters_set_between_steps_reach_the_next(monkeypatch):
     opt = mx.AdamWMulti([z(300)], [z(300)], state_bits=8, seed=3)
     seen = []
     monkeypatch.setattr(opt, "_on", lambda stream: 0)
-    monkeypatch.setattr(opt, "_capturing", lambda stream: False)
+    monkeypatch.setattr(opt, "_capturing", lambda *a: False)
     monkeypatch.setattr(mx._lib, "muon_adamw_multi", lambda desc, h, *a: seen.append((h.lr, h.beta1, h.beta2, h.eps, h.seed)))
     opt.step()
     opt.lr, opt.betas, opt.eps, opt.seed = 0.5, (0.25, 0.75), 1e-6, 9
