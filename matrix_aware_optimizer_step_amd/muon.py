@@ -92,7 +92,8 @@ def _stream_object(stream):
     stream, which needs no bookkeeping)."""
     if stream is None or hasattr(stream, "cuda_stream"):
         return stream
-    return torch.cuda.ExternalStream(int(stream))
+    # ExternalStream(0) would be some stream of torch's own
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
 
 
 def _record_on(stream, tensors) -> None:

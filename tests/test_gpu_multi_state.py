@@ -208,3 +208,27 @@ def test_a_norm_past_the_largest_float(mx):
             c.step()
             c = c.control
             assert (float(c.norm), float(c.scale), int(c.skip), int(c.step)) == (math.inf, scale, skip, not skip)
+
+
+def test_raw_handles_name_their_streams(mx):
+    side = torch.cuda.Stream()
+    for stream in (side, torch.cuda.default_stream()):
+        assert mx.muon._stream_object(stream.cuda_stream).cuda_stream == stream.cuda_stream
+
+
+def test_made_on_a_side_stream_and_stepped_on_the_default_one(mx):
+    """By its handle, 0: the memory, the side stream's, outlives the step."""
+    n = 1 << 20
+    p, twin, g = torch.ones(n, device="cuda"), torch.ones(n, device="cuda"), torch.randn(n, device="cuda")
+    mx.AdamWMulti([twin], [g], lr=1e-2).step()
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        opt = mx.AdamWMulti([p], [g], lr=1e-2)
+    torch.cuda._sleep(50_000_000)
+    opt.step(stream=0)
+    del opt
+    with torch.cuda.stream(side):
+        junk = [torch.full((n,), 1e30, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(p, twin) and len(junk) == 8

@@ -297,3 +297,12 @@ def test_hyperparameters_set_between_steps_reach_the_next(monkeypatch):
     opt.lr, opt.betas, opt.eps, opt.seed = 0.5, (0.25, 0.75), 1e-6, 9
     opt.step()
     assert seen == [(1e-3, 0.9, 0.999, 1e-8, 3), (0.5, 0.25, 0.75, 1e-6, 9)] and opt.t == 2
+
+
+def test_the_handle_zero_is_the_default_stream(monkeypatch):
+    """ExternalStream(0) is a new stream of torch's own, not the default one."""
+    default = object()
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda *a: default)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda raw, *a: ("external", raw))
+    assert mx.muon._stream_object(0) is default
+    assert mx.muon._stream_object(7) == ("external", 7)
