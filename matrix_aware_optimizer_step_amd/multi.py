@@ -63,6 +63,12 @@ def _check_apart(params, grads) -> None:
             raise ValueError("a gradient overlaps a parameter in memory")
 
 
+def _settle(device) -> None:
+    """What the current stream wrote is there: any stream may use it from here on."""
+    if device.type == "cuda":
+        torch.cuda.current_stream(device).synchronize()
+
+
 def _table(structs, device) -> torch.Tensor:
     """An array of ctypes structures in device memory."""
     return torch.from_numpy(np.frombuffer(bytes(structs), dtype=np.uint8).copy()).to(device)
@@ -84,9 +90,8 @@ class _OnDevice:
         self.device = device
         self._buffers = [b for b in buffers if b is not None]
         self._seen = set()  # streams that the allocator knows these buffers are used on
+        _settle(device)
         if device.type == "cuda":
-            # the buffers are filled: any stream may use them from here on
-            torch.cuda.current_stream(device).synchronize()
             self._seen.add(_raw_stream(device.index))
 
     def _on(self, stream):
@@ -149,8 +154,7 @@ class StepControl:
         self.scale.fill_(1.0)
         self.lr_factor.fill_(1.0)
         self.step.fill_(step)
-        if self.device.type == "cuda":
-            torch.cuda.current_stream(self.device).synchronize()
+        _settle(self.device)
 
     def data_ptr(self) -> int:
         return self.block.data_ptr()
@@ -170,6 +174,7 @@ class StepControl:
         self.step.fill_(int(state["step"]))
         self.skipped.fill_(int(state["skipped"]))
         self.lr_factor.fill_(float(state["lr_factor"]))
+        _settle(self.device)
 
 
 class GradClip(_OnDevice):
@@ -386,3 +391,4 @@ class AdamWMulti(_OnDevice):
             self.t = int(state["step"])
         else:
             self.control.step.fill_(int(state["step"]))
+        _settle(self.device)

@@ -232,3 +232,20 @@ def test_made_on_a_side_stream_and_stepped_on_the_default_one(mx):
         junk = [torch.full((n,), 1e30, device="cuda") for _ in range(8)]
     torch.cuda.synchronize()
     assert torch.equal(p, twin) and len(junk) == 8
+
+
+def test_restored_values_are_there_for_any_stream(mx):
+    """A load waits for its own device work, as the constructors do: a step on
+    another stream right after it finds what was loaded."""
+    g, side = torch.ones(300, device="cuda"), torch.cuda.Stream()
+    counts = mx.StepControl("cuda", step=41).state_dict()
+    clip = mx.GradClip([g])
+    opt = mx.AdamWMulti([torch.ones(300, device="cuda")], [g], control=clip.control)
+    saved = dict(opt.state_dict(), step=70)
+    for load, step in ((lambda: clip.control.load_state_dict(counts), 42), (lambda: opt.load_state_dict(saved), 71)):
+        torch.cuda.synchronize()
+        torch.cuda._sleep(50_000_000)
+        load()
+        clip.step(stream=side)
+        torch.cuda.synchronize()
+        assert int(clip.control.step) == step
