@@ -1,0 +1,596 @@
+"""The operators of a mixture-of-experts layer in 8-bit floating point that are measured, in their plain form and
+through the library.
+
+codes    a matrix as e4m3 codes with a scale for each block of 128 (of one row, or 128x128), in its own order, in
+         the transposed one, or both; rows gathered for experts where a case says so;
+product  the product A B^T of two such matrices, A's blocks of one row, B's of one row or 128x128; into bf16, or
+         added to an fp32 result;
+experts  the same with a matrix B for each expert: A's rows lie expert by expert, and one more product over each
+         expert's rows gives the experts' weight gradients;
+route    tokens to experts: scores (softmax or sigmoid), a bias that only chooses, groups, top-k, renormalised
+         weights, and the rows' order by expert; with its gradient;
+sums     each token's sum over its experts' rows, and the gradient of its weights.
+
+Codes are returned as codes beside their scales; the value of one is code * scale.
+"""
+
+import math
+import random
+
+import torch
+
+own = False
+
+BLOCK = 128          # elements that share a scale
+TOP = 448.0          # largest e4m3 value
+TINY = 2.0 ** -100   # a block whose largest value is below this holds zeros
+E4M3 = torch.float8_e4m3fn
+TYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def listed():
+    return [
+        # one token of a served model: latency alone
+        {"name": "route: 1 token, 6 of 64", "op": "route", "tokens": 1, "experts": 64, "k": 6, "score": "softmax",
+         "renormalize": False, "bias": False, "groups": 1, "top_groups": 1, "type": "f32", "align": 1, "back": False,
+         "masked": False},
+        # a batch of odd length under sigmoid scores, a balance bias and groups, with its gradient
+        {"name": "route: 5003 tokens, 8 of 256 in groups", "op": "route", "tokens": 5003, "experts": 256, "k": 8,
+         "score": "sigmoid", "renormalize": True, "bias": True, "groups": 8, "top_groups": 4, "type": "bf16",
+         "align": 128, "back": True, "masked": True},
+        # the tokens of one step over the 128-expert layer
+        {"name": "route: 65536 tokens, 8 of 128", "op": "route", "tokens": 65536, "experts": 128, "k": 8,
+         "score": "softmax", "renormalize": True, "bias": False, "groups": 1, "top_groups": 1, "type": "f32",
+         "align": 128, "back": True, "masked": False},
+        # activations of a few tokens being decoded, each sent to two experts
+        {"name": "codes: 17 rows of 4096, gathered", "op": "codes", "rows": 17, "cols": 4096, "block": 1, "k": 2,
+         "order": "rows", "type": "bf16"},
+        # activations of a training step, for the forward product and for the weight gradient
+        {"name": "codes: 16384 x 4096, both orders", "op": "codes", "rows": 16384, "cols": 4096, "block": 1, "k": 0,
+         "order": "both", "type": "bf16"},
+        # one token through an attention projection of the 8B-style layer
+        {"name": "product: 1 x 4096 x 4096", "op": "product", "m": 1, "n": 4096, "k": 4096, "block": 128,
+         "out": "bf16", "add": False},
+        # a weight gradient of odd sizes, added to what earlier batches left
+        {"name": "product: 1111 x 1000 x 2049, added", "op": "product", "m": 1111, "n": 1000, "k": 2049, "block": 1,
+         "out": "f32", "add": True},
+        # 8192 tokens through the gate matrix of the 8B-style layer
+        {"name": "product: 8192 x 14336 x 4096", "op": "product", "m": 8192, "n": 14336, "k": 4096, "block": 128,
+         "out": "bf16", "add": False},
+        # 32 tokens being decoded through the up matrices of the 128-expert layer
+        {"name": "experts: 32 tokens, 8 of 128", "op": "experts", "tokens": 32, "experts": 128, "k": 8, "n": 768,
+         "cols": 2048, "align": 1, "grad": False},
+        # 16384 tokens through the same matrices, and the gradient of the matrices
+        {"name": "experts: 16384 tokens, 8 of 128, and gradient", "op": "experts", "tokens": 16384, "experts": 128,
+         "k": 8, "n": 768, "cols": 2048, "align": 128, "grad": True},
+        # 32 tokens' outputs from their experts' rows
+        {"name": "sums: 32 tokens, 8 rows of 2048", "op": "sums", "tokens": 32, "k": 8, "cols": 2048, "type": "bf16",
+         "back": False},
+        # the same for a training step, and the gradient of the weights
+        {"name": "sums: 16384 tokens, 8 rows of 2048, and gradient", "op": "sums", "tokens": 16384, "k": 8,
+         "cols": 2048, "type": "bf16", "back": True},
+    ]
+
+
+def draw(rng):
+    def log(lo, hi):
+        return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+    op = rng.choice(["route", "codes", "product", "experts", "sums"])
+    if op == "route":
+        groups = rng.choice([1, 1, 2, 4, 8])
+        experts = groups * log(4, 512 // groups)
+        top = rng.randint(1, groups)
+        return {"op": op, "tokens": log(1, 30000), "experts": experts, "k": min(rng.randint(1, 12),
+                                                                               top * (experts // groups)),
+                "score": rng.choice(["softmax", "sigmoid"]), "renormalize": rng.random() < 0.6,
+                "bias": rng.random() < 0.5, "groups": groups, "top_groups": top, "type": rng.choice(["bf16", "f32"]),
+                "align": rng.choice([1, 128]), "back": rng.random() < 0.5, "masked": rng.random() < 0.3}
+    if op == "codes":
+        block = rng.choice([1, 1, 128])
+        cols = log(64, 16384)
+        rows = log(1, min(40000, (1 << 26) // cols))
+        return {"op": op, "rows": rows, "cols": cols, "block": block,
+                "k": rng.choice([0, 2, 5]) if block == 1 and rows * cols < 1 << 23 else 0,
+                "order": rng.choice(["rows", "cols", "both"]), "type": rng.choice(["bf16", "f32"])}
+    if op == "product":
+        n, k = log(64, 8192), log(64, 8192)
+        add = rng.random() < 0.3
+        return {"op": op, "m": log(1, min(16384, 480 * 10 ** 9 // (n * k))), "n": n, "k": k,
+                "block": rng.choice([1, 128, 128]), "out": "f32" if add else rng.choice(["bf16", "f32"]), "add": add}
+    if op == "experts":
+        n, cols, k = log(64, 2048), log(64, 2048), rng.randint(1, 4)
+        grad = rng.random() < 0.5
+        return {"op": op, "tokens": log(1, min(32768, 100 * 10 ** 9 // (n * cols * k))), "experts": log(4, 128),
+                "k": k, "n": n, "cols": cols, "align": 128 if grad else rng.choice([1, 128]), "grad": grad}
+    cols = log(64, 8192)
+    k = rng.randint(1, 10)
+    return {"op": op, "tokens": log(1, min(65536, (1 << 27) // (cols * k))), "k": k, "cols": cols,
+            "type": rng.choice(["bf16", "f32"]), "back": rng.random() < 0.5}
+
+
+# ------------------------------------------------------------ inputs
+
+def _up(n, to):
+    return -(-n // to) * to
+
+
+def _assign(tokens, experts, k, gen):
+    """Each token's k experts, some of them far more often than others, as a trained router's."""
+    lean = torch.randn(experts, generator=gen, device="cuda")
+    z = torch.randn(tokens, experts, generator=gen, device="cuda") + lean
+    return z.topk(k, 1)[1].to(torch.int32)
+
+
+def _order(chosen, experts, align):
+    """(row of each pair, pair of each row, first row of each expert): rows expert by expert, tokens in order."""
+    tokens, k = chosen.shape
+    flat = chosen.reshape(-1).long()
+    valid = flat >= 0
+    count = torch.zeros(experts + 1, dtype=torch.int64, device=flat.device)
+    count.index_add_(0, torch.where(valid, flat, experts), torch.ones_like(flat))
+    count = count[:experts]
+    offsets = torch.zeros(experts + 1, dtype=torch.int64, device=flat.device)
+    offsets[1:] = torch.cumsum((count + align - 1) // align * align, 0)
+    start = torch.cumsum(count, 0) - count
+    by = torch.sort(torch.where(valid, flat, experts), stable=True)[1]
+    e = flat[by]
+    place = torch.arange(flat.numel(), device=flat.device)
+    row = torch.where(e >= 0, offsets[e.clamp(min=0)] + place - start[e.clamp(min=0)], -1)
+    slots = torch.empty_like(flat)
+    slots[by] = row
+    capacity = _up(tokens * k + experts * (align - 1), align)
+    pairs = torch.full((capacity + 1,), -1, dtype=torch.int64, device=flat.device)
+    pairs[torch.where(row >= 0, row, capacity)] = torch.where(row >= 0, by, -1)
+    i32 = torch.int32
+    return slots.view(tokens, k).to(i32), pairs[:capacity].to(i32), offsets.to(i32)
+
+
+def _values(rows, cols, gen):
+    """Activations or gradients: rows of different sizes, some elements far above the rest, some rows empty."""
+    x = torch.randn(rows, cols, generator=gen, device="cuda")
+    x.mul_(torch.exp(torch.randn(rows, 1, generator=gen, device="cuda")))
+    x.mul_(torch.exp(1.5 * torch.randn(1, cols, generator=gen, device="cuda")))
+    if rows > 8:
+        x.mul_(torch.rand(rows, 1, generator=gen, device="cuda") > 0.02)
+    return x
+
+
+def _coded(x, block):
+    """Codes of a matrix with rows padded to whole blocks, and their scales, block by block."""
+    codes, scales = _encode(x, block)
+    wide = torch.zeros(*x.shape[:-1], _up(x.shape[-1], BLOCK), dtype=torch.uint8, device=x.device).view(E4M3)
+    wide[..., :x.shape[-1]] = codes
+    return wide[..., :x.shape[-1]], scales
+
+
+def prepare(case, seed):
+    gen = torch.Generator("cuda").manual_seed(int(seed))
+    st = {"case": dict(case)}
+    {"route": _make_route, "codes": _make_codes, "product": _make_product, "experts": _make_experts,
+     "sums": _make_sums}[case["op"]](case, gen, st)
+    if own and case["op"] in ("product", "experts"):  # what a program keeps: codes with their scales
+        import matrix_aware_optimizer_step_amd as mx
+        for name in ("a", "b", "at", "bt"):
+            if name in st:
+                st[name] = mx.BlockCodes(*st[name], st["block" if name == "b" else "one"])
+    return st
+
+
+def _make_route(case, gen, st):
+    T, E = case["tokens"], case["experts"]
+    dev = "cuda"
+    z = torch.randn(T, E, generator=gen, device=dev) * 1.5 + 0.5 * torch.randn(E, generator=gen, device=dev)
+    if case["masked"]:  # an expert that is switched off, and the padding of a batch
+        z[:, int(torch.randint(E, (1,), generator=gen, device=dev))] = -math.inf
+        st["mask"] = torch.rand(T, generator=gen, device=dev) > 0.1
+    st["logits"] = z.to(TYPES[case["type"]])
+    if case["bias"]:
+        st["bias"] = 0.05 * torch.randn(E, generator=gen, device=dev)
+    st["loads"] = torch.zeros(E, dtype=torch.int32, device=dev)
+    if case["back"]:
+        st["grad"] = 1e-3 * torch.randn(T, case["k"], generator=gen, device=dev)
+
+
+def _make_codes(case, gen, st):
+    rows, k = case["rows"], case["k"]
+    st["x"] = _values(rows, case["cols"], gen).to(TYPES[case["type"]])
+    if k:  # each row goes to k of 16 experts, times its weight there
+        st["pairs"] = _order(_assign(rows, 16, k, gen), 16, 1 if case["order"] == "rows" else BLOCK)[1]
+        st["weights"] = torch.rand(rows, k, generator=gen, device="cuda")
+
+
+def _make_product(case, gen, st):
+    m, n, k = case["m"], case["n"], case["k"]
+    st["one"], st["block"] = 1, case["block"]
+    st["a"] = _coded(_values(m, k, gen), 1)
+    st["b"] = _coded(0.02 * torch.randn(n, k, generator=gen, device="cuda"), case["block"])
+    if case["add"]:
+        st["out"] = torch.randn(m, n, generator=gen, device="cuda")
+
+
+def _make_experts(case, gen, st):
+    T, E, k, n, cols = (case[x] for x in ("tokens", "experts", "k", "n", "cols"))
+    _, pairs, st["offsets"] = _order(_assign(T, E, k, gen), E, case["align"])
+    rows = pairs.numel()
+    there = (pairs >= 0)[:, None]
+    st["one"], st["block"] = 1, BLOCK
+    x = _values(rows, cols, gen) * there
+    st["a"] = _coded(x, 1)
+    st["b"] = _coded(0.02 * torch.randn(E, n, cols, generator=gen, device="cuda"), BLOCK)
+    st["y"] = torch.zeros(rows, n, dtype=torch.bfloat16, device="cuda")  # rows behind the last expert stay zero
+    if case["grad"]:
+        st["bt"] = _coded(x.t().contiguous(), 1)
+        st["at"] = _coded((1e-3 * _values(rows, n, gen) * there).t().contiguous(), 1)
+        st["dw"] = 1e-2 * torch.randn(E, n, cols, generator=gen, device="cuda")
+
+
+def _make_sums(case, gen, st):
+    T, k, cols = case["tokens"], case["k"], case["cols"]
+    st["slots"], pairs, _ = _order(_assign(T, 64, k, gen), 64, 1)
+    st["y"] = _values(pairs.numel(), cols, gen).to(TYPES[case["type"]])
+    st["weights"] = torch.softmax(torch.randn(T, k, generator=gen, device="cuda"), 1)
+    if case["back"]:
+        st["grad"] = (1e-3 * torch.randn(T, cols, generator=gen, device="cuda")).to(TYPES[case["type"]])
+
+
+def run(st):
+    return (_through_library if own else _plainly)(st, st["case"])
+
+
+def _through_library(st, case):
+    import matrix_aware_optimizer_step_amd as mx
+    op = case["op"]
+    if op == "route":
+        r = mx.route(st["logits"], case["k"], bias=st.get("bias"), score=case["score"], groups=case["groups"],
+                     top_groups=case["top_groups"], renormalize=case["renormalize"], mask=st.get("mask"),
+                     align=case["align"], loads=st["loads"])
+        out = {"experts": r.experts, "weights": r.weights, "slots": r.slots, "pairs": r.pairs, "offsets": r.offsets,
+               "loads": st["loads"]}
+        if case["back"]:
+            out["grad"] = mx.route_backward(st["logits"], r, st["grad"])
+        return out
+    if op == "codes":
+        got = mx.quantize(st["x"], block_rows=case["block"], order=case["order"], pairs=st.get("pairs"),
+                          weights=st.get("weights"))
+        got = got if case["order"] == "both" else (got,)
+        return [t for q in got for t in (q.codes, q.scales)]
+    if op == "product":
+        return mx.block_matmul(st["a"], st["b"], out=st.get("out"), dtype=TYPES[case["out"]], accumulate=case["add"])
+    if op == "experts":
+        out = [mx.expert_matmul(st["a"], st["b"], st["offsets"], out=st["y"])]
+        if case["grad"]:
+            out.append(mx.expert_grad(st["at"], st["bt"], st["offsets"], out=st["dw"], accumulate=True))
+        return out
+    out = [mx.expert_sum(st["y"], st["slots"], st["weights"])]
+    if case["back"]:
+        out.append(mx.expert_dot(st["grad"], st["y"], st["slots"]))
+    return out
+
+
+# ------------------------------------------------------------ plain forms
+
+def _plainly(st, case):
+    return {"route": _plain_route, "codes": _plain_codes, "product": _plain_product, "experts": _plain_experts,
+            "sums": _plain_sums}[case["op"]](st, case)
+
+
+def _choose(st, case):
+    """Scores (in 64 bits: two may lie next to each other) and the chosen experts, best first, -1 where none is."""
+    z = st["logits"].double()
+    T, E = z.shape
+    G = case["groups"]
+    s = torch.softmax(z, 1) if case["score"] == "softmax" else torch.sigmoid(z)
+    value = s + st["bias"].double() if case["bias"] else s if G > 1 else z
+    value = torch.where(z == -math.inf, -math.inf, value)
+    if G > 1:
+        of = value.view(T, G, E // G).topk(min(2, E // G), 2)[0]
+        of = torch.where(of == -math.inf, 0.0, of).sum(2) + torch.where(of[:, :, 0] == -math.inf, -math.inf, 0.0)
+        best = torch.sort(of, dim=1, descending=True, stable=True)[1][:, :case["top_groups"]]
+        keep = torch.zeros(T, G, dtype=torch.bool, device=z.device).scatter_(1, best, True)
+        value = value.view(T, G, -1).masked_fill(~keep[:, :, None], -math.inf).view(T, E)
+    top, chosen = torch.sort(value, dim=1, descending=True, stable=True)
+    top, chosen = top[:, :case["k"]], chosen[:, :case["k"]]
+    none = top == -math.inf
+    if case["masked"]:
+        none = none | ~st["mask"][:, None]
+    return s, torch.where(none, -1, chosen)
+
+
+def _plain_route(st, case):
+    s, chosen = _choose(st, case)
+    there = chosen >= 0
+    at = chosen.clamp(min=0)
+    picked = torch.where(there, s.gather(1, at), 0.0)
+    total = picked.sum(1, keepdim=True) if case["renormalize"] else torch.ones_like(picked[:, :1])
+    w = torch.where(total > 0, picked / total, 0.0)
+    slots, pairs, offsets = _order(chosen, case["experts"], case["align"])
+    hits = torch.where(there, chosen, case["experts"]).view(-1)
+    st["loads"] += torch.bincount(hits, minlength=case["experts"] + 1)[:case["experts"]].to(torch.int32)
+    out = {"experts": chosen.to(torch.int32), "weights": w.float(), "slots": slots, "pairs": pairs,
+           "offsets": offsets, "loads": st["loads"]}
+    if case["back"]:
+        g = torch.where(there, st["grad"].double(), 0.0)
+        if case["renormalize"]:
+            g = torch.where(total > 0, (g - (g * w).sum(1, keepdim=True)) / total, 0.0)
+            g = torch.where(there, g, 0.0)
+        ds = torch.zeros_like(s).scatter_add_(1, at, g)
+        if case["score"] == "softmax":
+            dz = s * (ds - (ds * s).sum(1, keepdim=True))
+        else:
+            dz = ds * s * (1 - s)
+        out["grad"] = dz.to(st["logits"].dtype)
+    return out
+
+
+def _encode(x, block):
+    """e4m3 codes [.., rows, cols] and scales [.., blocks of columns, blocks of rows] of the last two dimensions."""
+    *lead, rows, cols = x.shape
+    x = x.float()
+    R, C = _up(rows, block), _up(cols, BLOCK)
+    wide = x if (R, C) == (rows, cols) else torch.nn.functional.pad(x, (0, C - cols, 0, R - rows))
+    wide = wide.view(*lead, R // block, block, C // BLOCK, BLOCK)
+    top = wide.abs().amax((-3, -1), keepdim=True)
+    s = torch.where(top < TINY, 0.0, top / TOP)
+    y = torch.where(top < TINY, 0.0, (wide * 0.875) / (top / 512.0))  # a quotient that is a tie stays one
+    codes = y.clamp(-TOP, TOP).to(E4M3).view(*lead, R, C)[..., :rows, :cols]
+    return codes, s.view(*lead, R // block, C // BLOCK).transpose(-1, -2).contiguous()
+
+
+def _plain_codes(st, case):
+    x = st["x"].float()
+    if case["k"]:
+        p = st["pairs"].long()
+        w = st["weights"].view(-1)[p.clamp(min=0)]
+        x = torch.where((p >= 0)[:, None], x[p.clamp(min=0) // case["k"]] * w[:, None], 0.0)
+    out = []
+    if case["order"] != "cols":
+        out += _encode(x, case["block"])
+    if case["order"] != "rows":
+        out += _encode(x.t(), case["block"])
+    return out
+
+
+def _decode(q, block, to=torch.float32):
+    """The values of codes and scales."""
+    codes, scales = q
+    rows, cols = codes.shape[-2:]
+    s = scales.to(to).transpose(-1, -2)
+    s = s.repeat_interleave(block, -2)[..., :rows, :] if block > 1 else s
+    if cols % BLOCK == 0:
+        return codes.to(to).view(*s.shape, BLOCK).mul_(s[..., None]).view(codes.shape)
+    return codes.to(to) * s.repeat_interleave(BLOCK, -1)[..., :cols]
+
+
+def _plain_product(st, case):
+    c = _decode(st["a"], 1) @ _decode(st["b"], case["block"]).t()
+    if case["add"]:
+        return st["out"].add_(c)
+    return c.to(TYPES[case["out"]])
+
+
+def _plain_experts(st, case):
+    a = _decode(st["a"], 1)
+    at = st["offsets"].tolist()
+    for e in range(case["experts"]):
+        if at[e + 1] > at[e]:
+            b = _decode((st["b"][0][e], st["b"][1][e]), BLOCK)
+            st["y"][at[e]:at[e + 1]] = a[at[e]:at[e + 1]] @ b.t()
+    if not case["grad"]:
+        return [st["y"]]
+    g, x = _decode(st["at"], 1), _decode(st["bt"], 1)
+    for e in range(case["experts"]):
+        if at[e + 1] > at[e]:
+            st["dw"][e] += g[:, at[e]:at[e + 1]] @ x[:, at[e]:at[e + 1]].t()
+    return [st["y"], st["dw"]]
+
+
+def _plain_sums(st, case):
+    rows = st["slots"].long()
+    y = st["y"].float()
+    out = [torch.stack([y[rows[:, j]] * st["weights"][:, j, None] for j in range(case["k"])]).sum(0).to(st["y"].dtype)]
+    if case["back"]:
+        g = st["grad"].float()
+        out.append(torch.stack([(y[rows[:, j]] * g).sum(1) for j in range(case["k"])], 1))
+    return out
+
+
+# ------------------------------------------------------------ the work and the exact values
+
+def work(case):
+    op = case["op"]
+    if op == "route":
+        T, E, k = case["tokens"], case["experts"], case["k"]
+        size = TYPES[case["type"]].itemsize
+        capacity = _up(T * k + E * (case["align"] - 1), case["align"])
+        nbytes, flops = T * E * size + T * k * 12 + capacity * 4 + E * 16, T * E * 8
+        if case["back"]:
+            # a renormalised softmax over the chosen needs their weights alone
+            again = 0 if case["renormalize"] and case["score"] == "softmax" else T * E * size
+            nbytes, flops = nbytes + again + T * E * size + T * k * 12, flops + T * E * 6
+        return {"bytes": nbytes, "flops": flops}
+    if op == "codes":
+        rows = case["rows"]
+        if case["k"]:
+            align = 1 if case["order"] == "rows" else BLOCK
+            rows = _up(rows * case["k"] + 16 * (align - 1), align)
+        n = rows * case["cols"]
+        orders = 2 if case["order"] == "both" else 1
+        scales = -(-n // BLOCK) * 4 // case["block"]
+        return {"bytes": case["rows"] * case["cols"] * TYPES[case["type"]].itemsize + orders * (n + scales),
+                "flops": 3 * n}
+    if op == "product":
+        m, n, k = case["m"], case["n"], case["k"]
+        scales = 4 * (m * k // BLOCK + n * k // BLOCK // case["block"])
+        return {"bytes": (m + n) * k + scales + m * n * TYPES[case["out"]].itemsize * (2 if case["add"] else 1),
+                "flops": 2 * m * n * k}
+    if op == "experts":
+        T, E, k, n, cols = (case[x] for x in ("tokens", "experts", "k", "n", "cols"))
+        rows = T * k
+        nbytes = rows * (cols * (1 + 4 / BLOCK) + 2 * n) + min(E, rows) * n * cols
+        flops = 2 * rows * n * cols
+        if case["grad"]:
+            nbytes, flops = nbytes + rows * (n + cols) * (1 + 4 / BLOCK) + 8 * E * n * cols, 2 * flops
+        return {"bytes": int(nbytes), "flops": flops}
+    T, k, cols, size = case["tokens"], case["k"], case["cols"], TYPES[case["type"]].itemsize
+    nbytes, flops = T * k * cols * size + T * cols * size + T * k * 8, 2 * T * k * cols
+    if case["back"]:
+        nbytes, flops = nbytes + T * k * cols * size + T * cols * size + T * k * 8, 2 * flops
+    return {"bytes": nbytes, "flops": flops}
+
+
+def exact(case, seed):
+    global own
+    was, own = own, False
+    try:
+        st = prepare(dict(case), seed)
+    finally:
+        own = was
+    return {"route": _exact_route, "codes": _exact_codes, "product": _exact_product, "experts": _exact_experts,
+            "sums": _exact_sums}[case["op"]](st, case)
+
+
+def _exact_route(st, case):
+    """Token by token on the host, in Python's own double precision arithmetic."""
+    T, E, k, G = case["tokens"], case["experts"], case["k"], case["groups"]
+    if T * E > 4_000_000:
+        return None
+    z = st["logits"].double().tolist()
+    bias = st["bias"].double().tolist() if case["bias"] else None
+    mask = st["mask"].tolist() if case["masked"] else [True] * T
+    grad = st["grad"].double().tolist() if case["back"] else None
+    chosen, weights, dz = [], [], []
+    for t in range(T):
+        row = z[t]
+        if case["score"] == "softmax":
+            top = max(row)
+            ex = [math.exp(x - top) for x in row]
+            total = math.fsum(ex)
+            s = [x / total for x in ex]
+        else:
+            s = [0.0 if x == -math.inf else 1 / (1 + math.exp(-x)) if x > 0 else math.exp(x) / (1 + math.exp(x))
+                 for x in row]
+        value = [s[e] + bias[e] for e in range(E)] if bias else list(s) if G > 1 else list(row)
+        open_ = [e for e in range(E) if row[e] != -math.inf]
+        if G > 1:
+            size = E // G
+            mark = []
+            for g in range(G):
+                best = sorted((value[e] for e in open_ if e // size == g), reverse=True)[:2]
+                mark.append(sum(best) if best else -math.inf)
+            kept = sorted(range(G), key=lambda g: (-mark[g], g))[:case["top_groups"]]
+            open_ = [e for e in open_ if e // size in kept]
+        mine = sorted(open_, key=lambda e: (-value[e], e))[:k] if mask[t] else []
+        total = math.fsum(s[e] for e in mine) if case["renormalize"] else 1.0
+        w = [s[e] / total if total > 0 else 0.0 for e in mine]
+        chosen.append(mine + [-1] * (k - len(mine)))
+        weights.append(w + [0.0] * (k - len(mine)))
+        if grad:
+            d = [0.0] * E
+            mean = math.fsum(a * b for a, b in zip(w, grad[t]))
+            for j, e in enumerate(mine):
+                d[e] = grad[t][j] if not case["renormalize"] else (grad[t][j] - mean) / total if total > 0 else 0.0
+            if case["score"] == "softmax":
+                mean = math.fsum(d[e] * s[e] for e in mine)
+                dz.append([s[e] * (d[e] - mean) for e in range(E)])
+            else:
+                dz.append([d[e] * s[e] * (1 - s[e]) for e in range(E)])
+    align = case["align"]
+    of = [[] for _ in range(E)]
+    for t in range(T):
+        for j in range(k):
+            if chosen[t][j] >= 0:
+                of[chosen[t][j]].append(t * k + j)
+    offsets, pairs, slots = [0], [], [-1] * (T * k)
+    for e in range(E):
+        for i, p in enumerate(of[e]):
+            slots[p] = offsets[e] + i
+        pairs += of[e] + [-1] * (-len(of[e]) % align)
+        offsets.append(len(pairs))
+    pairs += [-1] * (_up(T * k + E * (align - 1), align) - len(pairs))
+
+    def whole(x):
+        return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+    out = {"experts": whole(chosen), "weights": torch.tensor(weights, dtype=torch.float64, device="cuda"),
+           "slots": whole(slots).view(T, k), "pairs": whole(pairs), "offsets": whole(offsets),
+           "loads": whole([len(x) for x in of])}
+    if grad:
+        out["grad"] = torch.tensor(dz, dtype=torch.float64, device="cuda")
+    return out
+
+
+def _exact_codes(st, case):
+    x = st["x"].to(torch.float64)
+    if case["k"]:
+        p = st["pairs"].long()
+        src = torch.div(p, case["k"], rounding_mode="floor")
+        x = torch.cat([x, x.new_zeros(1, x.shape[1])])[src]  # the last row for -1
+        x = x * torch.cat([st["weights"].double().reshape(-1), x.new_zeros(1)])[p][:, None]
+    out = []
+    for name, m in (("rows", x), ("cols", x.t())):
+        if case["order"] not in (name, "both"):
+            continue
+        codes = torch.zeros_like(m)
+        step = case["block"]
+        nr, nc = -(-m.shape[0] // step), -(-m.shape[1] // BLOCK)
+        scales = torch.zeros(nc, nr, dtype=torch.float64, device=m.device)
+        for c in range(nc):
+            part = m[:, c * BLOCK:(c + 1) * BLOCK]
+            top = part.abs().amax(1)
+            if step > 1:
+                top = torch.nn.functional.pad(top, (0, nr * step - top.numel())).view(nr, step).amax(1)
+            top = torch.where(top < TINY, 0.0, top)
+            scales[c] = top / TOP
+            unit = torch.repeat_interleave(scales[c], step)[:m.shape[0], None]
+            y = torch.where(unit > 0, part / unit, 0.0)
+            quantum = torch.ldexp(torch.ones_like(y), (torch.frexp(y.abs())[1] - 1).clamp(min=-6) - 3)
+            codes[:, c * BLOCK:(c + 1) * BLOCK] = torch.round(y / quantum) * quantum
+        out += [codes, scales]
+    return out
+
+
+def _exact_values(q, block):
+    codes, scales = q
+    x = codes.to(torch.float64)
+    for c in range(scales.shape[0]):
+        s = torch.repeat_interleave(scales[c].to(torch.float64), block)[:x.shape[0]]
+        x[:, c * BLOCK:(c + 1) * BLOCK] *= s[:, None]
+    return x
+
+
+def _exact_product(st, case):
+    c = _exact_values(st["a"], 1).matmul(_exact_values(st["b"], case["block"]).t().contiguous())
+    return c + st["out"].to(torch.float64) if case["add"] else c
+
+
+def _exact_experts(st, case):
+    y, at = st["y"].to(torch.float64), st["offsets"].tolist()
+    a = _exact_values(st["a"], 1)
+    for e in range(case["experts"]):
+        lo, hi = at[e], at[e + 1]
+        if hi > lo:
+            b = _exact_values((st["b"][0][e], st["b"][1][e]), BLOCK)
+            y[lo:hi] = torch.matmul(a[lo:hi], b.t().contiguous())
+    if not case["grad"]:
+        return [y]
+    del a
+    dw = st["dw"].to(torch.float64)
+    g, x = _exact_values(st["at"], 1), _exact_values(st["bt"], 1)
+    for e in range(case["experts"]):
+        lo, hi = at[e], at[e + 1]
+        if hi > lo:
+            dw[e] += torch.matmul(g[:, lo:hi].contiguous(), x[:, lo:hi].t().contiguous())
+    return [y, dw]
+
+
+def _exact_sums(st, case):
+    T, k = case["tokens"], case["k"]
+    total = torch.zeros(T, case["cols"], dtype=torch.float64, device="cuda")
+    dots = torch.zeros(T, k, dtype=torch.float64, device="cuda")
+    for j in range(k):
+        y = st["y"].index_select(0, st["slots"][:, j]).to(torch.float64)
+        total.addcmul_(y, st["weights"][:, j:j + 1].to(torch.float64))
+        if case["back"]:
+            dots[:, j] = torch.linalg.vecdot(y, st["grad"].to(torch.float64))
+    return [total, dots] if case["back"] else [total]
