@@ -542,8 +542,8 @@ def _exact_codes(st, case):
                 top = torch.nn.functional.pad(top, (0, nr * step - top.numel())).view(nr, step).amax(1)
             top = torch.where(top < TINY, 0.0, top)
             scales[c] = top / TOP
-            unit = torch.repeat_interleave(scales[c], step)[:m.shape[0], None]
-            y = torch.where(unit > 0, part / unit, 0.0)
+            most = torch.repeat_interleave(top, step)[:m.shape[0], None]
+            y = torch.where(most > 0, part * TOP / most, 0.0)  # in this order a tie stays one
             quantum = torch.ldexp(torch.ones_like(y), (torch.frexp(y.abs())[1] - 1).clamp(min=-6) - 3)
             codes[:, c * BLOCK:(c + 1) * BLOCK] = torch.round(y / quantum) * quantum
         out += [codes, scales]
