@@ -659,6 +659,100 @@ const char* muon_last_error(void);
 /* MUON355_ABI_VERSION of the loaded library. */
 int muon_abi_version(void);
 
+/* ------------------------------------------------------------------------
+ * Expert layers in 8-bit floating point.
+ *
+ * What the layers whose matrices the step updates are run with, forward and
+ * backward: a weight or an activation as 8-bit codes, the products of such
+ * codes (of one matrix, of every expert's, and of the experts' weight
+ * gradients, added to the buffers that the step reads), the routing of tokens
+ * to experts with the bias that balances it, and the tokens' sums over their
+ * experts.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * A matrix of e4m3 codes (OCP: 4 exponent and 3 mantissa bits, largest value
+ * 448) with an fp32 scale for each block of 128 columns of one row
+ * (block_rows 1) or of 128 rows (block_rows 128):
+ *
+ *   value(r, c) = code(r, c) * scales[(c / 128) * scale_ld + r / block_rows]
+ *
+ * The scales of one block column lie together, as a product reads them.
+ * Rows are padded to whole blocks: ld >= cols rounded up to 128, and the codes
+ * behind a row's last column, up to the end of its last block, are zero.
+ * Everything that writes codes here writes these zeros; products read them.
+ */
+#define MUON_CODE_BLOCK 128
+
+typedef struct muon_codes {
+  void* codes;          /* matrix i at codes + i*stride bytes, 16-byte aligned */
+  float* scales;        /* matrix i at scales + i*scale_stride floats */
+  int64_t stride;       /* bytes between matrices, a multiple of 16 */
+  int64_t scale_stride; /* floats between matrices */
+  int64_t count;        /* number of matrices, 1 .. 65535 */
+  int64_t rows;         /* 1 .. 2^31 - 128 */
+  int64_t cols;         /* 1 .. 2^31 - 128 */
+  int64_t ld;           /* bytes between rows, a multiple of 16, below 2^31 */
+  int64_t scale_ld;     /* floats between block columns, >= rows / block_rows rounded up */
+  int32_t block_rows;   /* 1 or MUON_CODE_BLOCK */
+  int32_t reserved;     /* must be 0 */
+} muon_codes_t;
+
+/*
+ * A matrix, or a batch of them, as codes in its own order (q), as codes of its
+ * transpose (qt), or both from one pass over it:
+ *
+ *   scale = max|x| / 448,   code = round(448 * x / max|x|)   over a block,
+ *
+ * to nearest, ties to even; the quotient is correctly rounded before.  A block
+ * whose largest magnitude is below 2^-100 gets scale 0 and codes 0.  A block
+ * that holds a NaN or an infinity gets a scale that is not finite, and every
+ * value of it is NaN: products pass it on.
+ *
+ * x     : BF16 or F32, any alignment of its elements; read only.
+ * pairs : NULL, or device int32[n]: row i of the codes is row pairs[i] / k of x,
+ *         times weights[pairs[i]] when `weights` is not NULL, and zeros where
+ *         pairs[i] < 0 (rows sent to experts, as muon_route lists them).
+ *         x->count must be 1, block_rows 1; q has n rows and qt n columns.
+ *         A pair behind x's last row gives zeros too.  Without pairs, k is 1
+ *         and weights NULL.
+ * q, qt : either may be NULL; equal counts and block_rows.
+ */
+muon_status_t muon_block_quantize(const muon_batch_t* x, const int32_t* pairs, const float* weights, int64_t k,
+                                  const muon_codes_t* q, const muon_codes_t* qt, void* stream);
+
+/*
+ * Products C = A * B^T over codes: A has M rows, B has N, both K columns; C is
+ * M x N, row-major, BF16 or F32.  A's blocks have one row, B's one or 128.
+ * Sums over a block of 128 are fp32, each is multiplied by the two scales in
+ * fp32 and added to an fp32 sum in the order of the blocks.
+ *
+ * MUON_PRODUCT_BATCH : count products; a, b and c have equal counts; offsets
+ *   is NULL.
+ * MUON_PRODUCT_ROWS  : b holds E matrices, a and c one.  Rows offsets[e] ..
+ *   offsets[e+1]-1 of C are those rows of A times B[e]^T.  Rows behind
+ *   offsets[E] are left as they were.
+ * MUON_PRODUCT_REDUCE: c holds E matrices, a and b one.  C[e] is the product
+ *   over columns offsets[e] .. offsets[e+1]-1 alone; the offsets are multiples
+ *   of 128 (the last one may be K).  An expert without columns gets zeros.
+ *   A and B are codes of transposes here: C is a gradient of weights,
+ *   rows(A) = outputs, rows(B) = inputs, columns = rows of activations.
+ *
+ * offsets   : device int32[E+1], ascending, in [0, M] or [0, K].  Values
+ *             outside are taken as the nearest bound.
+ * accumulate: 1: C += the product (F32 only); an expert without columns is
+ *             left as it was.
+ * C must not overlap A or B.
+ */
+typedef enum muon_product {
+  MUON_PRODUCT_BATCH = 0,
+  MUON_PRODUCT_ROWS = 1,
+  MUON_PRODUCT_REDUCE = 2
+} muon_product_t;
+
+muon_status_t muon_block_matmul(const muon_codes_t* a, const muon_codes_t* b, const muon_batch_t* c,
+                                const int32_t* offsets, int32_t product, int32_t accumulate, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

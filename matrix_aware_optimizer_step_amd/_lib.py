@@ -33,13 +33,15 @@ EXPORTED = ("muon_abi_version", "muon_last_error", "muon_status_string", "muon_m
             "soap_statistics_grouped", "soap_qr_workspace", "soap_qr", "soap_refresh_workspace", "soap_refresh",
             "soap_refresh_grouped_workspace", "soap_refresh_grouped",
             "soap_precondition_workspace", "soap_precondition", "soap_precondition_grouped_workspace",
-            "soap_precondition_grouped")
+            "soap_precondition_grouped", "muon_block_quantize", "muon_block_matmul")
 
 ADAMW_CHUNK = 4096  # MUON_ADAMW_CHUNK
 GRAD_CHUNK = 16384  # MUON_GRAD_CHUNK
 PARAM_CHUNK = 4096  # MUON_PARAM_CHUNK
 STATE_BLOCK = 256   # MUON_STATE_BLOCK
 SKIP_NONFINITE = 1  # MUON_SKIP_NONFINITE
+CODE_BLOCK = 128    # MUON_CODE_BLOCK
+PRODUCT_BATCH, PRODUCT_ROWS, PRODUCT_REDUCE = 0, 1, 2  # muon_product_t
 
 
 class MuonError(RuntimeError):
@@ -96,6 +98,13 @@ class MuonAdamWHyper(ctypes.Structure):
                 ("eps", ctypes.c_double), ("seed", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
 
 
+class MuonCodes(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("stride", ctypes.c_int64),
+                ("scale_stride", ctypes.c_int64), ("count", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("ld", ctypes.c_int64), ("scale_ld", ctypes.c_int64),
+                ("block_rows", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 _lib = None
 
 
@@ -108,6 +117,7 @@ def load() -> ctypes.CDLL:
                            "(the Muon path has no CPU fallback)")
     lib = ctypes.CDLL(LIB_PATH)
     P = ctypes.POINTER(MuonBatch)
+    Q = ctypes.POINTER(MuonCodes)
     vp, f32, i32, i64, sz = ctypes.c_void_p, ctypes.c_float, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     sig = {
         "muon_abi_version": (ctypes.c_int, []),
@@ -163,6 +173,8 @@ def load() -> ctypes.CDLL:
                                                      ctypes.POINTER(i64)]),
         "soap_precondition_grouped": (ctypes.c_int, [ctypes.c_int, P, ctypes.POINTER(P), ctypes.POINTER(P), P, P, P,
                                                      i64, f32, f32, f32, vp, sz, vp]),
+        "muon_block_quantize": (ctypes.c_int, [P, vp, vp, i64, Q, Q, vp]),
+        "muon_block_matmul": (ctypes.c_int, [Q, Q, P, vp, i32, i32, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -445,3 +457,15 @@ def soap_precondition_grouped(grads, QLs, QRs, mbars, vbars, dirs, step: int, be
     st = load().soap_precondition_grouped(n, vec(grads), arr(QLs), arr(QRs), vec(mbars), vec(vbars), vec(dirs), step,
                                           beta1, beta2, eps, workspace_ptr, ws_bytes, stream)
     _check(st, "soap_precondition_grouped")
+
+
+def muon_block_quantize(x: MuonBatch, pairs_ptr: int | None, weights_ptr: int | None, k: int, q: MuonCodes | None,
+                        qt: MuonCodes | None, stream: int) -> None:
+    _check(load().muon_block_quantize(_ref(x), pairs_ptr, weights_ptr, k, _ref(q), _ref(qt), stream),
+           "muon_block_quantize")
+
+
+def muon_block_matmul(a: MuonCodes, b: MuonCodes, c: MuonBatch, offsets_ptr: int | None, product: int,
+                      accumulate: int, stream: int) -> None:
+    _check(load().muon_block_matmul(_ref(a), _ref(b), _ref(c), offsets_ptr, product, accumulate, stream),
+           "muon_block_matmul")

@@ -1,0 +1,332 @@
+// Products of 8-bit block codes on CDNA4 matrix cores (gfx950).
+//
+//   C[m][n] = sum over blocks b of 128 columns:
+//             sa[b][m] * sb[b][n or n/128] * (sum over k in b of A[m][k] * B[n][k])
+//
+// v_mfma_f32_16x16x128_f8f6f4 sums one block of a 16x16 tile in fp32, exactly
+// one block's worth, so a scale meets each partial sum once, in an fp32
+// multiply-add into the running sums.  That is one vector instruction per
+// output element and block (two where B has a scale for each row), half the
+// (the whole) time of the matrix instructions, which run beside them.
+//
+// B's rows are the instruction's rows and A's rows its columns, and the row
+// that a lane's four results belong to is chosen freely when B is read from
+// LDS: a lane ends up with one row m and 4*NT consecutive columns n of the
+// result, which it stores in whole 16-byte pieces without a detour.
+//
+// A workgroup computes a tile of BM x BN from k-tiles of one block, double
+// buffered in LDS by global_load_lds_dwordx4.  Rows are 128 bytes; the 16-byte
+// chunks of a row are XOR-permuted (a_swizzle, b_swizzle) so that the 16 rows
+// of a fragment's read cover all 64 banks.
+
+#include "block_internal.h"
+
+namespace muon {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ uint32_t lds_address(const void* l) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)(l)));
+}
+// Global -> LDS copies of 16 or 4 bytes per lane: lane i's bytes at base + off
+// land at LDS address l + 16 i (4 i).  Inline asm, as the compiler would
+// otherwise wait for them at LDS reads that have nothing to do with them; the
+// kernels order them with wait_all() and a barrier.
+__device__ __forceinline__ void copy16(const char* base, uint32_t off, uint32_t l) {
+  asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(__builtin_amdgcn_readfirstlane(l))
+               : "memory");
+}
+__device__ __forceinline__ void copy4(const char* base, uint32_t off, uint32_t l) {
+  asm volatile("global_load_lds_dword %0, %1" ::"v"(off), "s"(base), "{m0}"(__builtin_amdgcn_readfirstlane(l))
+               : "memory");
+}
+// All vector loads and LDS accesses of this wave are done, then the barrier.
+__device__ __forceinline__ void wait_all() {
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+__device__ __forceinline__ f32x4 mma(const i32x8& a, const i32x8& b) {
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, zero, 0, 0, 0, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
+}
+
+// N consecutive results of a row, `left` of them inside the matrix.
+template <int N>
+__device__ __forceinline__ void store_row(const MatBatch& c, char* row, int64_t col, int left, const float* v,
+                                          int accumulate) {
+  if (left <= 0) return;
+  if (c.dtype) {
+    char* p = row + col * 2;
+    if (left >= N && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+#pragma unroll
+      for (int k = 0; k < N; k += 8) {
+        uint4 u;
+        u.x = bf16_pair(v[k], v[k + 1]);
+        u.y = bf16_pair(v[k + 2], v[k + 3]);
+        u.z = bf16_pair(v[k + 4], v[k + 5]);
+        u.w = bf16_pair(v[k + 6], v[k + 7]);
+        *reinterpret_cast<uint4*>(p + 2 * k) = u;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (k < left) reinterpret_cast<__bf16*>(p)[k] = static_cast<__bf16>(v[k]);
+    }
+    return;
+  }
+  float* p = reinterpret_cast<float*>(row) + col;
+  if (left >= N && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+#pragma unroll
+    for (int k = 0; k < N; k += 4) {
+      float4 u = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+      if (accumulate) {
+        const float4 o = *reinterpret_cast<const float4*>(p + k);
+        u = make_float4(o.x + u.x, o.y + u.y, o.z + u.z, o.w + u.w);
+      }
+      *reinterpret_cast<float4*>(p + k) = u;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (k < left) p[k] = accumulate ? p[k] + v[k] : v[k];
+  }
+}
+
+// Row offset i of the list, kept inside [0, most] and above the one before.
+__device__ __forceinline__ int offset_at(const int32_t* offsets, int64_t i, int most) {
+  const int o = offsets[i];
+  return o < 0 ? 0 : o > most ? most : o;
+}
+
+// Which expert and which rows the m-tile `tile` of a list of segments is:
+// every segment is cut into tiles of BM rows by itself.  A wave scans the
+// segments, 64 at a time.  False: behind the last tile.
+template <int BM>
+__device__ __forceinline__ bool find_rows(const BlockGemmArgs& a, int tile, int& expert, int& first, int& end) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int64_t e0 = 0; e0 < a.count; e0 += 64) {
+    const int64_t e = e0 + lane;
+    int lo = 0, hi = 0;
+    if (e < a.count) {
+      lo = offset_at(a.offsets, e, a.M);
+      hi = offset_at(a.offsets, e + 1, a.M);
+    }
+    const int mine = hi > lo ? (hi - lo + BM - 1) / BM : 0;
+    int sum = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int x = __shfl_up(sum, d);
+      if (lane >= d) sum += x;
+    }
+    const int start = before + sum - mine;
+    const uint64_t hit = __ballot(tile >= start && tile < start + mine);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      expert = static_cast<int>(e0) + l;
+      first = __builtin_amdgcn_readlane(lo, l) + (tile - __builtin_amdgcn_readlane(start, l)) * BM;
+      end = __builtin_amdgcn_readlane(hi, l);
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(sum, 63);
+  }
+  return false;
+}
+
+constexpr int kGroupRows = 8;  // tile rows that are walked together, column by column
+
+// BM x BN tile, WM x WN waves of (BM/WM) x (BN/WN) each.  SB: B has a scale
+// for each row.
+template <int BM, int BN, int WM, int WN, bool SB>
+__global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmArgs a) {
+  constexpr int NW = WM * WN;
+  constexpr int MT = BM / WM / 16, NT = BN / WN / 16;  // 16x16 tiles of a wave
+  constexpr int SPAN = 4 * NT;                         // consecutive columns of a lane
+  constexpr int OPB = BM * 128;
+  constexpr int SCALES = (BM + BN) * 128;              // scales of A's rows, then of B's
+  constexpr int STAGE = SCALES + (BM + (SB ? BN : 0)) * 4;
+  constexpr int IA = BM / 8 / NW, IB = BN / 8 / NW;    // copies of 8 rows, per wave
+  static_assert(IA * 8 * NW == BM && IB * 8 * NW == BN && 2 * STAGE <= 160 * 1024, "tile");
+  static_assert(BM / 64 + (SB ? BN / 64 : 0) <= 2 * NW && BN / WN <= 128, "scale copies");
+  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+
+  // workgroup ids reach the 8 XCDs round-robin: each XCD takes a contiguous
+  // range of the tiles, so that tiles that share rows share its L2
+  const int total = static_cast<int>(a.total_tiles);
+  const int xcd = blockIdx.x & 7;
+  int t = (blockIdx.x >> 3) + xcd * (total >> 3) + (xcd < (total & 7) ? xcd : (total & 7));
+  const int per = a.tiles_m * a.tiles_n;
+  const int mat = t / per;
+  t -= mat * per;
+  const int span = kGroupRows * a.tiles_n;
+  const int grp = t / span, in = t - grp * span;
+  const int high = min(kGroupRows, a.tiles_m - grp * kGroupRows);
+  const int tj = in / high, ti = grp * kGroupRows + in - tj * high;
+
+  // the tile's rows [m0, m1) of A, the matrix of B and C, and its blocks of k
+  int m0 = ti * BM, m1 = a.M, which = mat, kb0 = 0, nk = (a.K + 127) >> 7;
+  if (a.mode == GEMM_ROWS) {
+    if (!find_rows<BM>(a, ti, which, m0, m1)) return;
+  } else if (a.mode == GEMM_REDUCE) {
+    const int lo = offset_at(a.offsets, mat, a.K) >> 7, hi = (offset_at(a.offsets, mat + 1, a.K) + 127) >> 7;
+    kb0 = lo;
+    nk = hi > lo ? hi - lo : 0;
+    if (nk == 0 && a.accumulate) return;
+  }
+  const int n0 = tj * BN;
+  const int64_t amat = a.mode == GEMM_BATCH ? mat : 0, bmat = a.mode == GEMM_REDUCE ? 0 : which;
+  const char* A = a.a.codes + amat * a.a.stride + m0 * a.a.ld + static_cast<int64_t>(kb0) * 128;
+  const char* B = a.b.codes + bmat * a.b.stride + n0 * a.b.ld + static_cast<int64_t>(kb0) * 128;
+  const float* SA = a.a.scales + amat * a.a.scale_stride + kb0 * a.a.scale_ld + m0;
+  const float* SB0 = a.b.scales + bmat * a.b.scale_stride + kb0 * a.b.scale_ld;
+
+  // copies: lane l of an instruction fills slot l % 8 of row l / 8; rows behind
+  // the matrix repeat its last one (their results are not stored)
+  uint32_t ofs_a[IA], ofs_b[IB];
+#pragma unroll
+  for (int r = 0; r < IA; ++r) {
+    const int row = (wave * IA + r) * 8 + (lane >> 3);
+    const int c = (lane & 7) ^ ((row >> 1) & 7);
+    ofs_a[r] = static_cast<uint32_t>(min(row, a.M - 1 - m0)) * static_cast<uint32_t>(a.a.ld) + c * 16;
+  }
+#pragma unroll
+  for (int r = 0; r < IB; ++r) {
+    const int row = (wave * IB + r) * 8 + (lane >> 3);
+    const int c = (lane & 7) ^ (((row >> 1) & 1) | ((row / SPAN & 3) << 1));
+    ofs_b[r] = static_cast<uint32_t>(min(row, a.N - 1 - n0)) * static_cast<uint32_t>(a.b.ld) + c * 16;
+  }
+  const uint32_t lds0 = lds_address(smem);
+  auto copy = [&](int kt, int stage) {
+    const char* pa = A + static_cast<int64_t>(kt) * 128;
+    const char* pb = B + static_cast<int64_t>(kt) * 128;
+    const uint32_t l = lds0 + stage * STAGE;
+#pragma unroll
+    for (int r = 0; r < IA; ++r) copy16(pa, ofs_a[r], l + (wave * IA + r) * 1024);
+#pragma unroll
+    for (int r = 0; r < IB; ++r) copy16(pb, ofs_b[r], l + OPB + (wave * IB + r) * 1024);
+    for (int s = wave; s < BM / 64 + (SB ? BN / 64 : 0); s += NW) {
+      if (s < BM / 64) {
+        copy4(reinterpret_cast<const char*>(SA + kt * a.a.scale_ld),
+              4 * static_cast<uint32_t>(min(s * 64 + lane, a.M - 1 - m0)), l + SCALES + s * 256);
+      } else {
+        const int row = (s - BM / 64) * 64 + lane;
+        copy4(reinterpret_cast<const char*>(SB0 + kt * a.b.scale_ld + n0),
+              4 * static_cast<uint32_t>(min(row, a.N - 1 - n0)), l + SCALES + s * 256);
+      }
+    }
+  };
+
+  const int wm = wave / WN, wn = wave - wm * WN;
+  const int l15 = lane & 15, g = lane >> 4;
+  const int arow = wm * (BM / WM) + l15;
+  const int brow = wn * (BN / WN) + (l15 >> 2) * SPAN + (l15 & 3);  // tile j adds 4 j
+  const int bswz = (((brow >> 1) & 1) | ((brow / SPAN & 3) << 1));
+  const int sbn = min(n0 + wn * (BN / WN), a.N - 1) >> 7;  // block row of B, square blocks (from B's first one)
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+
+  auto fragment = [&](const char* p, int swz) {
+    const i32x4 lo = *reinterpret_cast<const i32x4*>(p + ((g ^ swz) << 4));
+    const i32x4 hi = *reinterpret_cast<const i32x4*>(p + (((g + 4) ^ swz) << 4));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  };
+
+  if (nk > 0) copy(0, 0);
+  float sq = 0.0f;
+  if (!SB && nk > 0) sq = SB0[sbn];
+  wait_all();
+  for (int kt = 0; kt < nk; ++kt) {
+    const char* s = smem + (kt & 1) * STAGE;
+    const float sb = sq;
+    if (kt + 1 < nk) {
+      copy(kt + 1, (kt + 1) & 1);
+      if (!SB) sq = SB0[(kt + 1) * a.b.scale_ld + sbn];
+    }
+    i32x8 fa[MT];
+    float sa[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      fa[i] = fragment(s + (arow + i * 16) * 128, (l15 >> 1) & 7);
+      sa[i] = *reinterpret_cast<const float*>(s + SCALES + (arow + i * 16) * 4);
+      if (!SB) sa[i] *= sb;
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const i32x8 fb = fragment(s + OPB + (brow + 4 * j) * 128, bswz);
+      f32x4 p[MT];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) p[i] = mma(fb, fa[i]);
+      f32x4 w;
+      if (SB)
+        w = *reinterpret_cast<const f32x4*>(s + SCALES + BM * 4 + (wn * (BN / WN) + g * SPAN + 4 * j) * 4);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[i][j][r] = __builtin_fmaf(SB ? p[i][r] * w[r] : p[i][r], sa[i], acc[i][j][r]);
+    }
+    wait_all();
+  }
+
+  const int64_t cmat = a.mode == GEMM_ROWS ? 0 : mat;
+  char* C = a.c.ptrs ? static_cast<char*>(a.c.ptrs[cmat]) : a.c.base + cmat * a.c.stride_bytes;
+  const int n = n0 + wn * (BN / WN) + g * SPAN;
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int m = m0 + arow + i * 16;
+    if (m >= m1) continue;
+    float v[SPAN];
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[4 * j + r] = acc[i][j][r];
+    store_row<SPAN>(a.c, C + m * a.c.ld * (a.c.dtype ? 2 : 4), n, a.N - n, v, a.accumulate);
+  }
+}
+
+// Tiles of a launch: in ROWS every segment may end inside a tile.
+int64_t count_tiles(BlockGemmArgs& a, int bm, int bn) {
+  a.tiles_n = (a.N + bn - 1) / bn;
+  a.tiles_m = a.mode == GEMM_ROWS ? static_cast<int32_t>(a.M / bm + a.count) : (a.M + bm - 1) / bm;
+  a.total_tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n * (a.mode == GEMM_ROWS ? 1 : a.count);
+  return a.total_tiles;
+}
+
+}  // namespace
+
+hipError_t launch_block_gemm(const BlockGemmArgs& args, hipStream_t s) {
+  BlockGemmArgs a = args;
+  const int64_t n = count_tiles(a, 256, 256);
+  if (n >= 200) {
+    const uint32_t g = static_cast<uint32_t>(n);
+    if (a.square) {
+      gemm_kernel<256, 256, 4, 2, false><<<g, 512, 0, s>>>(a);
+    } else {
+      gemm_kernel<256, 256, 4, 2, true><<<g, 512, 0, s>>>(a);
+    }
+  } else {
+    const uint32_t g = static_cast<uint32_t>(count_tiles(a, 128, 128));
+    if (a.square) {
+      gemm_kernel<128, 128, 2, 2, false><<<g, 256, 0, s>>>(a);
+    } else {
+      gemm_kernel<128, 128, 2, 2, true><<<g, 256, 0, s>>>(a);
+    }
+  }
+  return hipGetLastError();
+}
+
+}  // namespace muon
