@@ -753,6 +753,111 @@ typedef enum muon_product {
 muon_status_t muon_block_matmul(const muon_codes_t* a, const muon_codes_t* b, const muon_batch_t* c,
                                 const int32_t* offsets, int32_t product, int32_t accumulate, void* stream);
 
+/*
+ * Routing of tokens to experts.  With the logits z of a token:
+ *
+ *   s = softmax(z) or sigmoid(z) over the experts;  key = s + bias
+ *   the experts are `groups` runs of equal length; a group's mark is the sum of
+ *   its group_best (1 or 2) largest keys; the top_groups best groups stay
+ *   chosen = the k largest keys of the groups that stay, best first
+ *   w_j = scale * s_j, over the sum of the chosen ones' s if `renormalize`
+ *         (0 where that sum is 0)
+ *
+ * The bias chooses and does not weigh.  Of equal keys or marks the lower index
+ * comes first.  Keys are compared as if computed exactly, to fp64's rounding;
+ * without a bias, in one group or with group_best 1, they are the logits.
+ * A logit of -inf takes its expert out; where fewer than k are left the rest
+ * of chosen is -1 with weight 0, and so is a token whose mask is 0.  A token
+ * with a NaN (or +inf under softmax, or with a NaN bias) goes nowhere: -1, and its weights are
+ * NaN, which muon_expert_sum passes on.
+ *
+ * The order of the (token, j) pairs by expert: expert e's rows are
+ * offsets[e] .. offsets[e+1]-1, in the order of the tokens, each expert's rounded up
+ * to a multiple of `align` rows (MUON_CODE_BLOCK where weight gradients are
+ * taken over them).  slots[t*k+j] is the pair's row or -1, pairs[row] is t*k+j
+ * or -1: between an expert's last pair and the next one's first row, and
+ * behind offsets[experts].  pairs has muon_route_capacity() elements.
+ */
+#define MUON_MAX_EXPERTS 512
+#define MUON_MAX_CHOSEN 16
+#define MUON_MAX_EXPERT_GROUPS 32
+
+typedef enum muon_score { MUON_SCORE_SOFTMAX = 0, MUON_SCORE_SIGMOID = 1 } muon_score_t;
+
+typedef struct muon_route {
+  const void* logits;   /* [tokens, experts], aligned to its element size */
+  int64_t ld;           /* elements between tokens, >= experts */
+  int64_t tokens;       /* >= 1; tokens * k < 2^31 */
+  int64_t experts;      /* 1 .. MUON_MAX_EXPERTS */
+  int64_t k;            /* 1 .. MUON_MAX_CHOSEN, <= experts of top_groups groups */
+  int32_t dtype;        /* muon_dtype_t of the logits */
+  int32_t score;        /* muon_score_t */
+  int32_t renormalize;  /* 0 or 1 */
+  int32_t groups;       /* 1 .. MUON_MAX_EXPERT_GROUPS, divides experts */
+  int32_t top_groups;   /* 1 .. groups */
+  int32_t group_best;   /* 1 or 2 */
+  int32_t align;        /* 1 .. 65536 */
+  float scale;          /* finite */
+} muon_route_t;
+
+/* Rows of the order: tokens*k + experts*(align-1), rounded up to a multiple of
+ * align; 0 for arguments that muon_route refuses. */
+int64_t muon_route_capacity(int64_t tokens, int64_t experts, int64_t k, int64_t align);
+/* Bytes of device workspace of muon_route. */
+size_t muon_route_workspace(int64_t tokens, int64_t experts);
+
+/*
+ * bias   : device float[experts] or NULL.  mask: device uint8[tokens] or NULL.
+ * chosen : int32[tokens*k], weights: float[tokens*k], written.
+ * slots  : int32[tokens*k], pairs: int32[capacity], offsets: int32[experts+1],
+ *          written; all three or none (NULL).
+ * loads  : int32[experts] or NULL: each expert's pairs are added (micro-batches
+ *          of a step add up; the caller keeps the sums below 2^31).
+ * workspace: at least muon_route_workspace bytes, 16-byte aligned; holds
+ *          temporaries of this call alone.
+ */
+muon_status_t muon_route(const muon_route_t* r, const float* bias, const uint8_t* mask, int32_t* chosen,
+                         float* weights, int32_t* slots, int32_t* pairs, int32_t* offsets, int32_t* loads,
+                         void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of the logits from the gradient of the weights, with chosen and
+ * weights as muon_route wrote them for the same description (its groups, bias
+ * and mask only chose).  grad_logits: [tokens, experts] of the logits' type,
+ * ld_grad elements between tokens, written whole.  A NaN in a token's weights or their
+ * gradients makes its row NaN.
+ */
+muon_status_t muon_route_backward(const muon_route_t* r, const int32_t* chosen, const float* weights,
+                                  const float* grad_weights, void* grad_logits, int64_t ld_grad, void* stream);
+
+/*
+ * The bias's own step, once an optimizer step: bias[e] += rate where the
+ * expert's load lies below the mean, -= rate where it lies above (compared in
+ * integers), and the loads start again from 0.  With several GPUs the loads
+ * are summed over them before.  With `control` a step that skips leaves the
+ * bias as it is (the loads start again all the same).  rate: finite, >= 0.
+ */
+muon_status_t muon_balance_update(float* bias, int32_t* loads, int64_t experts, float rate,
+                                  const muon_step_control_t* control, void* stream);
+
+/*
+ * Each token's sum over its experts' rows: out[t] = sum over j, in its order,
+ * of weights[t*k+j] * y[slots[t*k+j]], in fp32, rounded once (BF16 or F32,
+ * whichever y has).  A slot that is negative or behind y's last row counts as
+ * a row of zeros.  weights may be NULL (ones).  y and out: one matrix each,
+ * equal cols; out has a row for each token.  k: 1 .. MUON_MAX_CHOSEN.
+ */
+muon_status_t muon_expert_sum(const muon_batch_t* y, const int32_t* slots, const float* weights, int64_t k,
+                              const muon_batch_t* out, void* stream);
+
+/*
+ * The gradient of those weights: dots[t*k+j] = <grad[t], y[slots[t*k+j]]> in
+ * fp32, 0 where the slot has no row.  (The gradient of y is grad's rows in the
+ * order of the pairs, times the weights: muon_block_quantize makes its codes.)
+ */
+muon_status_t muon_expert_dot(const muon_batch_t* grad, const muon_batch_t* y, const int32_t* slots, int64_t k,
+                              float* dots, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,6 +12,7 @@ from . import _lib
 from ._lib import (MUON_BF16, MUON_F32, MUON_SCALE_MATCH_RMS, MUON_SCALE_NONE, MUON_SCALE_ORIGINAL, MuonBatch,
                    MuonError)
 from .blocks import BlockCodes, block_matmul, expert_grad, expert_matmul, quantize
+from .experts import BalanceBias, Routing, expert_dot, expert_sum, route, route_backward
 from .multi import AdamWMulti, GradClip, StepControl
 from .muon import (EPS, QUINTIC, AdamW, Batch, MuonStep, OptimizerStep, apply, apply_grouped, batch, is_muon_param,
                    momentum, momentum_grouped, orthogonalize, orthogonalize_grouped, workspace)
@@ -20,4 +21,5 @@ __all__ = ["_lib", "MUON_BF16", "MUON_F32", "MUON_SCALE_MATCH_RMS", "MUON_SCALE_
            "MuonBatch", "MuonError", "EPS", "QUINTIC", "Batch", "MuonStep", "apply", "apply_grouped", "batch",
            "momentum", "momentum_grouped", "orthogonalize", "orthogonalize_grouped", "workspace", "AdamW",
            "OptimizerStep", "is_muon_param", "AdamWMulti", "GradClip", "StepControl",
-           "BlockCodes", "block_matmul", "expert_grad", "expert_matmul", "quantize"]
+           "BlockCodes", "block_matmul", "expert_grad", "expert_matmul", "quantize",
+           "BalanceBias", "Routing", "expert_dot", "expert_sum", "route", "route_backward"]

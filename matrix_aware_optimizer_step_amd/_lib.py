@@ -33,7 +33,9 @@ EXPORTED = ("muon_abi_version", "muon_last_error", "muon_status_string", "muon_m
             "soap_statistics_grouped", "soap_qr_workspace", "soap_qr", "soap_refresh_workspace", "soap_refresh",
             "soap_refresh_grouped_workspace", "soap_refresh_grouped",
             "soap_precondition_workspace", "soap_precondition", "soap_precondition_grouped_workspace",
-            "soap_precondition_grouped", "muon_block_quantize", "muon_block_matmul")
+            "soap_precondition_grouped", "muon_block_quantize", "muon_block_matmul",
+            "muon_route_capacity", "muon_route_workspace", "muon_route", "muon_route_backward", "muon_balance_update",
+            "muon_expert_sum", "muon_expert_dot")
 
 ADAMW_CHUNK = 4096  # MUON_ADAMW_CHUNK
 GRAD_CHUNK = 16384  # MUON_GRAD_CHUNK
@@ -41,6 +43,8 @@ PARAM_CHUNK = 4096  # MUON_PARAM_CHUNK
 STATE_BLOCK = 256   # MUON_STATE_BLOCK
 SKIP_NONFINITE = 1  # MUON_SKIP_NONFINITE
 CODE_BLOCK = 128    # MUON_CODE_BLOCK
+MAX_EXPERTS, MAX_CHOSEN, MAX_EXPERT_GROUPS = 512, 16, 32  # MUON_MAX_EXPERTS, _CHOSEN, _EXPERT_GROUPS
+SCORES = {"softmax": 0, "sigmoid": 1}  # muon_score_t
 PRODUCT_BATCH, PRODUCT_ROWS, PRODUCT_REDUCE = 0, 1, 2  # muon_product_t
 
 
@@ -105,6 +109,14 @@ class MuonCodes(ctypes.Structure):
                 ("block_rows", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class MuonRoute(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("ld", ctypes.c_int64), ("tokens", ctypes.c_int64),
+                ("experts", ctypes.c_int64), ("k", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_best", ctypes.c_int32), ("align", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -117,7 +129,7 @@ def load() -> ctypes.CDLL:
                            "(the Muon path has no CPU fallback)")
     lib = ctypes.CDLL(LIB_PATH)
     P = ctypes.POINTER(MuonBatch)
-    Q = ctypes.POINTER(MuonCodes)
+    Q, R = ctypes.POINTER(MuonCodes), ctypes.POINTER(MuonRoute)
     vp, f32, i32, i64, sz = ctypes.c_void_p, ctypes.c_float, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
     sig = {
         "muon_abi_version": (ctypes.c_int, []),
@@ -175,6 +187,13 @@ def load() -> ctypes.CDLL:
                                                      i64, f32, f32, f32, vp, sz, vp]),
         "muon_block_quantize": (ctypes.c_int, [P, vp, vp, i64, Q, Q, vp]),
         "muon_block_matmul": (ctypes.c_int, [Q, Q, P, vp, i32, i32, vp]),
+        "muon_route_capacity": (i64, [i64, i64, i64, i64]),
+        "muon_route_workspace": (sz, [i64, i64]),
+        "muon_route": (ctypes.c_int, [R, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "muon_route_backward": (ctypes.c_int, [R, vp, vp, vp, vp, i64, vp]),
+        "muon_balance_update": (ctypes.c_int, [vp, vp, i64, f32, vp, vp]),
+        "muon_expert_sum": (ctypes.c_int, [P, vp, vp, i64, P, vp]),
+        "muon_expert_dot": (ctypes.c_int, [P, P, vp, i64, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -469,3 +488,38 @@ def muon_block_matmul(a: MuonCodes, b: MuonCodes, c: MuonBatch, offsets_ptr: int
                       accumulate: int, stream: int) -> None:
     _check(load().muon_block_matmul(_ref(a), _ref(b), _ref(c), offsets_ptr, product, accumulate, stream),
            "muon_block_matmul")
+
+
+def muon_route_capacity(tokens: int, experts: int, k: int, align: int) -> int:
+    return load().muon_route_capacity(tokens, experts, k, align)
+
+
+def muon_route_workspace(tokens: int, experts: int) -> int:
+    return load().muon_route_workspace(tokens, experts)
+
+
+def muon_route(route: MuonRoute, bias_ptr: int | None, mask_ptr: int | None, chosen_ptr: int, weights_ptr: int,
+               slots_ptr: int | None, pairs_ptr: int | None, offsets_ptr: int | None, loads_ptr: int | None,
+               workspace_ptr: int, ws_bytes: int, stream: int) -> None:
+    _check(load().muon_route(_ref(route), bias_ptr, mask_ptr, chosen_ptr, weights_ptr, slots_ptr, pairs_ptr,
+                             offsets_ptr, loads_ptr, workspace_ptr, ws_bytes, stream), "muon_route")
+
+
+def muon_route_backward(route: MuonRoute, chosen_ptr: int, weights_ptr: int, grad_weights_ptr: int,
+                        grad_logits_ptr: int, ld_grad: int, stream: int) -> None:
+    _check(load().muon_route_backward(_ref(route), chosen_ptr, weights_ptr, grad_weights_ptr, grad_logits_ptr, ld_grad,
+                                      stream), "muon_route_backward")
+
+
+def muon_balance_update(bias_ptr: int, loads_ptr: int, experts: int, rate: float, control_ptr: int | None,
+                        stream: int) -> None:
+    _check(load().muon_balance_update(bias_ptr, loads_ptr, experts, rate, control_ptr, stream), "muon_balance_update")
+
+
+def muon_expert_sum(y: MuonBatch, slots_ptr: int, weights_ptr: int | None, k: int, out: MuonBatch,
+                    stream: int) -> None:
+    _check(load().muon_expert_sum(_ref(y), slots_ptr, weights_ptr, k, _ref(out), stream), "muon_expert_sum")
+
+
+def muon_expert_dot(grad: MuonBatch, y: MuonBatch, slots_ptr: int, k: int, dots_ptr: int, stream: int) -> None:
+    _check(load().muon_expert_dot(_ref(grad), _ref(y), slots_ptr, k, dots_ptr, stream), "muon_expert_dot")

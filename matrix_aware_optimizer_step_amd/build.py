@@ -16,7 +16,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmuon355.so")
 SOURCES = ["abi.cpp", "abi_optim.cpp", "elementwise.hip", "ns_gemm.hip", "adamw.hip", "adamw_multi.hip", "grad_norm.hip",
-           "soap.hip", "scratch.hip", "abi_experts.cpp", "block_codes.hip", "block_gemm.hip"]
+           "soap.hip", "scratch.hip", "abi_experts.cpp", "block_codes.hip", "block_gemm.hip",
+           "route.hip", "expert_sum.hip"]
 ARCH = "gfx950"
 
 # Packed fp32 ALU ops are disabled in all device code.

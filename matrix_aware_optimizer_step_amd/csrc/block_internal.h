@@ -53,4 +53,67 @@ struct BlockGemmArgs {
 };
 hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t stream);
 
+// ------------------------------------------------------------ routing
+
+struct RouteArgs {
+  const char* logits;
+  int64_t ld;               // elements between tokens
+  const float* bias;        // [experts] or null
+  const uint8_t* mask;      // [tokens] or null: 0 = the token goes nowhere
+  int32_t* chosen;          // [tokens, k]
+  float* weights;           // [tokens, k]
+  int32_t* slots;           // [tokens, k]; slots, pairs and offsets may all be null
+  int32_t* pairs;           // [capacity]
+  int32_t* offsets;         // [experts + 1]
+  int32_t* loads;           // [experts] or null
+  uint8_t* counts;          // [blocks of kRouteTokens tokens][experts rounded up to 16]
+  int64_t capacity;
+  int32_t tokens, experts, k;
+  int32_t dtype;            // of the logits: 0 = f32, 1 = bf16
+  int32_t sigmoid, renormalize;
+  int32_t groups, top_groups, group_best;
+  int32_t align;
+  float scale;
+};
+constexpr int kRouteTokens = 64;  // tokens of a workgroup, one bit each in an expert's mask
+hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
+
+struct RouteBackwardArgs {
+  const char* logits;
+  int64_t ld;
+  const int32_t* chosen;
+  const float* weights;
+  const float* grad;        // [tokens, k]
+  char* out;                // [tokens, experts], as the logits
+  int64_t ld_out;
+  int32_t tokens, experts, k;
+  int32_t dtype;
+  int32_t sigmoid, renormalize;
+  float scale;
+};
+hipError_t launch_route_backward(const RouteBackwardArgs& a, hipStream_t stream);
+
+struct BalanceArgs {
+  float* bias;
+  int32_t* loads;
+  int32_t experts;
+  float rate;
+  const StepControl* control;  // or null
+};
+hipError_t launch_balance(const BalanceArgs& a, hipStream_t stream);
+
+// ------------------------------------------------------------ sums over a token's experts
+
+struct ExpertSumArgs {
+  MatBatch y;               // [rows, cols]
+  MatBatch out;             // [tokens, cols]; the gradient of the sums in the dot
+  const int32_t* slots;     // [tokens, k]
+  const float* weights;     // [tokens, k] or null (ones); the dot writes it
+  float* dots;
+  int64_t tokens;
+  int32_t rows, cols, k;
+};
+hipError_t launch_expert_sum(const ExpertSumArgs& a, hipStream_t stream);
+hipError_t launch_expert_dot(const ExpertSumArgs& a, hipStream_t stream);
+
 }  // namespace muon

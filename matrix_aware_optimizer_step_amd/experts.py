@@ -1,0 +1,254 @@
+"""Mixture-of-experts operators of libmuon355 for torch: the routing of tokens
+to experts with its gradient and the step of the bias that balances it, and the
+tokens' sums over their experts.
+
+Together with the block codes (``blocks``) they run the layers whose expert
+matrices the optimizer step updates::
+
+    r = route(logits, 8, bias=balance.bias, loads=balance.loads, align=128)
+    a, at = quantize(x, pairs=(r.pairs, 8), order="both")  # rows by expert
+    y = expert_matmul(a, codes.q, r.offsets)
+    out = expert_sum(y, r.slots, r.weights)
+
+and backward, from the gradient of ``out``::
+
+    g, gt = quantize(grad, pairs=r.pairs, weights=r.weights, order="both")
+    expert_grad(gt, at, r.offsets, out=weight_grads, accumulate=True)
+    grad_x = expert_sum(expert_matmul(g, codes.qt, r.offsets), r.slots)
+    grad_logits = route_backward(logits, r, expert_dot(grad, y, r.slots))
+
+Every call only enqueues kernels, on the current stream of its tensors' device
+or on ``stream``; there is no CPU path.
+"""
+
+from __future__ import annotations
+
+from dataclasses import dataclass
+
+import torch
+
+from . import _lib as L
+from .blocks import _enqueue, _need, _same_device
+from .muon import dtype_code
+from .multi import StepControl, _settle
+
+NO_EXPERT = -1
+
+
+@dataclass
+class Routing:
+    """What ``route`` found.
+
+    ``experts`` int32 [tokens, k]: the chosen ones, best first, -1 for none.
+    ``weights`` float32 [tokens, k].  ``slots`` int32 [tokens, k]: each pair's row in
+    the order by expert, or -1.  ``pairs`` int32 [rows]: each row's pair (token * k + j),
+    or -1.  ``offsets`` int32 [experts + 1]: each expert's first row.  The last
+    three are None with ``order=False``.
+    """
+    experts: torch.Tensor
+    weights: torch.Tensor
+    slots: torch.Tensor | None
+    pairs: torch.Tensor | None
+    offsets: torch.Tensor | None
+    score: str
+    renormalize: bool
+    scale: float
+
+    @property
+    def k(self) -> int:
+        return self.experts.shape[1]
+
+
+def _check_logits(logits) -> None:
+    _need(logits.dim() == 2, "logits must be [tokens, experts]")
+    _need(logits.stride(1) == 1 or logits.shape[1] <= 1, "logits must be row-major (last stride 1)")
+    _need(1 <= logits.shape[1] <= L.MAX_EXPERTS, f"experts outside [1, {L.MAX_EXPERTS}]")
+
+
+def _ld(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _vector(t, n, dtype, what, device) -> None:
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
+    _need(tuple(t.shape) == n and t.is_contiguous(), f"{what} must be contiguous and {n}, not {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, not on {device}")
+
+
+def route(logits: torch.Tensor, k: int, *, bias: torch.Tensor | None = None, score: str = "softmax", groups: int = 1,
+          top_groups: int = 1, group_best: int = 2, renormalize: bool = True, scale: float = 1.0,
+          mask: torch.Tensor | None = None, align: int = 1, loads: torch.Tensor | None = None, order: bool = True,
+          stream=None) -> Routing:
+    """Tokens to their k best experts (``muon_route``; muon355.h has the definition).
+
+    ``logits``: bfloat16 or float32 [tokens, experts], a row stride of its own.
+    ``bias`` (float32 [experts]) is added to the scores that choose, not to the
+    weights.  ``groups`` runs of experts are marked by the sum of their ``group_best``
+    (1 or 2) best, and the ``top_groups`` best stay.  ``mask`` (bool [tokens]): False
+    sends a token nowhere (padding).  A logit of -inf takes its expert out.
+    ``align``: each expert's rows are rounded up to a multiple of it (128 where
+    ``expert_grad`` follows).  ``loads`` (int32 [experts]): each expert's tokens are
+    added to it.  ``order=False`` leaves the order by expert out.
+    """
+    _check_logits(logits)
+    tokens, experts = logits.shape
+    device = logits.device
+    _need(score in L.SCORES, f"score must be one of {sorted(L.SCORES)}")
+    _need(1 <= k <= min(L.MAX_CHOSEN, experts), f"k outside [1, min({L.MAX_CHOSEN}, experts)]")
+    _vector(bias, (experts,), torch.float32, "bias", device)
+    _vector(mask, (tokens,), torch.bool, "mask", device)
+    _vector(loads, (experts,), torch.int32, "loads", device)
+    capacity = L.muon_route_capacity(max(tokens, 1), experts, k, align) if order else 0
+    _need(capacity > 0 or not order, "align outside [1, 65536], or an order of more than 2^31-1 rows")
+    if not tokens:
+        capacity = -(-experts * (align - 1) // align) * align if order else 0
+    n = tokens * k
+    ints = torch.empty((2 * n + capacity + experts + 1) if order else n, dtype=torch.int32, device=device)
+    weights = torch.empty(tokens, k, dtype=torch.float32, device=device)
+    chosen = ints[:n].view(tokens, k)
+    slots = pairs = offsets = None
+    if order:
+        slots, pairs = ints[n:2 * n].view(tokens, k), ints[2 * n:2 * n + capacity]
+        offsets = ints[2 * n + capacity:]
+    found = Routing(chosen, weights, slots, pairs, offsets, score, bool(renormalize), float(scale))
+    desc = L.MuonRoute(logits.data_ptr(), _ld(logits), max(tokens, 1), experts, k, dtype_code(logits), L.SCORES[score],
+                       int(bool(renormalize)), groups, top_groups, group_best, align, scale)
+    if tokens == 0:
+        _need(device.type == "cuda", "the tensors are not on a GPU (there is no CPU path)")
+        if order:
+            pairs.fill_(NO_EXPERT)
+            offsets.zero_()
+        return found
+    need = L.muon_route_workspace(tokens, experts)
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    at = ints.data_ptr()
+    _enqueue(device, stream, [ints, weights, ws], L.muon_route, desc, None if bias is None else bias.data_ptr(),
+             None if mask is None else mask.data_ptr(), at, weights.data_ptr(), at + 4 * n if order else None,
+             at + 8 * n if order else None, at + 8 * n + 4 * capacity if order else None,
+             None if loads is None else loads.data_ptr(), ws.data_ptr(), need)
+    return found
+
+
+def route_backward(logits: torch.Tensor, routing: Routing, grad_weights: torch.Tensor, *,
+                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Gradient of the logits that ``route`` was given, from the gradient of its
+    weights (float32 [tokens, k]), in the logits' type."""
+    _check_logits(logits)
+    device = logits.device
+    shape = (logits.shape[0], routing.k)
+    _vector(routing.experts, shape, torch.int32, "routing.experts", device)
+    _vector(routing.weights, shape, torch.float32, "routing.weights", device)
+    _vector(grad_weights, shape, torch.float32, "grad_weights", device)
+    made = out is None
+    if made:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=device)
+    else:
+        _need(out.shape == logits.shape and out.dtype == logits.dtype and (out.stride(1) == 1 or out.shape[1] <= 1),
+              "out must have the logits' shape and type and last stride 1")
+        _same_device(device, out=out)
+    if logits.shape[0] == 0:
+        return out
+    desc = L.MuonRoute(logits.data_ptr(), _ld(logits), logits.shape[0], logits.shape[1], routing.k, dtype_code(logits),
+                       L.SCORES[routing.score], int(routing.renormalize), 1, 1, 1, 1, routing.scale)
+    _enqueue(device, stream, [out] if made else [], L.muon_route_backward, desc, routing.experts.data_ptr(),
+             routing.weights.data_ptr(), grad_weights.data_ptr(), out.data_ptr(), _ld(out))
+    return out
+
+
+def _rows(t, what) -> L.MuonBatch:
+    _need(t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1), f"{what} must be a row-major matrix")
+    return L.MuonBatch(None, t.data_ptr(), 0, 1, t.shape[0], t.shape[1], _ld(t), dtype_code(t), 0)
+
+
+def _check_slots(slots, y) -> None:
+    _need(slots.dim() == 2 and 1 <= slots.shape[1] <= L.MAX_CHOSEN, f"slots must be [tokens, 1 .. {L.MAX_CHOSEN}]")
+    _vector(slots, tuple(slots.shape), torch.int32, "slots", y.device)
+
+
+def expert_sum(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None = None, *,
+               out: torch.Tensor | None = None, dtype=None, stream=None) -> torch.Tensor:
+    """Each token's sum of weights[t, j] * y[slots[t, j]] (weights None: ones),
+    in fp32, rounded once to ``dtype`` (None: y's).  A slot of -1 adds nothing."""
+    desc = _rows(y, "y")
+    _check_slots(slots, y)
+    tokens, k = slots.shape
+    _vector(weights, (tokens, k), torch.float32, "weights", y.device)
+    made = out is None
+    if made:
+        out = torch.empty(tokens, y.shape[1], dtype=dtype or y.dtype, device=y.device)
+    _need(tuple(out.shape) == (tokens, y.shape[1]), f"out must be {(tokens, y.shape[1])}")
+    _same_device(y.device, out=out)
+    od = _rows(out, "out")
+    if out.numel() == 0:
+        return out
+    if y.shape[0] == 0:
+        return out.zero_()
+    _enqueue(y.device, stream, [out] if made else [], L.muon_expert_sum, desc, slots.data_ptr(),
+             None if weights is None else weights.data_ptr(), k, od)
+    return out
+
+
+def expert_dot(grad: torch.Tensor, y: torch.Tensor, slots: torch.Tensor, *, out: torch.Tensor | None = None,
+               stream=None) -> torch.Tensor:
+    """The gradient of ``expert_sum``'s weights: <grad[t], y[slots[t, j]]>, float32 [tokens, k]."""
+    gd, yd = _rows(grad, "grad"), _rows(y, "y")
+    _check_slots(slots, y)
+    tokens, k = slots.shape
+    _need(tuple(grad.shape) == (tokens, y.shape[1]), f"grad must be {(tokens, y.shape[1])}")
+    _same_device(y.device, grad=grad)
+    made = out is None
+    if made:
+        out = torch.empty(tokens, k, dtype=torch.float32, device=y.device)
+    _vector(out, (tokens, k), torch.float32, "out", y.device)
+    if out.numel() == 0:
+        return out
+    if y.numel() == 0:
+        return out.zero_()
+    _enqueue(y.device, stream, [out] if made else [], L.muon_expert_dot, gd, yd, slots.data_ptr(), k, out.data_ptr())
+    return out
+
+
+class BalanceBias:
+    """The bias that keeps a router's experts evenly loaded, and the loads it
+    goes by.
+
+    Give ``bias`` and ``loads`` to ``route`` in every forward pass of a step; ``step()``
+    (``OptimizerStep(balance=[...])`` calls it after its updates) moves each
+    expert's bias by ``rate`` towards the mean load and starts the loads again from
+    zero (``muon_balance_update``).  With a ``StepControl`` a skipped step leaves the bias as it is.
+    With several GPUs sum ``loads`` over them first, with an all-reduce.
+    """
+
+    def __init__(self, experts: int, rate: float = 1e-3, device="cuda"):
+        _need(1 <= experts <= L.MAX_EXPERTS, f"experts outside [1, {L.MAX_EXPERTS}]")
+        self.rate = float(rate)
+        self.bias = torch.zeros(experts, dtype=torch.float32, device=device)
+        self.loads = torch.zeros(experts, dtype=torch.int32, device=device)
+        _settle(self.bias.device)
+
+    def step(self, control: StepControl | None = None, stream=None) -> None:
+        device = self.bias.device
+        if control is not None and control.device != device:
+            raise ValueError("control is on another device than the bias")
+        _enqueue(device, stream, [self.bias, self.loads], L.muon_balance_update, self.bias.data_ptr(),
+                 self.loads.data_ptr(), self.bias.numel(), self.rate, None if control is None else control.data_ptr())
+
+    def state_dict(self) -> dict:
+        return {"bias": self.bias.to("cpu", copy=True), "loads": self.loads.to("cpu", copy=True), "rate": self.rate}
+
+    def check_state(self, state: dict) -> None:
+        """Raises where load_state_dict() would refuse the state."""
+        for key, own in (("bias", self.bias), ("loads", self.loads)):
+            if key not in state or state[key].shape != own.shape:
+                raise ValueError("the state was saved for another number of experts")
+
+    def load_state_dict(self, state: dict) -> None:
+        self.check_state(state)
+        self.bias.copy_(state["bias"])
+        self.loads.copy_(state["loads"])
+        self.rate = float(state["rate"])
+        _settle(self.bias.device)
