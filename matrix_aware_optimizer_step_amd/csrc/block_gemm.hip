@@ -145,6 +145,16 @@ __device__ __forceinline__ void store_row(const MatBatch& c, char* row, int64_t 
   }
 }
 
+// The permutation of the 16-byte chunks of a row in LDS.  Sixteen lanes read a
+// chunk of 16 rows together; two rows are 256 bytes, one pass over the banks,
+// so the chunks of the 8 pairs of rows have to differ: consecutive rows for A,
+// rows {0, 1, 2, 3} + 4 j + SPAN * {0, 1, 2, 3} for B.
+__device__ __forceinline__ int a_swizzle(int row) { return (row >> 1) & 7; }
+template <int SPAN>
+__device__ __forceinline__ int b_swizzle(int row) {
+  return ((row >> 1) & 1) | ((row / SPAN & 3) << 1);
+}
+
 // Row offset i of the list, kept inside [0, most] and above the one before.
 __device__ __forceinline__ int offset_at(const int32_t* offsets, int64_t i, int most) {
   const int o = offsets[i];
@@ -235,38 +245,40 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
   const float* SA = a.a.scales + amat * a.a.scale_stride + kb0 * a.a.scale_ld + m0;
   const float* SB0 = a.b.scales + bmat * a.b.scale_stride + kb0 * a.b.scale_ld;
 
-  // copies: lane l of an instruction fills slot l % 8 of row l / 8; rows behind
-  // the matrix repeat its last one (their results are not stored)
-  uint32_t ofs_a[IA], ofs_b[IB];
-#pragma unroll
-  for (int r = 0; r < IA; ++r) {
-    const int row = (wave * IA + r) * 8 + (lane >> 3);
-    const int c = (lane & 7) ^ ((row >> 1) & 7);
-    ofs_a[r] = static_cast<uint32_t>(min(row, a.M - 1 - m0)) * static_cast<uint32_t>(a.a.ld) + c * 16;
-  }
-#pragma unroll
-  for (int r = 0; r < IB; ++r) {
-    const int row = (wave * IB + r) * 8 + (lane >> 3);
-    const int c = (lane & 7) ^ (((row >> 1) & 1) | ((row / SPAN & 3) << 1));
-    ofs_b[r] = static_cast<uint32_t>(min(row, a.N - 1 - n0)) * static_cast<uint32_t>(a.b.ld) + c * 16;
-  }
+  // copies: lane l of an instruction fills slot l % 8 of row l / 8, and a
+  // wave's instructions are STEP rows apart; rows behind the matrix repeat its
+  // last one (their results are not stored).  The offsets are computed where
+  // they are used, two instructions each: held, they cost the registers that
+  // keep the loop free of scratch memory.
+  constexpr int STEP = 8 * NW;
+  static_assert(STEP % 16 == 0 && (STEP / SPAN == 2 || STEP / SPAN == 4), "the swizzles repeat");
+  const int row8 = wave * 8 + (lane >> 3);
+  const uint32_t chunk_a = ((lane & 7) ^ a_swizzle(row8)) << 4;
+  const uint32_t chunk_b = ((lane & 7) ^ b_swizzle<SPAN>(row8)) << 4;
+  const int last_a = a.M - 1 - m0, last_b = a.N - 1 - n0;
+  const uint32_t lda = static_cast<uint32_t>(a.a.ld), ldb = static_cast<uint32_t>(a.b.ld);
   const uint32_t lds0 = lds_address(smem);
   auto copy = [&](int kt, int stage) {
     const char* pa = A + static_cast<int64_t>(kt) * 128;
     const char* pb = B + static_cast<int64_t>(kt) * 128;
-    const uint32_t l = lds0 + stage * STAGE;
+    const uint32_t l = lds0 + stage * STAGE + wave * 1024;
 #pragma unroll
-    for (int r = 0; r < IA; ++r) copy16(pa, ofs_a[r], l + (wave * IA + r) * 1024);
+    for (int r = 0; r < IA; ++r)
+      copy16(pa, __umul24(min(row8 + r * STEP, last_a), lda) + chunk_a, l + r * STEP * 128);
 #pragma unroll
-    for (int r = 0; r < IB; ++r) copy16(pb, ofs_b[r], l + OPB + (wave * IB + r) * 1024);
-    for (int s = wave; s < BM / 64 + (SB ? BN / 64 : 0); s += NW) {
-      if (s < BM / 64) {
-        copy4(reinterpret_cast<const char*>(SA + kt * a.a.scale_ld),
-              4 * static_cast<uint32_t>(min(s * 64 + lane, a.M - 1 - m0)), l + SCALES + s * 256);
-      } else {
-        const int row = (s - BM / 64) * 64 + lane;
-        copy4(reinterpret_cast<const char*>(SB0 + kt * a.b.scale_ld + n0),
-              4 * static_cast<uint32_t>(min(row, a.N - 1 - n0)), l + SCALES + s * 256);
+    for (int r = 0; r < IB; ++r)
+      copy16(pb, __umul24(min(row8 + r * STEP, last_b), ldb) + (chunk_b ^ (STEP / SPAN == 2 && r % 2 ? 64 : 0)),
+             l + OPB + r * STEP * 128);
+    // the scales, 64 rows an instruction
+#pragma unroll
+    for (int r = 0; r < (BM / 64 + (SB ? BN / 64 : 0) + NW - 1) / NW; ++r) {
+      const int q = wave + r * NW;
+      if (q < BM / 64) {
+        copy4(reinterpret_cast<const char*>(SA + kt * a.a.scale_ld), 4 * min(q * 64 + lane, last_a),
+              lds0 + stage * STAGE + SCALES + q * 256);
+      } else if (SB && q < BM / 64 + BN / 64) {
+        copy4(reinterpret_cast<const char*>(SB0 + kt * a.b.scale_ld + n0), 4 * min(q * 64 - BM + lane, last_b),
+              lds0 + stage * STAGE + SCALES + q * 256);
       }
     }
   };
@@ -275,18 +287,19 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
   const int l15 = lane & 15, g = lane >> 4;
   const int arow = wm * (BM / WM) + l15;
   const int brow = wn * (BN / WN) + (l15 >> 2) * SPAN + (l15 & 3);  // tile j adds 4 j
-  const int bswz = (((brow >> 1) & 1) | ((brow / SPAN & 3) << 1));
-  const int sbn = min(n0 + wn * (BN / WN), a.N - 1) >> 7;  // block row of B, square blocks (from B's first one)
+  const int sbn = min(n0 + wn * (BN / WN), a.N - 1) >> 7;  // block row of B, square blocks
   f32x4 acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 
-  auto fragment = [&](Fragment<WIDE>& f, const char* p, int swz) {
-    f.set(*reinterpret_cast<const i32x4*>(p + ((g ^ swz) << 4)),
-          *reinterpret_cast<const i32x4*>(p + (((g + 4) ^ swz) << 4)));
-  };
+  // a lane's 32 codes of a row: chunks g and g + 4.  (Tile rows 16 apart, and
+  // B's rows 4 j apart, share the swizzle up to b_swizzle's lowest bit, which
+  // 4 j leaves alone.)
+  const uint32_t a_lo = arow * 128 + ((g ^ a_swizzle(arow)) << 4), a_hi = a_lo ^ 64;
+  const uint32_t b_lo = OPB + brow * 128 + ((g ^ b_swizzle<SPAN>(brow)) << 4), b_hi = b_lo ^ 64;
+  const uint32_t a_scale = SCALES + arow * 4, b_scale = SCALES + (BM + wn * (BN / WN) + g * SPAN) * 4;
 
   if (nk > 0) copy(0, 0);
   float sq = 0.0f;
@@ -299,30 +312,44 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
       copy(kt + 1, (kt + 1) & 1);
       if (!SB) sq = SB0[(kt + 1) * a.b.scale_ld + sbn];
     }
-    Fragment<WIDE> fa[MT];
+    Fragment<WIDE> fa[MT], fb[2];
     float sa[MT];
+    f32x4 p[2][MT], w[2];
+    auto read_b = [&](int j) {
+      fb[j & 1].set(*reinterpret_cast<const i32x4*>(s + b_lo + 512 * j),
+                    *reinterpret_cast<const i32x4*>(s + b_hi + 512 * j));
+    };
+    auto add = [&](int i, int j) {  // a tile's sums, times their scales
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        acc[i][j][r] = __builtin_fmaf(SB ? p[j & 1][i][r] * w[j & 1][r] : p[j & 1][i][r], sa[i], acc[i][j][r]);
+    };
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+      fa[i].set(*reinterpret_cast<const i32x4*>(s + a_lo + 2048 * i),
+                *reinterpret_cast<const i32x4*>(s + a_hi + 2048 * i));
+    read_b(0);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      fragment(fa[i], s + (arow + i * 16) * 128, (l15 >> 1) & 7);
-      sa[i] = *reinterpret_cast<const float*>(s + SCALES + (arow + i * 16) * 4);
+      sa[i] = *reinterpret_cast<const float*>(s + a_scale + 64 * i);
       if (!SB) sa[i] *= sb;
     }
+    // The products of tile column j run while the sums of j - 1 are added and
+    // the codes of j + 1 come from LDS.  The order is pinned: left to itself
+    // the compiler adds each product at once and waits for it.
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      Fragment<WIDE> fb;
-      fragment(fb, s + OPB + (brow + 4 * j) * 128, bswz);
-      f32x4 p[MT];
+      if (j + 1 < NT) read_b(j + 1);
+      if (SB) w[j & 1] = *reinterpret_cast<const f32x4*>(s + b_scale + 16 * j);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) p[i] = fb * fa[i];
-      f32x4 w;
-      if (SB)
-        w = *reinterpret_cast<const f32x4*>(s + SCALES + BM * 4 + (wn * (BN / WN) + g * SPAN + 4 * j) * 4);
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          acc[i][j][r] = __builtin_fmaf(SB ? p[i][r] * w[r] : p[i][r], sa[i], acc[i][j][r]);
+      for (int i = 0; i < MT; ++i) {
+        p[j & 1][i] = fb[j & 1] * fa[i];
+        if (j > 0) add(i, j - 1);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) add(i, NT - 1);
     wait_all();
   }
 
@@ -350,21 +377,13 @@ int64_t count_tiles(BlockGemmArgs& a, int bm, int bn) {
   return a.total_tiles;
 }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, bool WIDE>
 void launch(BlockGemmArgs& a, hipStream_t s) {
   const uint32_t g = static_cast<uint32_t>(count_tiles(a, BM, BN));
-  if (a.c.dtype) {
-    if (a.square) {
-      gemm_kernel<BM, BN, WM, WN, false, false><<<g, 64 * WM * WN, 0, s>>>(a);
-    } else {
-      gemm_kernel<BM, BN, WM, WN, true, false><<<g, 64 * WM * WN, 0, s>>>(a);
-    }
+  if (a.square) {
+    gemm_kernel<BM, BN, WM, WN, false, WIDE><<<g, 64 * WM * WN, 0, s>>>(a);
   } else {
-    if (a.square) {
-      gemm_kernel<BM, BN, WM, WN, false, true><<<g, 64 * WM * WN, 0, s>>>(a);
-    } else {
-      gemm_kernel<BM, BN, WM, WN, true, true><<<g, 64 * WM * WN, 0, s>>>(a);
-    }
+    gemm_kernel<BM, BN, WM, WN, true, WIDE><<<g, 64 * WM * WN, 0, s>>>(a);
   }
 }
 
@@ -372,10 +391,16 @@ void launch(BlockGemmArgs& a, hipStream_t s) {
 
 hipError_t launch_block_gemm(const BlockGemmArgs& args, hipStream_t s) {
   BlockGemmArgs a = args;
-  if (count_tiles(a, 256, 256) >= 200) {
-    launch<256, 256, 4, 2>(a, s);
+  if (a.c.dtype) {
+    if (count_tiles(a, 256, 256) >= 200) {
+      launch<256, 256, 4, 2, false>(a, s);
+    } else {
+      launch<128, 128, 2, 2, false>(a, s);
+    }
+  } else if (count_tiles(a, 256, 128) >= 200) {
+    launch<256, 128, 4, 2, true>(a, s);
   } else {
-    launch<128, 128, 2, 2>(a, s);
+    launch<128, 128, 2, 2, true>(a, s);
   }
   return hipGetLastError();
 }
