@@ -9,15 +9,17 @@
 // output element and block (two where B has a scale for each row), half the
 // (the whole) time of the matrix instructions, which run beside them.
 //
-// B's rows are the instruction's rows and A's rows its columns, and the row
-// that a lane's four results belong to is chosen freely when B is read from
-// LDS: a lane ends up with one row m and 4*NT consecutive columns n of the
-// result, which it stores in whole 16-byte pieces without a detour.
+// B's rows are the instruction's rows and A's rows its columns, and which row
+// of B the instruction's row stands for is chosen when B is read from LDS
+// (b_row): a lane ends up with 16 bytes of one row of the result, and four
+// lanes with 64, stored without a detour.
 //
 // A workgroup computes a tile of BM x BN from k-tiles of one block, double
 // buffered in LDS by global_load_lds_dwordx4.  Rows are 128 bytes; the 16-byte
 // chunks of a row are XOR-permuted (a_swizzle, b_swizzle) so that the 16 rows
 // of a fragment's read cover all 64 banks.
+
+#include <type_traits>
 
 #include "block_internal.h"
 
@@ -103,56 +105,57 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
 
-// N consecutive results of a row, `left` of them inside the matrix.
-template <int N>
-__device__ __forceinline__ void store_row(const MatBatch& c, char* row, int64_t col, int left, const float* v,
-                                          int accumulate) {
-  if (left <= 0) return;
-  if (c.dtype) {
-    char* p = row + col * 2;
-    if (left >= N && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
-#pragma unroll
-      for (int k = 0; k < N; k += 8) {
-        uint4 u;
-        u.x = bf16_pair(v[k], v[k + 1]);
-        u.y = bf16_pair(v[k + 2], v[k + 3]);
-        u.z = bf16_pair(v[k + 4], v[k + 5]);
-        u.w = bf16_pair(v[k + 6], v[k + 7]);
-        *reinterpret_cast<uint4*>(p + 2 * k) = u;
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < N; ++k)
-        if (k < left) reinterpret_cast<__bf16*>(p)[k] = static_cast<__bf16>(v[k]);
-    }
-    return;
-  }
-  float* p = reinterpret_cast<float*>(row) + col;
-  if (left >= N && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
-#pragma unroll
-    for (int k = 0; k < N; k += 4) {
-      float4 u = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+// 16 bytes of a row of the result from column n on, `left` elements of them
+// inside the matrix.
+template <bool WIDE>
+__device__ __forceinline__ void store_run(char* row, int64_t n, int left, const float* v, int accumulate) {
+  if (WIDE) {
+    float* p = reinterpret_cast<float*>(row) + n;
+    if (left >= 4) {
+      float4 u = make_float4(v[0], v[1], v[2], v[3]);
       if (accumulate) {
-        const float4 o = *reinterpret_cast<const float4*>(p + k);
+        float4 o;
+        __builtin_memcpy(&o, p, 16);
         u = make_float4(o.x + u.x, o.y + u.y, o.z + u.z, o.w + u.w);
       }
-      *reinterpret_cast<float4*>(p + k) = u;
+      __builtin_memcpy(p, &u, 16);  // at any alignment
+    } else {
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        if (k < left) p[k] = accumulate ? p[k] + v[k] : v[k];
     }
   } else {
+    char* p = row + 2 * n;
+    uint32_t u[4];
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-      if (k < left) p[k] = accumulate ? p[k] + v[k] : v[k];
+    for (int k = 0; k < 4; ++k) u[k] = bf16_pair(v[2 * k], v[2 * k + 1]);
+    if (left >= 8) {
+      __builtin_memcpy(p, u, 16);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 7; ++k)
+        if (k < left) reinterpret_cast<uint16_t*>(p)[k] = static_cast<uint16_t>(u[k / 2] >> (16 * (k % 2)));
+    }
   }
 }
 
+// B's row (a column of the result) that row r of the instruction's tile j
+// stands for.  A lane has four consecutive rows of the instruction, r = 4 g ..
+// 4 g + 3, of every j.  F32 results take them as they are: four lanes write 64
+// bytes of a row.  BF16 results make two j neighbours, eight consecutive
+// columns of a lane, so that four lanes again write 64 bytes together.
+template <bool WIDE>
+__device__ __forceinline__ int b_row(int j, int r) {
+  return WIDE ? 16 * j + r : 32 * (j / 2) + 8 * (r >> 2) + 4 * (j % 2) + (r & 3);
+}
 // The permutation of the 16-byte chunks of a row in LDS.  Sixteen lanes read a
 // chunk of 16 rows together; two rows are 256 bytes, one pass over the banks,
-// so the chunks of the 8 pairs of rows have to differ: consecutive rows for A,
-// rows {0, 1, 2, 3} + 4 j + SPAN * {0, 1, 2, 3} for B.
+// so the chunks of the 8 pairs of rows have to differ: of consecutive rows, or
+// of rows b_row(j, 0 .. 15).
 __device__ __forceinline__ int a_swizzle(int row) { return (row >> 1) & 7; }
-template <int SPAN>
+template <bool WIDE>
 __device__ __forceinline__ int b_swizzle(int row) {
-  return ((row >> 1) & 1) | ((row / SPAN & 3) << 1);
+  return WIDE ? a_swizzle(row) : ((row >> 1) & 1) | ((row >> 3 & 3) << 1);
 }
 
 // Row offset i of the list, kept inside [0, most] and above the one before.
@@ -204,14 +207,14 @@ template <int BM, int BN, int WM, int WN, bool SB, bool WIDE>
 __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmArgs a) {
   constexpr int NW = WM * WN;
   constexpr int MT = BM / WM / 16, NT = BN / WN / 16;  // 16x16 tiles of a wave
-  constexpr int SPAN = 4 * NT;                         // consecutive columns of a lane
   constexpr int OPB = BM * 128;
-  constexpr int SCALES = (BM + BN) * 128;              // scales of A's rows, then of B's
-  constexpr int STAGE = SCALES + (BM + (SB ? BN : 0)) * 4;
+  constexpr int STAGE = (BM + BN) * 128;
+  constexpr int SCALES = 2 * STAGE;                    // scales of A's rows, then of B's, of three k-tiles
+  constexpr int SCALE_STAGE = BM * 4 + (SB ? BN * 4 : 256);
   constexpr int IA = BM / 8 / NW, IB = BN / 8 / NW;    // copies of 8 rows, per wave
-  static_assert(IA * 8 * NW == BM && IB * 8 * NW == BN && 2 * STAGE <= 160 * 1024, "tile");
-  static_assert(BM / 64 + (SB ? BN / 64 : 0) <= 2 * NW && BN / WN <= 128, "scale copies");
-  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+  static_assert(IA * 8 * NW == BM && IB * 8 * NW == BN && SCALES + 3 * SCALE_STAGE <= 160 * 1024, "tile");
+  static_assert(BN / WN <= 128 && NT % 2 == 0, "a wave's columns lie in one block of B");
+  __shared__ __attribute__((aligned(1024))) char smem[SCALES + 3 * SCALE_STAGE];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
@@ -243,7 +246,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
   const char* A = a.a.codes + amat * a.a.stride + m0 * a.a.ld + static_cast<int64_t>(kb0) * 128;
   const char* B = a.b.codes + bmat * a.b.stride + n0 * a.b.ld + static_cast<int64_t>(kb0) * 128;
   const float* SA = a.a.scales + amat * a.a.scale_stride + kb0 * a.a.scale_ld + m0;
-  const float* SB0 = a.b.scales + bmat * a.b.scale_stride + kb0 * a.b.scale_ld;
+  const float* SB0 = a.b.scales + bmat * a.b.scale_stride + kb0 * a.b.scale_ld + (SB ? n0 : n0 >> 7);
 
   // copies: lane l of an instruction fills slot l % 8 of row l / 8, and a
   // wave's instructions are STEP rows apart; rows behind the matrix repeat its
@@ -251,121 +254,151 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
   // they are used, two instructions each: held, they cost the registers that
   // keep the loop free of scratch memory.
   constexpr int STEP = 8 * NW;
-  static_assert(STEP % 16 == 0 && (STEP / SPAN == 2 || STEP / SPAN == 4), "the swizzles repeat");
+  static_assert(STEP % 32 == 0, "the swizzles repeat");
   const int row8 = wave * 8 + (lane >> 3);
   const uint32_t chunk_a = ((lane & 7) ^ a_swizzle(row8)) << 4;
-  const uint32_t chunk_b = ((lane & 7) ^ b_swizzle<SPAN>(row8)) << 4;
+  const uint32_t chunk_b = ((lane & 7) ^ b_swizzle<WIDE>(row8)) << 4;
   const int last_a = a.M - 1 - m0, last_b = a.N - 1 - n0;
   const uint32_t lda = static_cast<uint32_t>(a.a.ld), ldb = static_cast<uint32_t>(a.b.ld);
   const uint32_t lds0 = lds_address(smem);
-  auto copy = [&](int kt, int stage) {
+  // scales: 64 of A's rows, or of B's, for a wave (256 x 256 and 128 x 128: one
+  // instruction each); waves that are left repeat the last one's
+  constexpr int kScaleCopies = BM / 64 + (SB ? BN / 64 : 1);
+  static_assert(kScaleCopies <= NW, "one copy of scales for a wave");
+  const int slot = min(wave, kScaleCopies - 1);
+  const bool of_a = slot < BM / 64;
+  const float* const scales = of_a ? SA : SB0;
+  const int64_t scale_ld = of_a ? a.a.scale_ld : a.b.scale_ld;
+  const uint32_t ofs_s = 4 * (of_a ? min(slot * 64 + lane, last_a)
+                                   : SB ? min(slot * 64 - BM + lane, last_b) : min(lane, last_b >> 7));
+  auto copy = [&](int kt, uint32_t scale_stage) __attribute__((always_inline)) {
     const char* pa = A + static_cast<int64_t>(kt) * 128;
     const char* pb = B + static_cast<int64_t>(kt) * 128;
-    const uint32_t l = lds0 + stage * STAGE + wave * 1024;
+    const uint32_t l = lds0 + (kt & 1) * STAGE;
+    int row = row8;
+    asm volatile("" : "+v"(row));  // not before the loop: eight registers
 #pragma unroll
     for (int r = 0; r < IA; ++r)
-      copy16(pa, __umul24(min(row8 + r * STEP, last_a), lda) + chunk_a, l + r * STEP * 128);
+      copy16(pa, __umul24(min(row + r * STEP, last_a), lda) + chunk_a, l + wave * 1024 + r * STEP * 128);
 #pragma unroll
     for (int r = 0; r < IB; ++r)
-      copy16(pb, __umul24(min(row8 + r * STEP, last_b), ldb) + (chunk_b ^ (STEP / SPAN == 2 && r % 2 ? 64 : 0)),
-             l + OPB + r * STEP * 128);
-    // the scales, 64 rows an instruction
-#pragma unroll
-    for (int r = 0; r < (BM / 64 + (SB ? BN / 64 : 0) + NW - 1) / NW; ++r) {
-      const int q = wave + r * NW;
-      if (q < BM / 64) {
-        copy4(reinterpret_cast<const char*>(SA + kt * a.a.scale_ld), 4 * min(q * 64 + lane, last_a),
-              lds0 + stage * STAGE + SCALES + q * 256);
-      } else if (SB && q < BM / 64 + BN / 64) {
-        copy4(reinterpret_cast<const char*>(SB0 + kt * a.b.scale_ld + n0), 4 * min(q * 64 - BM + lane, last_b),
-              lds0 + stage * STAGE + SCALES + q * 256);
-      }
-    }
+      copy16(pb, __umul24(min(row + r * STEP, last_b), ldb) + chunk_b, l + OPB + wave * 1024 + r * STEP * 128);
+    copy4(reinterpret_cast<const char*>(scales + kt * scale_ld), ofs_s, lds0 + scale_stage + slot * 256);
   };
 
   const int wm = wave / WN, wn = wave - wm * WN;
   const int l15 = lane & 15, g = lane >> 4;
   const int arow = wm * (BM / WM) + l15;
-  const int brow = wn * (BN / WN) + (l15 >> 2) * SPAN + (l15 & 3);  // tile j adds 4 j
-  const int sbn = min(n0 + wn * (BN / WN), a.N - 1) >> 7;  // block row of B, square blocks
+  const int brow = wn * (BN / WN) + b_row<WIDE>(0, l15);
   f32x4 acc[MT][NT];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 
-  // a lane's 32 codes of a row: chunks g and g + 4.  (Tile rows 16 apart, and
-  // B's rows 4 j apart, share the swizzle up to b_swizzle's lowest bit, which
-  // 4 j leaves alone.)
+  // a lane's 32 codes of a row: chunks g and g + 4
   const uint32_t a_lo = arow * 128 + ((g ^ a_swizzle(arow)) << 4), a_hi = a_lo ^ 64;
-  const uint32_t b_lo = OPB + brow * 128 + ((g ^ b_swizzle<SPAN>(brow)) << 4), b_hi = b_lo ^ 64;
-  const uint32_t a_scale = SCALES + arow * 4, b_scale = SCALES + (BM + wn * (BN / WN) + g * SPAN) * 4;
+  const uint32_t b_lo = OPB + brow * 128 + ((g ^ b_swizzle<WIDE>(brow)) << 4), b_hi = b_lo ^ 64;
+  const uint32_t a_scale = arow * 4;
+  const uint32_t b_scale = BM * 4 + (SB ? (wn * (BN / WN) + b_row<WIDE>(0, 4 * g)) * 4 : wn * (BN / WN) / 128 * 4);
 
-  if (nk > 0) copy(0, 0);
-  float sq = 0.0f;
-  if (!SB && nk > 0) sq = SB0[sbn];
-  wait_all();
-  for (int kt = 0; kt < nk; ++kt) {
-    const char* s = smem + (kt & 1) * STAGE;
-    const float sb = sq;
-    if (kt + 1 < nk) {
-      copy(kt + 1, (kt + 1) & 1);
-      if (!SB) sq = SB0[(kt + 1) * a.b.scale_ld + sbn];
-    }
-    Fragment<WIDE> fa[MT], fb[2];
-    float sa[MT];
-    f32x4 p[2][MT], w[2];
-    auto read_b = [&](int j) {
-      fb[j & 1].set(*reinterpret_cast<const i32x4*>(s + b_lo + 512 * j),
-                    *reinterpret_cast<const i32x4*>(s + b_hi + 512 * j));
-    };
-    auto add = [&](int i, int j) {  // a tile's sums, times their scales
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-        acc[i][j][r] = __builtin_fmaf(SB ? p[j & 1][i][r] * w[j & 1][r] : p[j & 1][i][r], sa[i], acc[i][j][r]);
-    };
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-      fa[i].set(*reinterpret_cast<const i32x4*>(s + a_lo + 2048 * i),
-                *reinterpret_cast<const i32x4*>(s + a_hi + 2048 * i));
-    read_b(0);
+  Fragment<WIDE> fa[MT], fb[2];
+  f32x4 p[2][MT], w[2];
+  float sa[MT], sa_next[MT];
+  auto read_a = [&](const char* s, int i) {
+    fa[i].set(*reinterpret_cast<const i32x4*>(s + a_lo + 2048 * i),
+              *reinterpret_cast<const i32x4*>(s + a_hi + 2048 * i));
+  };
+  auto read_b = [&](const char* s, int j) {
+    const int row = b_row<WIDE>(j, 0);  // 4 more rows, or 16 or 32 more, have the same swizzle
+    fb[j & 1].set(*reinterpret_cast<const i32x4*>(s + b_lo + 128 * row),
+                  *reinterpret_cast<const i32x4*>(s + b_hi + 128 * row));
+  };
+  auto read_scales = [&](const char* s) {
+    const float sb = SB ? 1.0f : *reinterpret_cast<const float*>(s + b_scale);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
-      sa[i] = *reinterpret_cast<const float*>(s + a_scale + 64 * i);
-      if (!SB) sa[i] *= sb;
+      sa_next[i] = *reinterpret_cast<const float*>(s + a_scale + 64 * i);
+      if (!SB) sa_next[i] *= sb;
     }
-    // The products of tile column j run while the sums of j - 1 are added and
-    // the codes of j + 1 come from LDS.  The order is pinned: left to itself
-    // the compiler adds each product at once and waits for it.
+  };
+  auto add = [&](int i, int j) {  // a tile's sums, times their scales
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      acc[i][j][r] = __builtin_fmaf(SB ? p[j & 1][i][r] * w[j & 1][r] : p[j & 1][i][r], sa[i], acc[i][j][r]);
+  };
+
+  // The products of tile column j run while the sums of j - 1 are added and
+  // the codes of j + 1 come from LDS.  In the last column's step every wave
+  // has read its k-tile: it waits for its copies of the next one, joins the
+  // barrier and reads the next one's first codes behind the last products.
+  // The order is pinned: left to itself the compiler adds each product at once
+  // and waits for it.
+  // (A wave may be one barrier ahead of another that still reads its k-tile's
+  // scales for B in the last step: they have three stages.)
+  uint32_t ss = SCALES, ss_next = SCALES + SCALE_STAGE;
+  auto block = [&](int kt, auto last) __attribute__((always_inline)) {
+    constexpr bool kMore = !decltype(last)::value;
+    const char* s = smem + (kt & 1) * STAGE;
+    const char* next = smem + (~kt & 1) * STAGE;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) sa[i] = sa_next[i];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      if (j + 1 < NT) read_b(j + 1);
-      if (SB) w[j & 1] = *reinterpret_cast<const f32x4*>(s + b_scale + 16 * j);
+      if (j + 1 < NT) {
+        read_b(s, j + 1);
+      } else if (kMore) {
+        wait_all();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (SB) w[j & 1] = *reinterpret_cast<const f32x4*>(smem + ss + b_scale + 4 * b_row<WIDE>(j, 0));
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         p[j & 1][i] = fb[j & 1] * fa[i];
         if (j > 0) add(i, j - 1);
+        if (kMore && j + 1 == NT) {
+          read_a(next, i);
+          if (i == 0) read_b(next, 0);
+          if (i == 1) read_scales(smem + ss_next);
+        }
         __builtin_amdgcn_sched_barrier(0);
+        if (kMore && j == 0 && i == 0) copy(kt + 1, ss_next);
       }
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) add(i, NT - 1);
+  };
+  if (nk > 0) {
+    copy(0, ss);
     wait_all();
+#pragma unroll
+    for (int i = 0; i < MT; ++i) read_a(smem, i);
+    read_b(smem, 0);
+    read_scales(smem + ss);
+    for (int kt = 0; kt + 1 < nk; ++kt) {
+      block(kt, std::false_type{});
+      ss = ss_next;
+      ss_next = ss_next == SCALES + 2 * SCALE_STAGE ? SCALES : ss_next + SCALE_STAGE;
+    }
+    block(nk - 1, std::true_type{});
   }
 
   const int64_t cmat = a.mode == GEMM_ROWS ? 0 : mat;
   char* C = a.c.ptrs ? static_cast<char*>(a.c.ptrs[cmat]) : a.c.base + cmat * a.c.stride_bytes;
-  const int n = n0 + wn * (BN / WN) + g * SPAN;
+  constexpr int RUN = WIDE ? 4 : 8;  // consecutive columns of a lane
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int m = m0 + arow + i * 16;
     if (m >= m1) continue;
-    float v[SPAN];
+    char* row = C + m * a.c.ld * (WIDE ? 4 : 2);
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+    for (int j = 0; j < NT; j += RUN / 4) {
+      const int n = n0 + wn * (BN / WN) + b_row<WIDE>(j, 4 * g);
+      float v[RUN];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[4 * j + r] = acc[i][j][r];
-    store_row<SPAN>(a.c, C + m * a.c.ld * (a.c.dtype ? 2 : 4), n, a.N - n, v, a.accumulate);
+      for (int r = 0; r < RUN; ++r) v[r] = acc[i][j + r / 4][r % 4];
+      store_run<WIDE>(row, n, a.N - n, v, a.accumulate);
+    }
   }
 }
 
