@@ -139,6 +139,23 @@ __device__ __forceinline__ void store_run(char* row, int64_t n, int left, const 
   }
 }
 
+// The same for four elements.
+template <bool WIDE>
+__device__ __forceinline__ void store_few(char* row, int64_t n, int left, const float* v, int accumulate) {
+  if (WIDE) {
+    store_run<true>(row, n, left, v, accumulate);
+    return;
+  }
+  const uint32_t u[2] = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+  if (left >= 4) {
+    __builtin_memcpy(row + 2 * n, u, 8);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      if (k < left) reinterpret_cast<uint16_t*>(row)[n + k] = static_cast<uint16_t>(u[k / 2] >> (16 * (k % 2)));
+  }
+}
+
 // B's row (a column of the result) that row r of the instruction's tile j
 // stands for.  A lane has four consecutive rows of the instruction, r = 4 g ..
 // 4 g + 3, of every j.  F32 results take them as they are: four lanes write 64
@@ -156,6 +173,10 @@ __device__ __forceinline__ int a_swizzle(int row) { return (row >> 1) & 7; }
 template <bool WIDE>
 __device__ __forceinline__ int b_swizzle(int row) {
   return WIDE ? a_swizzle(row) : ((row >> 1) & 1) | ((row >> 3 & 3) << 1);
+}
+
+__device__ __forceinline__ char* c_matrix(const MatBatch& c, int64_t i) {
+  return c.ptrs ? static_cast<char*>(c.ptrs[i]) : c.base + i * c.stride_bytes;
 }
 
 // Row offset i of the list, kept inside [0, most] and above the one before.
@@ -384,7 +405,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
   }
 
   const int64_t cmat = a.mode == GEMM_ROWS ? 0 : mat;
-  char* C = a.c.ptrs ? static_cast<char*>(a.c.ptrs[cmat]) : a.c.base + cmat * a.c.stride_bytes;
+  char* C = c_matrix(a.c, cmat);
   constexpr int RUN = WIDE ? 4 : 8;  // consecutive columns of a lane
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
@@ -399,6 +420,104 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
       for (int r = 0; r < RUN; ++r) v[r] = acc[i][j + r / 4][r % 4];
       store_run<WIDE>(row, n, a.N - n, v, a.accumulate);
     }
+  }
+}
+
+// Few rows (a token being decoded, or a few for each expert): B is read once
+// and that is the time.  A workgroup takes 16 rows of B; its waves take the
+// blocks of k in turn, each straight from memory into the registers that the
+// matrix instruction reads, kAhead blocks in flight, and their sums are added
+// in the order of the waves in LDS.  All of a 4096 x 4096 matrix is on its way
+// at once.  The rows of A, MT * 16 at a time, come out of L2.
+//
+// In ROWS a workgroup belongs to one expert, so that it needs two offsets and
+// no search; an expert with more than MT * 16 rows takes several passes.
+constexpr int kFewWaves = 8;
+constexpr int kFewThreads = 64 * kFewWaves;
+
+template <int MT, bool SB, bool WIDE>
+__global__ __launch_bounds__(kFewThreads) void few_rows_kernel(const BlockGemmArgs a) {
+  constexpr int kAhead = MT == 1 ? 4 : MT == 2 ? 2 : 1;
+  __shared__ f32x4 part[kFewWaves][MT][64];
+  const int lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int mat = blockIdx.x / a.tiles_n, n0 = (blockIdx.x - mat * a.tiles_n) * 16;
+  int first = 0, end = a.M;
+  if (a.mode == GEMM_ROWS) {
+    first = offset_at(a.offsets, mat, a.M);
+    end = offset_at(a.offsets, mat + 1, a.M);
+  }
+  const int nk = (a.K + 127) >> 7;
+  const int64_t amat = a.mode == GEMM_ROWS ? 0 : mat;
+  const char* B = a.b.codes + mat * a.b.stride + static_cast<int64_t>(min(n0 + l15, a.N - 1)) * a.b.ld + 16 * g;
+  const float* SB0 = a.b.scales + mat * a.b.scale_stride;
+  char* C = c_matrix(a.c, amat);
+  const int n = n0 + 4 * g;  // this lane's columns of the result
+  for (int m0 = first; m0 < end; m0 += MT * 16) {
+    const char* A[MT];
+    const float* SA[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int64_t m = min(m0 + i * 16 + l15, end - 1);
+      A[i] = a.a.codes + amat * a.a.stride + m * a.a.ld + 16 * g;
+      SA[i] = a.a.scales + amat * a.a.scale_stride + m;
+    }
+    f32x4 acc[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+    for (int kb0 = wave; kb0 < nk; kb0 += kFewWaves * kAhead) {
+      i32x4 bl[kAhead], bh[kAhead], al[kAhead][MT], ah[kAhead][MT];
+      float sa[kAhead][MT], sb[kAhead][SB ? 4 : 1];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int kb = kb0 + u * kFewWaves;
+        if (kb >= nk) break;
+        const int64_t k = static_cast<int64_t>(kb) * 128;
+        bl[u] = *reinterpret_cast<const i32x4*>(B + k);
+        bh[u] = *reinterpret_cast<const i32x4*>(B + k + 64);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          al[u][i] = *reinterpret_cast<const i32x4*>(A[i] + k);
+          ah[u][i] = *reinterpret_cast<const i32x4*>(A[i] + k + 64);
+          sa[u][i] = SA[i][kb * a.a.scale_ld];
+        }
+        if (SB) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) sb[u][r] = SB0[kb * a.b.scale_ld + min(n + r, a.N - 1)];
+        } else {
+          sb[u][0] = SB0[kb * a.b.scale_ld + (n0 >> 7)];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (kb0 + u * kFewWaves >= nk) break;
+        Fragment<WIDE> fb;
+        fb.set(bl[u], bh[u]);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          Fragment<WIDE> fa;
+          fa.set(al[u][i], ah[u][i]);
+          const f32x4 p = fb * fa;
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            acc[i][r] = __builtin_fmaf(SB ? p[r] * sb[u][r] : p[r], SB ? sa[u][i] : sa[u][i] * sb[u][0], acc[i][r]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) part[wave][i][lane] = acc[i];
+    __syncthreads();
+    if (wave < MT) {
+      f32x4 sum = part[0][wave][lane];
+#pragma unroll
+      for (int q = 1; q < kFewWaves; ++q) sum += part[q][wave][lane];
+      const int m = m0 + wave * 16 + l15;
+      if (m < end) {
+        const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
+        store_few<WIDE>(C + m * a.c.ld * (WIDE ? 4 : 2), n, a.N - n, v, a.accumulate);
+      }
+    }
+    if (m0 + MT * 16 < end) __syncthreads();
   }
 }
 
@@ -420,21 +539,42 @@ void launch(BlockGemmArgs& a, hipStream_t s) {
   }
 }
 
+template <int MT, bool WIDE>
+void launch_few(BlockGemmArgs& a, hipStream_t s) {
+  a.tiles_n = (a.N + 15) / 16;
+  const uint32_t g = static_cast<uint32_t>(a.tiles_n * a.count);
+  if (a.square) {
+    few_rows_kernel<MT, false, WIDE><<<g, kFewThreads, 0, s>>>(a);
+  } else {
+    few_rows_kernel<MT, true, WIDE><<<g, kFewThreads, 0, s>>>(a);
+  }
+}
+
+template <bool WIDE>
+void launch_typed(BlockGemmArgs& a, hipStream_t s) {
+  const int64_t rows = a.mode == GEMM_ROWS ? a.M / a.count : a.M;  // (on average)
+  if (a.mode != GEMM_REDUCE && rows <= 64 && a.count * ((a.N + 15) / 16) < int64_t{1} << 23) {
+    if (rows <= (a.mode == GEMM_ROWS ? 8 : 16)) {
+      launch_few<1, WIDE>(a, s);
+    } else if (rows <= (a.mode == GEMM_ROWS ? 24 : 32)) {
+      launch_few<2, WIDE>(a, s);
+    } else {
+      launch_few<4, WIDE>(a, s);
+    }
+  } else if (!WIDE && count_tiles(a, 256, 256) >= 200) {
+    launch<256, 256, 4, 2, false>(a, s);
+  } else if (WIDE && count_tiles(a, 256, 128) >= 200) {
+    launch<256, 128, 4, 2, true>(a, s);
+  } else {
+    launch<128, 128, 2, 2, WIDE>(a, s);
+  }
+}
+
 }  // namespace
 
 hipError_t launch_block_gemm(const BlockGemmArgs& args, hipStream_t s) {
   BlockGemmArgs a = args;
-  if (a.c.dtype) {
-    if (count_tiles(a, 256, 256) >= 200) {
-      launch<256, 256, 4, 2, false>(a, s);
-    } else {
-      launch<128, 128, 2, 2, false>(a, s);
-    }
-  } else if (count_tiles(a, 256, 128) >= 200) {
-    launch<256, 128, 4, 2, true>(a, s);
-  } else {
-    launch<128, 128, 2, 2, true>(a, s);
-  }
+  a.c.dtype ? launch_typed<false>(a, s) : launch_typed<true>(a, s);
   return hipGetLastError();
 }
 
