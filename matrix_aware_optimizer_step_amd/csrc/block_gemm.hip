@@ -47,9 +47,12 @@ __device__ __forceinline__ void copy4(const char* base, uint32_t off, uint32_t l
   asm volatile("global_load_lds_dword %0, %1" ::"v"(off), "s"(base), "{m0}"(__builtin_amdgcn_readfirstlane(l))
                : "memory");
 }
-// All vector loads and LDS accesses of this wave are done, then the barrier.
-__device__ __forceinline__ void wait_all() {
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+// All LDS accesses of this wave are done and all but its N newest vector loads,
+// then the barrier.
+template <int N>
+__device__ __forceinline__ void wait_all_but() {
+  static_assert(N >= 0 && N < 64, "vmcnt has six bits");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
 // One block's worth of a 16x16 tile from the 32 codes that each lane holds of a
@@ -224,18 +227,18 @@ constexpr int kGroupRows = 8;  // tile rows that are walked together, column by 
 
 // BM x BN tile, WM x WN waves of (BM/WM) x (BN/WN) each.  SB: B has a scale
 // for each row.
-template <int BM, int BN, int WM, int WN, bool SB, bool WIDE>
+template <int BM, int BN, int WM, int WN, int STAGES, bool SB, bool WIDE>
 __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmArgs a) {
   constexpr int NW = WM * WN;
   constexpr int MT = BM / WM / 16, NT = BN / WN / 16;  // 16x16 tiles of a wave
   constexpr int OPB = BM * 128;
   constexpr int STAGE = (BM + BN) * 128;
-  constexpr int SCALES = 2 * STAGE;                    // scales of A's rows, then of B's, of three k-tiles
+  constexpr int SCALES = STAGES * STAGE;               // scales of A's rows, then of B's, of STAGES + 1 k-tiles
   constexpr int SCALE_STAGE = BM * 4 + (SB ? BN * 4 : 256);
   constexpr int IA = BM / 8 / NW, IB = BN / 8 / NW;    // copies of 8 rows, per wave
-  static_assert(IA * 8 * NW == BM && IB * 8 * NW == BN && SCALES + 3 * SCALE_STAGE <= 160 * 1024, "tile");
+  static_assert(IA * 8 * NW == BM && IB * 8 * NW == BN && SCALES + (STAGES + 1) * SCALE_STAGE <= 160 * 1024, "tile");
   static_assert(BN / WN <= 128 && NT % 2 == 0, "a wave's columns lie in one block of B");
-  __shared__ __attribute__((aligned(1024))) char smem[SCALES + 3 * SCALE_STAGE];
+  __shared__ __attribute__((aligned(1024))) char smem[SCALES + (STAGES + 1) * SCALE_STAGE];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
@@ -292,10 +295,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
   const int64_t scale_ld = of_a ? a.a.scale_ld : a.b.scale_ld;
   const uint32_t ofs_s = 4 * (of_a ? min(slot * 64 + lane, last_a)
                                    : SB ? min(slot * 64 - BM + lane, last_b) : min(lane, last_b >> 7));
-  auto copy = [&](int kt, uint32_t scale_stage) __attribute__((always_inline)) {
+  auto copy = [&](int kt, uint32_t stage, uint32_t scale_stage) __attribute__((always_inline)) {
     const char* pa = A + static_cast<int64_t>(kt) * 128;
     const char* pb = B + static_cast<int64_t>(kt) * 128;
-    const uint32_t l = lds0 + (kt & 1) * STAGE;
+    const uint32_t l = lds0 + stage;
     int row = row8;
     asm volatile("" : "+v"(row));  // not before the loop: eight registers
 #pragma unroll
@@ -355,13 +358,22 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
   // barrier and reads the next one's first codes behind the last products.
   // The order is pinned: left to itself the compiler adds each product at once
   // and waits for it.
+  //
   // (A wave may be one barrier ahead of another that still reads its k-tile's
-  // scales for B in the last step: they have three stages.)
-  uint32_t ss = SCALES, ss_next = SCALES + SCALE_STAGE;
+  // scales for B in the last step: scales have a stage more than codes.)
+  constexpr int COPIES = IA + IB + 1;  // of a wave for a k-tile
+  auto after = [](uint32_t x, uint32_t step, uint32_t from, int n) { return x == from + (n - 1) * step ? from : x + step; };
+  uint32_t cs = 0, ss = SCALES;                    // stages that are read
+  uint32_t cw = 0, sw = SCALES;                    // and that are copied into
+  auto copy_next = [&](int kt) __attribute__((always_inline)) {
+    copy(kt, cw, sw);
+    cw = after(cw, STAGE, 0, STAGES);
+    sw = after(sw, SCALE_STAGE, SCALES, STAGES + 1);
+  };
   auto block = [&](int kt, auto last) __attribute__((always_inline)) {
     constexpr bool kMore = !decltype(last)::value;
-    const char* s = smem + (kt & 1) * STAGE;
-    const char* next = smem + (~kt & 1) * STAGE;
+    const char* s = smem + cs;
+    const uint32_t cs_next = after(cs, STAGE, 0, STAGES), ss_next = after(ss, SCALE_STAGE, SCALES, STAGES + 1);
 #pragma unroll
     for (int i = 0; i < MT; ++i) sa[i] = sa_next[i];
 #pragma unroll
@@ -369,7 +381,11 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
       if (j + 1 < NT) {
         read_b(s, j + 1);
       } else if (kMore) {
-        wait_all();
+        if (STAGES > 2 && kt + STAGES - 1 < nk) {
+          wait_all_but<(STAGES - 2) * COPIES>();
+        } else {
+          wait_all_but<0>();
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
       if (SB) w[j & 1] = *reinterpret_cast<const f32x4*>(smem + ss + b_scale + 4 * b_row<WIDE>(j, 0));
@@ -378,35 +394,60 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
         p[j & 1][i] = fb[j & 1] * fa[i];
         if (j > 0) add(i, j - 1);
         if (kMore && j + 1 == NT) {
-          read_a(next, i);
-          if (i == 0) read_b(next, 0);
+          read_a(smem + cs_next, i);
+          if (i == 0) read_b(smem + cs_next, 0);
           if (i == 1) read_scales(smem + ss_next);
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (kMore && j == 0 && i == 0) copy(kt + 1, ss_next);
+        if (kMore && j == 0 && i == 0) {
+          if (STAGES == 2 || kt + STAGES - 1 < nk) copy_next(kt + STAGES - 1);
+        }
       }
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) add(i, NT - 1);
+    cs = cs_next;
+    ss = ss_next;
   };
   if (nk > 0) {
-    copy(0, ss);
-    wait_all();
+#pragma unroll
+    for (int q = 0; q < STAGES - 1; ++q)
+      if (q < nk) copy_next(q);
+    if (STAGES > 2 && nk >= STAGES - 1) {
+      wait_all_but<(STAGES - 2) * COPIES>();
+    } else {
+      wait_all_but<0>();
+    }
 #pragma unroll
     for (int i = 0; i < MT; ++i) read_a(smem, i);
     read_b(smem, 0);
     read_scales(smem + ss);
-    for (int kt = 0; kt + 1 < nk; ++kt) {
-      block(kt, std::false_type{});
-      ss = ss_next;
-      ss_next = ss_next == SCALES + 2 * SCALE_STAGE ? SCALES : ss_next + SCALE_STAGE;
-    }
+    for (int kt = 0; kt + 1 < nk; ++kt) block(kt, std::false_type{});
     block(nk - 1, std::true_type{});
   }
 
   const int64_t cmat = a.mode == GEMM_ROWS ? 0 : mat;
   char* C = c_matrix(a.c, cmat);
   constexpr int RUN = WIDE ? 4 : 8;  // consecutive columns of a lane
+  const int n_first = n0 + wn * (BN / WN);
+  if (WIDE && a.accumulate && n_first + BN / WN <= a.N) {
+    // a row's old values are all on their way before the first is needed
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      const int m = m0 + arow + i * 16;
+      if (m >= m1) continue;
+      char* row = C + m * a.c.ld * 4;
+      f32x4 old[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) __builtin_memcpy(&old[j], row + 4 * (n_first + b_row<true>(j, 4 * g)), 16);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        old[j] += acc[i][j];
+        __builtin_memcpy(row + 4 * (n_first + b_row<true>(j, 4 * g)), &old[j], 16);
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
     const int m = m0 + arow + i * 16;
@@ -414,7 +455,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
     char* row = C + m * a.c.ld * (WIDE ? 4 : 2);
 #pragma unroll
     for (int j = 0; j < NT; j += RUN / 4) {
-      const int n = n0 + wn * (BN / WN) + b_row<WIDE>(j, 4 * g);
+      const int n = n_first + b_row<WIDE>(j, 4 * g);
       float v[RUN];
 #pragma unroll
       for (int r = 0; r < RUN; ++r) v[r] = acc[i][j + r / 4][r % 4];
@@ -424,7 +465,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
 }
 
 // Few rows (a token being decoded, or a few for each expert): B is read once
-// and that is the time.  A workgroup takes 16 rows of B; its waves take the
+// and that is the time.  A workgroup takes 16 rows of B; its W waves take the
 // blocks of k in turn, each straight from memory into the registers that the
 // matrix instruction reads, kAhead blocks in flight, and their sums are added
 // in the order of the waves in LDS.  All of a 4096 x 4096 matrix is on its way
@@ -432,13 +473,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
 //
 // In ROWS a workgroup belongs to one expert, so that it needs two offsets and
 // no search; an expert with more than MT * 16 rows takes several passes.
-constexpr int kFewWaves = 8;
-constexpr int kFewThreads = 64 * kFewWaves;
-
-template <int MT, bool SB, bool WIDE>
-__global__ __launch_bounds__(kFewThreads) void few_rows_kernel(const BlockGemmArgs a) {
-  constexpr int kAhead = MT == 1 ? 4 : MT == 2 ? 2 : 1;
-  __shared__ f32x4 part[kFewWaves][MT][64];
+template <int MT, int W, bool SB, bool WIDE>
+__global__ __launch_bounds__(64 * W) void few_rows_kernel(const BlockGemmArgs a) {
+  constexpr int kAhead = MT == 1 ? 4 : 2;
+  __shared__ f32x4 part[W][MT][64];
   const int lane = threadIdx.x & 63, l15 = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int mat = blockIdx.x / a.tiles_n, n0 = (blockIdx.x - mat * a.tiles_n) * 16;
@@ -465,12 +503,12 @@ __global__ __launch_bounds__(kFewThreads) void few_rows_kernel(const BlockGemmAr
     f32x4 acc[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) acc[i] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-    for (int kb0 = wave; kb0 < nk; kb0 += kFewWaves * kAhead) {
+    for (int kb0 = wave; kb0 < nk; kb0 += W * kAhead) {
       i32x4 bl[kAhead], bh[kAhead], al[kAhead][MT], ah[kAhead][MT];
       float sa[kAhead][MT], sb[kAhead][SB ? 4 : 1];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        const int kb = kb0 + u * kFewWaves;
+        const int kb = kb0 + u * W;
         if (kb >= nk) break;
         const int64_t k = static_cast<int64_t>(kb) * 128;
         bl[u] = *reinterpret_cast<const i32x4*>(B + k);
@@ -490,7 +528,7 @@ __global__ __launch_bounds__(kFewThreads) void few_rows_kernel(const BlockGemmAr
       }
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        if (kb0 + u * kFewWaves >= nk) break;
+        if (kb0 + u * W >= nk) break;
         Fragment<WIDE> fb;
         fb.set(bl[u], bh[u]);
 #pragma unroll
@@ -510,7 +548,7 @@ __global__ __launch_bounds__(kFewThreads) void few_rows_kernel(const BlockGemmAr
     if (wave < MT) {
       f32x4 sum = part[0][wave][lane];
 #pragma unroll
-      for (int q = 1; q < kFewWaves; ++q) sum += part[q][wave][lane];
+      for (int q = 1; q < W; ++q) sum += part[q][wave][lane];
       const int m = m0 + wave * 16 + l15;
       if (m < end) {
         const float v[4] = {sum[0], sum[1], sum[2], sum[3]};
@@ -529,44 +567,58 @@ int64_t count_tiles(BlockGemmArgs& a, int bm, int bn) {
   return a.total_tiles;
 }
 
-template <int BM, int BN, int WM, int WN, bool WIDE>
+template <int BM, int BN, int WM, int WN, int STAGES, bool WIDE>
 void launch(BlockGemmArgs& a, hipStream_t s) {
   const uint32_t g = static_cast<uint32_t>(count_tiles(a, BM, BN));
   if (a.square) {
-    gemm_kernel<BM, BN, WM, WN, false, WIDE><<<g, 64 * WM * WN, 0, s>>>(a);
+    gemm_kernel<BM, BN, WM, WN, STAGES, false, WIDE><<<g, 64 * WM * WN, 0, s>>>(a);
   } else {
-    gemm_kernel<BM, BN, WM, WN, true, WIDE><<<g, 64 * WM * WN, 0, s>>>(a);
+    gemm_kernel<BM, BN, WM, WN, STAGES, true, WIDE><<<g, 64 * WM * WN, 0, s>>>(a);
   }
 }
 
-template <int MT, bool WIDE>
+template <int MT, int W, bool WIDE>
 void launch_few(BlockGemmArgs& a, hipStream_t s) {
   a.tiles_n = (a.N + 15) / 16;
   const uint32_t g = static_cast<uint32_t>(a.tiles_n * a.count);
   if (a.square) {
-    few_rows_kernel<MT, false, WIDE><<<g, kFewThreads, 0, s>>>(a);
+    few_rows_kernel<MT, W, false, WIDE><<<g, 64 * W, 0, s>>>(a);
   } else {
-    few_rows_kernel<MT, true, WIDE><<<g, kFewThreads, 0, s>>>(a);
+    few_rows_kernel<MT, W, true, WIDE><<<g, 64 * W, 0, s>>>(a);
   }
 }
 
+// Which kernel and tile, by what was measured (us, bf16 results unless noted):
+//   1 .. 32 rows (8 .. 24 on an expert's average): few_rows_kernel; 16 x 4096 x
+//     4096 7.7 against 13.9 with tiles of 64;
+//   256 x 256 from 200 tiles on (4096^3: 64 against 82 with 128 x 128; at 128
+//     tiles, 2048 x 4096 x 4096, 59 against 43); with segments of rows from 512
+//     rows a segment on (512: 189 against 194; 128: 87 against 65);
+//   128 x 128 from 128 tiles on, with four stages in flight while there is no
+//     more than one tile for a compute unit (1024 x 4096 x 4096: 26 against 38
+//     with two, 35 with tiles of 64), with two stages and two workgroups on a
+//     compute unit above (2048 x 4096 x 4096: 43 against 49);
+//   64 x 64, four stages, below (256 x 4096 x 4096: 14 against 23 and 38).
+// F32 results gain nothing from larger tiles than 128 x 128 (8192 x 8192 x
+// 4096: 553 against 570 with 256 x 128).
 template <bool WIDE>
 void launch_typed(BlockGemmArgs& a, hipStream_t s) {
-  const int64_t rows = a.mode == GEMM_ROWS ? a.M / a.count : a.M;  // (on average)
-  if (a.mode != GEMM_REDUCE && rows <= 64 && a.count * ((a.N + 15) / 16) < int64_t{1} << 23) {
-    if (rows <= (a.mode == GEMM_ROWS ? 8 : 16)) {
-      launch_few<1, WIDE>(a, s);
-    } else if (rows <= (a.mode == GEMM_ROWS ? 24 : 32)) {
-      launch_few<2, WIDE>(a, s);
-    } else {
-      launch_few<4, WIDE>(a, s);
-    }
-  } else if (!WIDE && count_tiles(a, 256, 256) >= 200) {
-    launch<256, 256, 4, 2, false>(a, s);
-  } else if (WIDE && count_tiles(a, 256, 128) >= 200) {
-    launch<256, 128, 4, 2, true>(a, s);
+  const int64_t rows = a.mode == GEMM_ROWS ? a.M / a.count : a.M;  // of a segment, on average
+  const bool few = a.mode != GEMM_REDUCE && a.count * ((a.N + 15) / 16) < int64_t{1} << 23;
+  const bool deep = a.K >= 4096;
+  const bool large = count_tiles(a, 256, 256) >= 200 && (a.mode != GEMM_ROWS || rows >= 512);
+  if (few && rows <= (a.mode == GEMM_ROWS ? 8 : 16)) {
+    deep ? launch_few<1, 8, WIDE>(a, s) : launch_few<1, 4, WIDE>(a, s);
+  } else if (few && rows <= (a.mode == GEMM_ROWS ? 24 : 32)) {
+    deep ? launch_few<2, 8, WIDE>(a, s) : launch_few<2, 4, WIDE>(a, s);
+  } else if (!WIDE && large) {
+    launch<256, 256, 4, 2, 2, false>(a, s);
+  } else if (count_tiles(a, 128, 128) > 256) {
+    launch<128, 128, 2, 2, 2, WIDE>(a, s);
+  } else if (count_tiles(a, 128, 128) > 128) {
+    launch<128, 128, 4, 2, 4, WIDE>(a, s);
   } else {
-    launch<128, 128, 2, 2, WIDE>(a, s);
+    launch<64, 64, 2, 2, 4, WIDE>(a, s);
   }
 }
 
