@@ -33,10 +33,9 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
-def _same_device(device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+def _same_device(device, t, name) -> None:
+    if t is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
 
 
 def _enqueue(device, stream, fresh, fn, *args) -> None:
@@ -76,11 +75,12 @@ class BlockCodes:
         if codes.dtype != E4M3 or scales.dtype != torch.float32:
             raise TypeError("codes must be float8_e4m3fn and scales float32")
         _need(codes.dim() in (2, 3) and scales.dim() == codes.dim(), "codes and scales must both be 2-D or both 3-D")
-        _same_device(codes.device, scales=scales)
+        _same_device(codes.device, scales, "scales")
         rows, cols = codes.shape[-2:]
         wide, high = -(-cols // L.CODE_BLOCK), -(-rows // block_rows)
-        _need(tuple(scales.shape[-2:]) == (wide, high) and codes.shape[:-2] == scales.shape[:-2],
-              f"scales of {tuple(codes.shape)} codes must be {(*codes.shape[:-2], wide, high)}, not {tuple(scales.shape)}")
+        if tuple(scales.shape) != (*codes.shape[:-2], wide, high):
+            raise ValueError(f"scales of {tuple(codes.shape)} codes must be {(*codes.shape[:-2], wide, high)}, "
+                             f"not {tuple(scales.shape)}")
         # (a dimension of one element may carry any stride)
         _need(codes.stride(-1) == 1 or cols <= 1, "codes must be row-major (last stride 1)")
         _need(scales.stride(-1) == 1 or high <= 1, "the scales of a block column must be contiguous")
@@ -92,22 +92,30 @@ class BlockCodes:
         if rows and cols:
             end += (rows - 1) * ld + (codes.stride(0) * (codes.shape[0] - 1) if codes.dim() == 3 else 0)
             _need(end <= codes.untyped_storage().nbytes(), "the last row's padding lies outside of the codes' memory")
+        self._describe(codes, scales, block_rows, codes.shape[0] if codes.dim() == 3 else None, rows, cols, ld, scale_ld)
+
+    def _describe(self, codes, scales, block_rows, count, rows, cols, ld, scale_ld) -> None:
         self.codes, self.scales, self.block_rows = codes, scales, block_rows
         self.shape, self.device = codes.shape, codes.device
         self.rows, self.cols = rows, cols
-        self.count = codes.shape[0] if codes.dim() == 3 else 1
-        many = codes.dim() == 3
-        self.desc = L.MuonCodes(codes.data_ptr(), scales.data_ptr(), codes.stride(0) if many else 0,
-                                scales.stride(0) if many else 0, self.count, rows, cols, ld, scale_ld, block_rows, 0)
+        self.count = 1 if count is None else count
+        self.desc = L.MuonCodes(codes.data_ptr(), scales.data_ptr(), 0 if count is None else codes.stride(0),
+                                0 if count is None else scales.stride(0), self.count, rows, cols, ld, scale_ld,
+                                block_rows, 0)
 
     @classmethod
     def empty(cls, rows: int, cols: int, block_rows: int = 1, count: int | None = None, device="cuda") -> "BlockCodes":
         """Buffers for ``quantize(..., out=)`` to fill (whole blocks: it also writes the padding)."""
+        _need(block_rows in (1, L.CODE_BLOCK), "block_rows must be 1 or 128")
+        ld, high = _up(cols, L.CODE_BLOCK), -(-rows // block_rows)
+        wide = ld // L.CODE_BLOCK
         lead = () if count is None else (count,)
-        codes = torch.empty(*lead, rows, _up(cols, L.CODE_BLOCK), dtype=E4M3, device=device)
-        scales = torch.empty(*lead, -(-cols // L.CODE_BLOCK), -(-rows // block_rows), dtype=torch.float32,
-                             device=device)
-        return cls(codes[..., :cols], scales, block_rows)
+        codes = torch.empty((*lead, rows, ld), dtype=E4M3, device=device)
+        scales = torch.empty((*lead, wide, high), dtype=torch.float32, device=device)
+        self = cls.__new__(cls)
+        self._describe(codes if ld == cols else codes[..., :cols], scales, block_rows, count, rows, cols, max(ld, 1),
+                       max(high, 1))
+        return self
 
     def __getitem__(self, i: int) -> "BlockCodes":
         """Matrix i of a batch."""
@@ -140,47 +148,56 @@ def quantize(x, *, block_rows: int = 1, order: str = "rows", pairs: torch.Tensor
     """
     _need(order in ("rows", "cols", "both"), 'order must be "rows", "cols" or "both"')
     _need(block_rows in (1, L.CODE_BLOCK), "block_rows must be 1 or 128")
-    b = batch(x)
-    first = b.keep[-1]
-    device = first.device
-    k = 1
-    if isinstance(pairs, tuple):
-        pairs, k = pairs
-    if weights is not None:
-        _need(pairs is not None, "weights need pairs")
-        _need(weights.dim() == 2 and weights.shape[0] == b.rows, "weights must be [rows of x, k]")
-        _need(weights.dtype == torch.float32 and weights.is_contiguous(), "weights must be contiguous float32")
-        _need(k in (1, weights.shape[1]), "weights and k differ")
-        k = weights.shape[1]
-    rows = b.rows
+    if isinstance(x, torch.Tensor) and x.dim() == 2:
+        desc, owned, count, device = _matrix(x, "x"), [], None, x.device
+    else:
+        b = batch(x)
+        desc, owned, count, device = b.desc, b.owned, b.count, b.keep[-1].device
+    k, rows, cols = 1, desc.rows, desc.cols
     if pairs is not None:
+        if isinstance(pairs, tuple):
+            pairs, k = pairs
         _need(pairs.dtype == torch.int32 and pairs.dim() == 1 and pairs.is_contiguous(),
               "pairs must be a contiguous int32 vector")
-        _need(b.count == 1 and first.dim() == 2, "pairs take one matrix")
+        _need(count is None, "pairs take one matrix")
         _need(block_rows == 1, "pairs take blocks of one row")
+        _same_device(device, pairs, "pairs")
+        if weights is not None:
+            _need(weights.dim() == 2 and weights.shape[0] == rows, "weights must be [rows of x, k]")
+            _need(weights.dtype == torch.float32 and weights.is_contiguous(), "weights must be contiguous float32")
+            _need(k in (1, weights.shape[1]), "weights and k differ")
+            _same_device(device, weights, "weights")
+            k = weights.shape[1]
         rows = pairs.numel()
-    _same_device(device, pairs=pairs, weights=weights)
-    many = None if isinstance(first, torch.Tensor) and first.dim() == 2 and not isinstance(x, (list, tuple)) else b.count
+    else:
+        _need(weights is None, "weights need pairs")
     fresh = []
     if out is None:
-        shapes = [(rows, b.cols)] * (order != "cols") + [(b.cols, rows)] * (order != "rows")
-        got = [BlockCodes.empty(r, c, block_rows, many, device) for r, c in shapes]
-        fresh = [t for q in got for t in (q.codes, q.scales)]
+        q = None if order == "cols" else BlockCodes.empty(rows, cols, block_rows, count, device)
+        qt = None if order == "rows" else BlockCodes.empty(cols, rows, block_rows, count, device)
+        fresh = [t for one in (q, qt) if one is not None for t in (one.codes, one.scales)]
     else:
-        got = list(out) if order == "both" else [out]
-        _need(len(got) == (2 if order == "both" else 1) and all(isinstance(q, BlockCodes) for q in got),
-              "out must be a BlockCodes, or two of them for both orders")
-        for i, q in enumerate(got):
-            turned = order == "cols" or i == 1
-            _need((q.rows, q.cols) == ((b.cols, rows) if turned else (rows, b.cols)) and q.count == b.count and
-                  q.block_rows == block_rows, "out does not fit the codes")
-            _same_device(device, out=q.codes)
-    if rows and b.cols and b.count:
-        q = got[0].desc if order != "cols" else None
-        qt = got[-1].desc if order != "rows" else None
-        _enqueue(device, stream, fresh + b.owned, L.muon_block_quantize, b.desc,
-                 None if pairs is None else pairs.data_ptr(), None if weights is None else weights.data_ptr(), k, q, qt)
-    return tuple(got) if order == "both" else got[0]
+        q, qt = out if order == "both" else (None, out) if order == "cols" else (out, None)
+        for one, shape in ((q, (rows, cols)), (qt, (cols, rows))):
+            if one is not None:
+                _need(isinstance(one, BlockCodes) and (one.rows, one.cols) == shape and one.block_rows == block_rows and
+                      one.codes.dim() == (2 if count is None else 3) and one.count == (count or 1),
+                      "out must be BlockCodes of the codes' shape (a pair of them for both orders)")
+                _same_device(device, one.codes, "out")
+    if rows and cols and count != 0:
+        _enqueue(device, stream, fresh + owned, L.muon_block_quantize, desc,
+                 None if pairs is None else pairs.data_ptr(), None if weights is None else weights.data_ptr(), k,
+                 None if q is None else q.desc, None if qt is None else qt.desc)
+    return (q, qt) if order == "both" else q if qt is None else qt
+
+
+def _matrix(t, what) -> L.MuonBatch:
+    if t.dim() != 2 or not (t.stride(1) == 1 or t.shape[1] <= 1):
+        raise ValueError(f"{what} must be a row-major matrix (last stride 1)")
+    rows, cols = t.shape
+    ld = t.stride(0)
+    return L.MuonBatch(None, t.data_ptr(), 0, 1, rows, cols, ld if rows > 1 or ld > cols else max(cols, 1),
+                       dtype_code(t), 0)
 
 
 def _result(out, shape, dtype, accumulate, device):
@@ -188,9 +205,10 @@ def _result(out, shape, dtype, accumulate, device):
     if out is None:
         _need(not accumulate, "accumulate needs out")
         return torch.empty(shape, dtype=dtype, device=device), True
-    _need(tuple(out.shape) == tuple(shape), f"out must be {tuple(shape)}, not {tuple(out.shape)}")
+    if tuple(out.shape) != shape:
+        raise ValueError(f"out must be {shape}, not {tuple(out.shape)}")
     _need(out.stride(-1) == 1 or out.shape[-1] <= 1, "out must be row-major (last stride 1)")
-    _same_device(device, out=out)
+    _same_device(device, out, "out")
     if accumulate and out.dtype != torch.float32:
         raise TypeError("only a float32 result accumulates")
     return out, False
@@ -206,14 +224,14 @@ def _check_operands(a, b) -> None:
     if not (isinstance(a, BlockCodes) and isinstance(b, BlockCodes)):
         raise TypeError("a and b must be BlockCodes")
     _need(a.block_rows == 1, "a's blocks must have one row")
-    _need(a.cols == b.cols, f"a has {a.cols} columns and b {b.cols}")
-    _same_device(a.device, b=b.codes)
+    _need(a.cols == b.cols, "a and b differ in columns")
+    _same_device(a.device, b.codes, "b")
 
 
 def _check_offsets(offsets, device) -> None:
     _need(offsets.dtype == torch.int32 and offsets.dim() == 1 and offsets.is_contiguous() and offsets.numel() >= 2,
           "offsets must be a contiguous int32 vector of one more than the experts")
-    _same_device(device, offsets=offsets)
+    _same_device(device, offsets, "offsets")
 
 
 def block_matmul(a: BlockCodes, b: BlockCodes, *, out: torch.Tensor | None = None, dtype=torch.bfloat16,

@@ -23,12 +23,13 @@ or on ``stream``; there is no CPU path.
 
 from __future__ import annotations
 
+import functools
 from dataclasses import dataclass
 
 import torch
 
 from . import _lib as L
-from .blocks import _enqueue, _need, _same_device
+from .blocks import _enqueue, _matrix, _need, _same_device
 from .muon import dtype_code
 from .multi import StepControl, _settle
 
@@ -62,21 +63,29 @@ class Routing:
 def _check_logits(logits) -> None:
     _need(logits.dim() == 2, "logits must be [tokens, experts]")
     _need(logits.stride(1) == 1 or logits.shape[1] <= 1, "logits must be row-major (last stride 1)")
-    _need(1 <= logits.shape[1] <= L.MAX_EXPERTS, f"experts outside [1, {L.MAX_EXPERTS}]")
+    if not 1 <= logits.shape[1] <= L.MAX_EXPERTS:
+        raise ValueError(f"experts outside [1, {L.MAX_EXPERTS}]")
 
 
 def _ld(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
-def _vector(t, n, dtype, what, device) -> None:
-    if t is None:
-        return
+def _check(t, shape, dtype, what, device) -> None:
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, not {t.dtype}")
-    _need(tuple(t.shape) == n and t.is_contiguous(), f"{what} must be contiguous and {n}, not {tuple(t.shape)}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous and {tuple(shape)}, not {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{what} is on {t.device}, not on {device}")
+
+
+@functools.lru_cache(maxsize=256)
+def _sizes(tokens, experts, k, align, order):
+    """Rows of the order, and 32-bit words of the workspace."""
+    rows = L.muon_route_capacity(tokens, experts, k, align) if order else 0
+    _need(rows > 0 or not order, "align outside [1, 65536], or an order of more than 2^31-1 rows")
+    return rows, -(-L.muon_route_workspace(tokens, experts) // 4)
 
 
 def route(logits: torch.Tensor, k: int, *, bias: torch.Tensor | None = None, score: str = "softmax", groups: int = 1,
@@ -97,39 +106,43 @@ def route(logits: torch.Tensor, k: int, *, bias: torch.Tensor | None = None, sco
     _check_logits(logits)
     tokens, experts = logits.shape
     device = logits.device
-    _need(score in L.SCORES, f"score must be one of {sorted(L.SCORES)}")
-    _need(1 <= k <= min(L.MAX_CHOSEN, experts), f"k outside [1, min({L.MAX_CHOSEN}, experts)]")
-    _vector(bias, (experts,), torch.float32, "bias", device)
-    _vector(mask, (tokens,), torch.bool, "mask", device)
-    _vector(loads, (experts,), torch.int32, "loads", device)
-    capacity = L.muon_route_capacity(max(tokens, 1), experts, k, align) if order else 0
-    _need(capacity > 0 or not order, "align outside [1, 65536], or an order of more than 2^31-1 rows")
-    if not tokens:
-        capacity = -(-experts * (align - 1) // align) * align if order else 0
-    n = tokens * k
-    ints = torch.empty((2 * n + capacity + experts + 1) if order else n, dtype=torch.int32, device=device)
-    weights = torch.empty(tokens, k, dtype=torch.float32, device=device)
-    chosen = ints[:n].view(tokens, k)
-    slots = pairs = offsets = None
-    if order:
-        slots, pairs = ints[n:2 * n].view(tokens, k), ints[2 * n:2 * n + capacity]
-        offsets = ints[2 * n + capacity:]
-    found = Routing(chosen, weights, slots, pairs, offsets, score, bool(renormalize), float(scale))
-    desc = L.MuonRoute(logits.data_ptr(), _ld(logits), max(tokens, 1), experts, k, dtype_code(logits), L.SCORES[score],
-                       int(bool(renormalize)), groups, top_groups, group_best, align, scale)
+    if score not in L.SCORES:
+        raise ValueError(f"score must be one of {sorted(L.SCORES)}")
+    if not 1 <= k <= min(L.MAX_CHOSEN, experts):
+        raise ValueError(f"k outside [1, min({L.MAX_CHOSEN}, experts)]")
+    if bias is not None:
+        _check(bias, (experts,), torch.float32, "bias", device)
+    if mask is not None:
+        _check(mask, (tokens,), torch.bool, "mask", device)
+    if loads is not None:
+        _check(loads, (experts,), torch.int32, "loads", device)
+    rows, ws = _sizes(max(tokens, 1), experts, k, align, order)
     if tokens == 0:
-        _need(device.type == "cuda", "the tensors are not on a GPU (there is no CPU path)")
+        rows = -(-experts * (align - 1) // align) * align if order else 0
+    # one buffer: experts, slots, pairs, offsets, and a workspace on a multiple of 16 bytes
+    n = tokens * k
+    end = -(-(2 * n + rows + experts + 1) // 4) * 4 if order else -(-n // 4) * 4
+    ints = torch.empty(end + ws, dtype=torch.int32, device=device)
+    weights = torch.empty((tokens, k), dtype=torch.float32, device=device)
+    found = Routing(ints.as_strided((tokens, k), (k, 1)), weights,
+                    ints.as_strided((tokens, k), (k, 1), n) if order else None,
+                    ints.as_strided((rows,), (1,), 2 * n) if order else None,
+                    ints.as_strided((experts + 1,), (1,), 2 * n + rows) if order else None,
+                    score, bool(renormalize), float(scale))
+    if tokens == 0:
+        if device.type != "cuda":
+            raise RuntimeError("the tensors are not on a GPU (there is no CPU path)")
         if order:
-            pairs.fill_(NO_EXPERT)
-            offsets.zero_()
+            found.pairs.fill_(NO_EXPERT)
+            found.offsets.zero_()
         return found
-    need = L.muon_route_workspace(tokens, experts)
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    desc = L.MuonRoute(logits.data_ptr(), _ld(logits), tokens, experts, k, dtype_code(logits), L.SCORES[score],
+                       1 if renormalize else 0, groups, top_groups, group_best, align, scale)
     at = ints.data_ptr()
-    _enqueue(device, stream, [ints, weights, ws], L.muon_route, desc, None if bias is None else bias.data_ptr(),
+    _enqueue(device, stream, (ints, weights), L.muon_route, desc, None if bias is None else bias.data_ptr(),
              None if mask is None else mask.data_ptr(), at, weights.data_ptr(), at + 4 * n if order else None,
-             at + 8 * n if order else None, at + 8 * n + 4 * capacity if order else None,
-             None if loads is None else loads.data_ptr(), ws.data_ptr(), need)
+             at + 8 * n if order else None, at + 8 * n + 4 * rows if order else None,
+             None if loads is None else loads.data_ptr(), at + 4 * end, 4 * ws)
     return found
 
 
@@ -140,54 +153,52 @@ def route_backward(logits: torch.Tensor, routing: Routing, grad_weights: torch.T
     _check_logits(logits)
     device = logits.device
     shape = (logits.shape[0], routing.k)
-    _vector(routing.experts, shape, torch.int32, "routing.experts", device)
-    _vector(routing.weights, shape, torch.float32, "routing.weights", device)
-    _vector(grad_weights, shape, torch.float32, "grad_weights", device)
+    _check(routing.experts, shape, torch.int32, "routing.experts", device)
+    _check(routing.weights, shape, torch.float32, "routing.weights", device)
+    _check(grad_weights, shape, torch.float32, "grad_weights", device)
     made = out is None
     if made:
         out = torch.empty(logits.shape, dtype=logits.dtype, device=device)
     else:
         _need(out.shape == logits.shape and out.dtype == logits.dtype and (out.stride(1) == 1 or out.shape[1] <= 1),
               "out must have the logits' shape and type and last stride 1")
-        _same_device(device, out=out)
+        _same_device(device, out, "out")
     if logits.shape[0] == 0:
         return out
     desc = L.MuonRoute(logits.data_ptr(), _ld(logits), logits.shape[0], logits.shape[1], routing.k, dtype_code(logits),
                        L.SCORES[routing.score], int(routing.renormalize), 1, 1, 1, 1, routing.scale)
-    _enqueue(device, stream, [out] if made else [], L.muon_route_backward, desc, routing.experts.data_ptr(),
+    _enqueue(device, stream, (out,) if made else (), L.muon_route_backward, desc, routing.experts.data_ptr(),
              routing.weights.data_ptr(), grad_weights.data_ptr(), out.data_ptr(), _ld(out))
     return out
 
 
-def _rows(t, what) -> L.MuonBatch:
-    _need(t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1), f"{what} must be a row-major matrix")
-    return L.MuonBatch(None, t.data_ptr(), 0, 1, t.shape[0], t.shape[1], _ld(t), dtype_code(t), 0)
-
-
-def _check_slots(slots, y) -> None:
-    _need(slots.dim() == 2 and 1 <= slots.shape[1] <= L.MAX_CHOSEN, f"slots must be [tokens, 1 .. {L.MAX_CHOSEN}]")
-    _vector(slots, tuple(slots.shape), torch.int32, "slots", y.device)
+def _check_slots(slots, device) -> None:
+    if slots.dim() != 2 or not 1 <= slots.shape[1] <= L.MAX_CHOSEN:
+        raise ValueError(f"slots must be [tokens, 1 .. {L.MAX_CHOSEN}]")
+    _check(slots, slots.shape, torch.int32, "slots", device)
 
 
 def expert_sum(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None = None, *,
                out: torch.Tensor | None = None, dtype=None, stream=None) -> torch.Tensor:
     """Each token's sum of weights[t, j] * y[slots[t, j]] (weights None: ones),
     in fp32, rounded once to ``dtype`` (None: y's).  A slot of -1 adds nothing."""
-    desc = _rows(y, "y")
-    _check_slots(slots, y)
+    desc, device = _matrix(y, "y"), y.device
+    _check_slots(slots, device)
     tokens, k = slots.shape
-    _vector(weights, (tokens, k), torch.float32, "weights", y.device)
-    made = out is None
+    if weights is not None:
+        _check(weights, (tokens, k), torch.float32, "weights", device)
+    shape, made = (tokens, y.shape[1]), out is None
     if made:
-        out = torch.empty(tokens, y.shape[1], dtype=dtype or y.dtype, device=y.device)
-    _need(tuple(out.shape) == (tokens, y.shape[1]), f"out must be {(tokens, y.shape[1])}")
-    _same_device(y.device, out=out)
-    od = _rows(out, "out")
-    if out.numel() == 0:
+        out = torch.empty(shape, dtype=dtype or y.dtype, device=device)
+    elif tuple(out.shape) != shape:
+        raise ValueError(f"out must be {shape}, not {tuple(out.shape)}")
+    _same_device(device, out, "out")
+    od = _matrix(out, "out")
+    if tokens == 0 or shape[1] == 0:
         return out
     if y.shape[0] == 0:
         return out.zero_()
-    _enqueue(y.device, stream, [out] if made else [], L.muon_expert_sum, desc, slots.data_ptr(),
+    _enqueue(device, stream, (out,) if made else (), L.muon_expert_sum, desc, slots.data_ptr(),
              None if weights is None else weights.data_ptr(), k, od)
     return out
 
@@ -195,20 +206,22 @@ def expert_sum(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | Non
 def expert_dot(grad: torch.Tensor, y: torch.Tensor, slots: torch.Tensor, *, out: torch.Tensor | None = None,
                stream=None) -> torch.Tensor:
     """The gradient of ``expert_sum``'s weights: <grad[t], y[slots[t, j]]>, float32 [tokens, k]."""
-    gd, yd = _rows(grad, "grad"), _rows(y, "y")
-    _check_slots(slots, y)
+    gd, yd, device = _matrix(grad, "grad"), _matrix(y, "y"), y.device
+    _check_slots(slots, device)
     tokens, k = slots.shape
-    _need(tuple(grad.shape) == (tokens, y.shape[1]), f"grad must be {(tokens, y.shape[1])}")
-    _same_device(y.device, grad=grad)
+    if tuple(grad.shape) != (tokens, y.shape[1]):
+        raise ValueError(f"grad must be {(tokens, y.shape[1])}, not {tuple(grad.shape)}")
+    _same_device(device, grad, "grad")
     made = out is None
     if made:
-        out = torch.empty(tokens, k, dtype=torch.float32, device=y.device)
-    _vector(out, (tokens, k), torch.float32, "out", y.device)
+        out = torch.empty((tokens, k), dtype=torch.float32, device=device)
+    else:
+        _check(out, (tokens, k), torch.float32, "out", device)
     if out.numel() == 0:
         return out
     if y.numel() == 0:
         return out.zero_()
-    _enqueue(y.device, stream, [out] if made else [], L.muon_expert_dot, gd, yd, slots.data_ptr(), k, out.data_ptr())
+    _enqueue(device, stream, (out,) if made else (), L.muon_expert_dot, gd, yd, slots.data_ptr(), k, out.data_ptr())
     return out
 
 
@@ -224,7 +237,8 @@ class BalanceBias:
     """
 
     def __init__(self, experts: int, rate: float = 1e-3, device="cuda"):
-        _need(1 <= experts <= L.MAX_EXPERTS, f"experts outside [1, {L.MAX_EXPERTS}]")
+        if not 1 <= experts <= L.MAX_EXPERTS:
+            raise ValueError(f"experts outside [1, {L.MAX_EXPERTS}]")
         self.rate = float(rate)
         self.bias = torch.zeros(experts, dtype=torch.float32, device=device)
         self.loads = torch.zeros(experts, dtype=torch.int32, device=device)
