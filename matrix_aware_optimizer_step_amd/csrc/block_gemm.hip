@@ -73,7 +73,8 @@ struct Fragment<false> {
   __device__ __forceinline__ void set(const i32x4& lo, const i32x4& hi) {
     v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
   }
-  __device__ __forceinline__ f32x4 operator*(const Fragment& o) const {
+  static constexpr int kSteps = 1;
+  __device__ __forceinline__ f32x4 step(int, const Fragment& o, const f32x4&) const {
     const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v, o.v, zero, 0, 0, 0, 0, 0, 0);
   }
@@ -95,11 +96,10 @@ struct Fragment<true> {
     v[2] = eight(hi[0], hi[1]);
     v[3] = eight(hi[2], hi[3]);
   }
-  __device__ __forceinline__ f32x4 operator*(const Fragment& o) const {
-    f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[q], o.v[q], p, 0, 0, 0);
-    return p;
+  static constexpr int kSteps = 4;
+  __device__ __forceinline__ f32x4 step(int q, const Fragment& o, const f32x4& p) const {
+    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[q], o.v[q], q ? p : zero, 0, 0, 0);
   }
 };
 
@@ -329,15 +329,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
   Fragment<WIDE> fa[MT], fb[2];
   f32x4 p[2][MT], w[2];
   float sa[MT], sa_next[MT];
+  // codes as they lie in LDS, and as the matrix instruction takes them (for F32
+  // results that is a conversion, which waits for them: it comes later)
+  i32x4 raw_a[MT][2], raw_b[2];
   auto read_a = [&](const char* s, int i) {
-    fa[i].set(*reinterpret_cast<const i32x4*>(s + a_lo + 2048 * i),
-              *reinterpret_cast<const i32x4*>(s + a_hi + 2048 * i));
+    raw_a[i][0] = *reinterpret_cast<const i32x4*>(s + a_lo + 2048 * i);
+    raw_a[i][1] = *reinterpret_cast<const i32x4*>(s + a_hi + 2048 * i);
   };
+  auto set_a = [&](int i) { fa[i].set(raw_a[i][0], raw_a[i][1]); };
   auto read_b = [&](const char* s, int j) {
     const int row = b_row<WIDE>(j, 0);  // 4 more rows, or 16 or 32 more, have the same swizzle
-    fb[j & 1].set(*reinterpret_cast<const i32x4*>(s + b_lo + 128 * row),
-                  *reinterpret_cast<const i32x4*>(s + b_hi + 128 * row));
+    raw_b[0] = *reinterpret_cast<const i32x4*>(s + b_lo + 128 * row);
+    raw_b[1] = *reinterpret_cast<const i32x4*>(s + b_hi + 128 * row);
   };
+  auto set_b = [&](int j) { fb[j & 1].set(raw_b[0], raw_b[1]); };
   auto read_scales = [&](const char* s) {
     const float sb = SB ? 1.0f : *reinterpret_cast<const float*>(s + b_scale);
 #pragma unroll
@@ -380,6 +385,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
     for (int j = 0; j < NT; ++j) {
       if (j + 1 < NT) {
         read_b(s, j + 1);
+        if (!WIDE) set_b(j + 1);
       } else if (kMore) {
         if (STAGES > 2 && kt + STAGES - 1 < nk) {
           wait_all_but<(STAGES - 2) * COPIES>();
@@ -389,23 +395,51 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
         __builtin_amdgcn_sched_barrier(0);
       }
       if (SB) w[j & 1] = *reinterpret_cast<const f32x4*>(smem + ss + b_scale + 4 * b_row<WIDE>(j, 0));
+      constexpr int Q = Fragment<WIDE>::kSteps;
+      if (WIDE && kMore && j + 1 == NT) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        p[j & 1][i] = fb[j & 1] * fa[i];
-        if (j > 0) add(i, j - 1);
-        if (kMore && j + 1 == NT) {
-          read_a(smem + cs_next, i);
-          if (i == 0) read_b(smem + cs_next, 0);
-          if (i == 1) read_scales(smem + ss_next);
+        for (int i = 0; i < MT; ++i) read_a(smem + cs_next, i);
+        read_b(smem + cs_next, 0);
+        read_scales(smem + ss_next);
+      }
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          p[j & 1][i] = fb[j & 1].step(q, fa[i], p[j & 1][i]);  // (MT sums in turn: none waits for its own last one)
+          if (!WIDE) {
+            if (j > 0) add(i, j - 1);
+            if (kMore && j + 1 == NT) {
+              read_a(smem + cs_next, i);
+              set_a(i);
+              if (i == 0) {
+                read_b(smem + cs_next, 0);
+                set_b(0);
+              }
+              if (i == 1) read_scales(smem + ss_next);
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          if (kMore && j == 0 && q == 0 && i == 0) {
+            if (STAGES == 2 || kt + STAGES - 1 < nk) copy_next(kt + STAGES - 1);
+          }
         }
-        __builtin_amdgcn_sched_barrier(0);
-        if (kMore && j == 0 && i == 0) {
-          if (STAGES == 2 || kt + STAGES - 1 < nk) copy_next(kt + STAGES - 1);
+        if (WIDE) {
+#pragma unroll
+          for (int i = q * MT / Q; i < (q + 1) * MT / Q; ++i)
+            if (j > 0) add(i, j - 1);
+          if (q + 2 == Q && j + 1 < NT) set_b(j + 1);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < MT; ++i) add(i, NT - 1);
+    if (WIDE && kMore) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) set_a(i);
+      set_b(0);
+    }
     cs = cs_next;
     ss = ss_next;
   };
@@ -419,8 +453,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
       wait_all_but<0>();
     }
 #pragma unroll
-    for (int i = 0; i < MT; ++i) read_a(smem, i);
+    for (int i = 0; i < MT; ++i) {
+      read_a(smem, i);
+      set_a(i);
+    }
     read_b(smem, 0);
+    set_b(0);
     read_scales(smem + ss);
     for (int kt = 0; kt + 1 < nk; ++kt) block(kt, std::false_type{});
     block(nk - 1, std::true_type{});
@@ -535,7 +573,9 @@ __global__ __launch_bounds__(64 * W) void few_rows_kernel(const BlockGemmArgs a)
         for (int i = 0; i < MT; ++i) {
           Fragment<WIDE> fa;
           fa.set(al[u][i], ah[u][i]);
-          const f32x4 p = fb * fa;
+          f32x4 p;
+#pragma unroll
+          for (int q = 0; q < Fragment<WIDE>::kSteps; ++q) p = fb.step(q, fa, p);
 #pragma unroll
           for (int r = 0; r < 4; ++r)
             acc[i][r] = __builtin_fmaf(SB ? p[r] * sb[u][r] : p[r], SB ? sa[u][i] : sa[u][i] * sb[u][0], acc[i][r]);
