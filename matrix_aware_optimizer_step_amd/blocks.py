@@ -191,6 +191,36 @@ def quantize(x, *, block_rows: int = 1, order: str = "rows", pairs: torch.Tensor
     return (q, qt) if order == "both" else q if qt is None else qt
 
 
+class WeightCodes:
+    """The codes of a weight, or of several equal ones (an expert layer's), kept
+    in both orders and made anew from the weights by ``refresh()``.
+
+    ``weights``: a matrix, a batch [count, rows, cols], or a list of equal
+    matrices, bfloat16 or float32, read from the same storage every time.
+    ``codes`` are the weights' (the forward product reads them), ``transposed`` those
+    of their transposes (the gradient of a layer's input does), both with blocks of
+    128x128.  ``OptimizerStep(codes={...})`` refreshes after each of its steps.
+    """
+
+    def __init__(self, weights):
+        self.batch = batch(weights)
+        first = self.batch.keep[-1]
+        _need(self.batch.rows > 0 and self.batch.cols > 0 and self.batch.count > 0, "no weights")
+        count = None if isinstance(weights, torch.Tensor) and weights.dim() == 2 else self.batch.count
+        device = first.device
+        self.device = device
+        self.codes = BlockCodes.empty(self.batch.rows, self.batch.cols, L.CODE_BLOCK, count, device)
+        self.transposed = BlockCodes.empty(self.batch.cols, self.batch.rows, L.CODE_BLOCK, count, device)
+        self.refresh()
+        torch.cuda.current_stream(device).synchronize()  # any stream may use them from here on
+
+    def refresh(self, stream=None) -> None:
+        """Enqueues ``muon_block_quantize`` of the weights as they are then."""
+        kept = [self.codes.codes, self.codes.scales, self.transposed.codes, self.transposed.scales]
+        _enqueue(self.device, stream, kept + self.batch.owned, L.muon_block_quantize, self.batch.desc, None, None, 1,
+                 self.codes.desc, self.transposed.desc)
+
+
 def _matrix(t, what) -> L.MuonBatch:
     if t.dim() != 2 or not (t.stride(1) == 1 or t.shape[1] <= 1):
         raise ValueError(f"{what} must be a row-major matrix (last stride 1)")

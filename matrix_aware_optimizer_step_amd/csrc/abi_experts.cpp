@@ -26,7 +26,7 @@ constexpr int64_t kMaxWorkgroups = (int64_t{1} << 23) - 1;
 bool aligned(const void* p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// A batch of dense matrices.  `gathered`: pairs name its rows.
+// A batch of dense matrices.
 muon_status_t check_dense(const muon_batch_t* b, const char* name) {
   if (!b) return fail(MUON_ERR_INVALID_VALUE, "%s: descriptor is NULL", name);
   if (b->dtype != MUON_F32 && b->dtype != MUON_BF16)
@@ -248,8 +248,8 @@ int64_t muon_route_capacity(int64_t tokens, int64_t experts, int64_t k, int64_t 
 
 size_t muon_route_workspace(int64_t tokens, int64_t experts) {
   if (!route_sizes_ok(tokens, experts, 1, 1)) return 0;
-  // the counts of every 64 tokens, a byte each (no more than 64)
-  const size_t bytes = static_cast<size_t>(ceil_div(tokens, kRouteTokens) * (ceil_div(experts, 16) * 16));
+  // the counts of every 16 or 64 tokens, a byte each
+  const size_t bytes = static_cast<size_t>(ceil_div(tokens, route_group(tokens, experts)) * (ceil_div(experts, 16) * 16));
   return bytes < 256 ? 256 : bytes;
 }
 
@@ -271,7 +271,7 @@ muon_status_t muon_route(const muon_route_t* r, const float* bias, const uint8_t
     return fail(MUON_ERR_WORKSPACE, "workspace of %zu bytes given, %zu needed", ws_bytes, need);
   if (!aligned(workspace, 16)) return fail(MUON_ERR_WORKSPACE, "workspace must be 16-byte aligned");
   // 1024 lanes for 64 tokens
-  if (ceil_div(r->tokens, kRouteTokens) >= int64_t{1} << 22)
+  if (ceil_div(r->tokens, 64) >= int64_t{1} << 22)
     return fail(MUON_ERR_UNSUPPORTED, "%lld tokens are too many for one launch", (long long)r->tokens);
   RouteArgs a{};
   a.logits = static_cast<const char*>(r->logits);

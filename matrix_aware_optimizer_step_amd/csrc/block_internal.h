@@ -66,16 +66,20 @@ struct RouteArgs {
   int32_t* pairs;           // [capacity]
   int32_t* offsets;         // [experts + 1]
   int32_t* loads;           // [experts] or null
-  uint8_t* counts;          // [blocks of kRouteTokens tokens][experts rounded up to 16]
+  uint8_t* counts;          // [runs of `group` tokens][experts rounded up to 16]
   int64_t capacity;
   int32_t tokens, experts, k;
   int32_t dtype;            // of the logits: 0 = f32, 1 = bf16
   int32_t sigmoid, renormalize;
   int32_t groups, top_groups, group_best;
   int32_t align;
+  int32_t group;            // set by the launcher: 16 or 64
   float scale;
 };
-constexpr int kRouteTokens = 64;  // tokens of a workgroup, one bit each in an expert's mask
+// Tokens of a run, whose counts are one row of the workspace.
+constexpr int32_t route_group(int64_t tokens, int64_t experts) {
+  return tokens <= 64 || tokens > 16384 || experts > 256 ? 64 : 16;
+}
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
 
 struct RouteBackwardArgs {

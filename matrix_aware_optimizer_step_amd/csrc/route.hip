@@ -13,12 +13,16 @@
 // Equal inputs to the comparison give equal answers whatever the arithmetic:
 // where the keys are the logits themselves (no bias, one group or groups by
 // their best) they are compared as they are.  Where they are scores, rounded
-// to fp32, a token in which two keys that decide something lie within the
-// rounding is done again in fp64, one token in a thousand.
+// to fp32, keys that lie within the rounding of each other and decide something
+// are computed again in fp64: the few experts in question, one a lane, put in
+// order among themselves (a token in a thousand); or the whole token, where it
+// is a border between groups, or more experts than lanes.
 //
 // The order by expert needs no sort and no atomics on global memory: a token
 // chooses an expert at most once, so 64 tokens are one 64-bit mask for each
 // expert, and a pair's place among them is the number of bits below its own.
+
+#include <type_traits>
 
 #include "block_internal.h"
 
@@ -26,9 +30,18 @@ namespace muon {
 namespace {
 
 constexpr int kLanes = 16;
-constexpr int kRouteThreads = kRouteTokens * kLanes;
 constexpr int kPlanTokens = 256;  // tokens of a workgroup of the second kernel
-constexpr float kNear = 4e-6f;    // of a key's terms: more than two scores' rounding errors
+
+// Keys of fp32 scores that are further apart than this are in the right order.
+// A score is off by 2^-22 of itself (the exponential by an ulp, a sum and a
+// quotient by half an ulp each), a softmax also by 0.37 * 2^-24 (its argument's
+// rounding, e^-x x <= 0.37), and by its sum's rounding, the same factor for all
+// scores of a token: 36 additions at most, 2^-23 * 18, which shifts two keys by
+// that times the difference of their biases.  The addition of the bias is off by
+// half an ulp of the key.  Twice all that:
+__device__ __forceinline__ float margin(float key, float widest) {
+  return 6.6e-7f * fabsf(key) + 9.5e-6f * widest + 6e-8f;
+}
 
 __device__ __forceinline__ float inf() { return __builtin_inff(); }
 
@@ -46,14 +59,17 @@ __device__ __forceinline__ double rotated(double x) {
   const uint32_t lo = rotated<CTRL>(static_cast<int>(u)), hi = rotated<CTRL>(static_cast<int>(u >> 32));
   return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
+// The larger one (no operand is a NaN: tokens that hold one are set apart).
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return __builtin_fmax(a, b); }
+__device__ __forceinline__ int larger(int a, int b) { return max(a, b); }
 // Over a row of 16 lanes, in every one of them.
 template <typename T>
 __device__ __forceinline__ T row_max(T x) {
-  T y;
-  y = rotated<0x128>(x); x = x > y ? x : y;
-  y = rotated<0x124>(x); x = x > y ? x : y;
-  y = rotated<0x122>(x); x = x > y ? x : y;
-  y = rotated<0x121>(x); return x > y ? x : y;
+  x = larger(x, rotated<0x128>(x));
+  x = larger(x, rotated<0x124>(x));
+  x = larger(x, rotated<0x122>(x));
+  return larger(x, rotated<0x121>(x));
 }
 __device__ __forceinline__ int row_min(int x) {
   x = min(x, rotated<0x128>(x));
@@ -104,14 +120,16 @@ __device__ __forceinline__ void load(float* z, const char* row, int dtype, int f
 
 // What a token's 16 lanes found: lane j has the j-th best.
 struct Choice {
-  int expert;   // -1: none
-  float z;
-  bool near;    // two keys that decide something are too close for their type
+  int expert;    // -1: none
+  float z, bias; // its logit and bias
+  int found;     // lanes that hold a candidate: k, or more where some are as near as the k-th
+  bool near;     // the candidates' order, or who is among them, needs fp64
+  bool again;    // the whole token does
 };
 
 // The k best of a token.  T: type of the keys; SCORES: the keys are scores
 // (plus bias), else the logits.  `shared`: LDS floats of this token's own
-// (2 * kMaxExpertGroups of T).
+// (kMaxExpertGroups + 2 * kLanes of T).
 template <typename T, int V, bool SCORES>
 __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, const float* bias, int lane, T* shared) {
   const int first = lane * V;
@@ -122,7 +140,7 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, con
     if (!a.sigmoid) {
       float m = z[0];
 #pragma unroll
-      for (int v = 1; v < V; ++v) m = z[v] > m ? z[v] : m;
+      for (int v = 1; v < V; ++v) m = larger(m, z[v]);
       top = row_max(m);
       T sum = T(0);
 #pragma unroll
@@ -146,34 +164,54 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, con
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] = T(z[v]);
   }
-  bool near = false;
+  bool near = false, again = false;
   if (a.groups > 1) {
-    // the two best of each group: lanes own runs of experts that may cross
-    // group borders, so every lane offers its best two of each group it holds
     const int size = a.experts / a.groups;
     const int g0 = first / size, in0 = first - g0 * size;  // group of the lane's first expert, and its place there
-    for (int g = 0; g < a.groups; ++g) {
-      T b1 = -T(inf()), b2 = -T(inf());
+    if (size % V == 0) {
+      // every lane's experts are of one group, a group is size / V lanes: each
+      // lane's two best go to LDS, and lane g joins those of group g
+      T b1 = key[0], b2 = -T(inf());
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int in = first + v - g * size;
-        if (in >= 0 && in < size) {
-          if (key[v] > b1) {
-            b2 = b1;
-            b1 = key[v];
-          } else if (key[v] > b2) {
-            b2 = key[v];
-          }
+      for (int v = 1; v < V; ++v) {
+        b2 = larger(b2, key[v] < b1 ? key[v] : b1);
+        b1 = larger(b1, key[v]);
+      }
+      T* two = shared + kMaxExpertGroups;
+      two[2 * lane] = b1;
+      two[2 * lane + 1] = b2;
+      __builtin_amdgcn_wave_barrier();
+      if (lane < a.groups) {  // (no more groups than lanes)
+        const int lanes = size / V;
+        b1 = b2 = -T(inf());
+        for (int l = lane * lanes; l < (lane + 1) * lanes; ++l) {
+          const T x = two[2 * l], y = two[2 * l + 1];
+          b2 = larger(larger(b2, y), x < b1 ? x : b1);
+          b1 = larger(b1, x);
         }
+        shared[lane] = a.group_best > 1 && b2 > -T(inf()) ? b1 + b2 : b1;
       }
-      const T m1 = row_max(b1);
-      T score = m1;
-      if (a.group_best > 1) {
-        const int who = row_min(b1 == m1 ? lane : kLanes);  // the lane whose best is the group's
-        const T m2 = row_max(lane == who ? b2 : b1);
-        if (m2 > -T(inf())) score = m1 + m2;
+    } else {
+      // runs of experts that cross group borders: every lane offers its two
+      // best of each group
+      for (int g = 0; g < a.groups; ++g) {
+        T b1 = -T(inf()), b2 = -T(inf());
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const int in = first + v - g * size;
+          const T x = in >= 0 && in < size ? key[v] : -T(inf());
+          b2 = larger(b2, x < b1 ? x : b1);
+          b1 = larger(b1, x);
+        }
+        const T m1 = row_max(b1);
+        T score = m1;
+        if (a.group_best > 1) {
+          const int who = row_min(b1 == m1 ? lane : kLanes);  // the lane whose best is the group's
+          const T m2 = row_max(lane == who ? b2 : b1);
+          if (m2 > -T(inf())) score = m1 + m2;
+        }
+        shared[g] = score;  // every lane writes the same value
       }
-      shared[g] = score;  // every lane writes the same value
     }
     __builtin_amdgcn_wave_barrier();
     // a group stays if fewer than top_groups are better (or equal and before it)
@@ -193,8 +231,7 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, con
         high = mark > high ? mark : high;
       }
     }
-    if (SCORES && high > -T(inf()) && low - high <= T(2 * kNear) * (fabs(static_cast<float>(low)) + 2 * widest))
-      near = true;
+    if (SCORES && high > -T(inf()) && low - high <= T(2 * margin(static_cast<float>(low), 2 * widest))) again = true;
     int g = g0, in = in0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -207,15 +244,22 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, con
   }
   Choice c;
   c.expert = -1;
-  c.z = 0.0f;
+  c.z = c.bias = 0.0f;
   T before = T(0);
   float z_before = 0.0f, b_before = 0.0f;
-  for (int j = 0; j < a.k; ++j) {
+  int j = 0;
+  for (;; ++j) {
     T best = key[0];
 #pragma unroll
-    for (int v = 1; v < V; ++v) best = key[v] > best ? key[v] : best;
+    for (int v = 1; v < V; ++v) best = larger(best, key[v]);
     best = row_max(best);
     if (!(best > -T(inf()))) break;  // the same in all 16 lanes
+    const bool close = SCORES && sizeof(T) == 4 && j > 0 && before - best <= T(margin(static_cast<float>(best), widest));
+    if (j >= a.k && !close) break;
+    if (j == kLanes) {
+      again = true;
+      break;
+    }
     int at = V;
     float zv = 0.0f, bv = 0.0f;
 #pragma unroll
@@ -233,9 +277,7 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, con
     if (SCORES) {
       zv = row_max(mine ? zv : -inf());
       if (a.bias) bv = row_max(mine ? bv : -inf());
-      if (j > 0 && before - best <= T(kNear) * (fabs(static_cast<float>(best)) + widest) &&
-          !(zv == z_before && bv == b_before))
-        near = true;
+      if (close && !(zv == z_before && bv == b_before)) near = true;
       before = best;
       z_before = zv;
       b_before = bv;
@@ -245,18 +287,53 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, con
     if (lane == j) {
       c.expert = expert;
       c.z = zv;
+      c.bias = bv;
     }
   }
-  if (SCORES && sizeof(T) == 4) {  // and the last one against everything that is left
-    bool close = false;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      close = close || (key[v] > -T(inf()) && before - key[v] <= T(kNear) * (fabs(static_cast<float>(before)) + widest) &&
-                        !(z[v] == z_before && (!a.bias || bias[v] == b_before)));
-    near = near || row_max(close ? 1 : 0);
-  }
+  c.found = j;
   c.near = near;
+  c.again = again;
   return c;
+}
+
+// The candidates' order by their keys in fp64, one a lane.
+template <int V>
+__device__ __forceinline__ void put_in_order(const RouteArgs& a, const float* z, Choice& c, int lane, double* shared) {
+  double key = -inf();
+  if (a.sigmoid) {
+    if (lane < c.found) key = sigmoid(static_cast<double>(c.z));
+  } else {
+    float m = z[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) m = larger(m, z[v]);
+    m = row_max(m);
+    double sum = 0.0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) sum += exponential(static_cast<double>(z[v]) - m);
+    sum = row_sum(sum);
+    if (lane < c.found) key = exponential(static_cast<double>(c.z) - m) / sum;
+  }
+  key += c.bias;
+  int rank = 0;
+  shared[lane] = key;
+  int* experts = reinterpret_cast<int*>(shared + kLanes);
+  experts[lane] = c.expert;
+  __builtin_amdgcn_wave_barrier();
+  for (int o = 0; o < c.found; ++o) {
+    const double x = shared[o];
+    rank += x > key || (x == key && experts[o] < c.expert);
+  }
+  __builtin_amdgcn_wave_barrier();
+  float* logits = reinterpret_cast<float*>(shared);
+  if (lane < c.found) {
+    experts[rank] = c.expert;
+    logits[rank] = c.z;
+  }
+  __builtin_amdgcn_wave_barrier();
+  if (lane < c.found) {
+    c.expert = experts[lane];
+    c.z = logits[lane];
+  }
 }
 
 // Exclusive sums of the experts' rows, each rounded up to `align`, by one
@@ -294,9 +371,11 @@ __device__ __forceinline__ void write_rest(const RouteArgs& a, const int* total,
                                            int blocks) {
   const int threads = blockDim.x;
   if (a.pairs) {
-    if (a.align > 1)
-      for (int e = block; e < a.experts; e += blocks)
-        for (int r = base[e] + total[e] + threadIdx.x; r < base[e + 1]; r += threads) a.pairs[r] = -1;
+    if (a.align > 1) {  // a wave for an expert
+      const int waves = threads / 64;
+      for (int e = block * waves + (threadIdx.x >> 6); e < a.experts; e += blocks * waves)
+        for (int r = base[e] + total[e] + (threadIdx.x & 63); r < base[e + 1]; r += 64) a.pairs[r] = -1;
+    }
     for (int64_t r = base[a.experts] + static_cast<int64_t>(block) * threads + threadIdx.x; r < a.capacity;
          r += static_cast<int64_t>(blocks) * threads)
       a.pairs[r] = -1;
@@ -309,20 +388,21 @@ __device__ __forceinline__ void write_rest(const RouteArgs& a, const int* total,
   }
 }
 
-// 64 tokens in a workgroup of 64 * 16 lanes, or of half as many in two passes
-// (V = 32: the registers).
-template <int V>
-constexpr int kThreadsOf = V > 16 ? kRouteThreads / 2 : kRouteThreads;
+// TOKENS tokens in a workgroup of 16 lanes each; of 64 tokens in passes of 32
+// with V = 16 and of 16 with V = 32 (the registers).
+template <int V, int TOKENS>
+constexpr int kThreadsOf = TOKENS * kLanes / (TOKENS < 64 || V < 16 ? 1 : V / 8);
 
-template <int V, bool SCORES>
-__global__ __launch_bounds__(kThreadsOf<V>) void route_kernel(const RouteArgs a) {
-  constexpr int kThreads = kThreadsOf<V>;
+template <int V, int TOKENS, bool SCORES>
+__global__ __launch_bounds__((kThreadsOf<V, TOKENS>)) void route_kernel(const RouteArgs a) {
+  constexpr int kThreads = kThreadsOf<V, TOKENS>;
   __shared__ uint64_t mask[kMaxExperts];
   __shared__ int total[kMaxExperts], base[kMaxExperts + 1];
-  __shared__ int16_t found[kRouteTokens][kMaxChosen];
-  __shared__ double marks[kThreads / kLanes][SCORES ? kMaxExpertGroups : kMaxExpertGroups / 2];
+  __shared__ int16_t found[TOKENS][kMaxChosen];
+  using Mark = std::conditional_t<SCORES, double, float>;
+  __shared__ Mark marks[kThreads / kLanes][kMaxExpertGroups + 2 * kLanes];
   const int lane = threadIdx.x & (kLanes - 1);
-  const int64_t token0 = static_cast<int64_t>(blockIdx.x) * kRouteTokens;
+  const int64_t token0 = static_cast<int64_t>(blockIdx.x) * TOKENS;
   const bool plan = a.slots || a.loads;
   for (int e = threadIdx.x; e < a.experts; e += kThreads) mask[e] = 0;
   __syncthreads();
@@ -334,7 +414,7 @@ __global__ __launch_bounds__(kThreadsOf<V>) void route_kernel(const RouteArgs a)
     bad_bias = bad_bias || bias[v] != bias[v];
   }
 #pragma unroll 1
-  for (int local = threadIdx.x / kLanes; local < kRouteTokens; local += kThreads / kLanes) {
+  for (int local = threadIdx.x / kLanes; local < TOKENS; local += kThreads / kLanes) {
     const int64_t token = token0 + local;
     if (token >= a.tokens) break;
     const bool there = !a.mask || a.mask[token];
@@ -351,11 +431,13 @@ __global__ __launch_bounds__(kThreadsOf<V>) void route_kernel(const RouteArgs a)
       for (int v = 0; v < V; ++v) z[v] = -inf();
     }
     Choice c;
-    double* own = marks[threadIdx.x / kLanes];
+    Mark* own = marks[threadIdx.x / kLanes];
     c = choose<float, V, SCORES>(a, z, bias, lane, reinterpret_cast<float*>(own));
     if constexpr (SCORES) {
-      if (__ballot(c.near)) c = choose<double, V, true>(a, z, bias, lane, own);
+      if (c.near && !c.again) put_in_order<V>(a, z, c, lane, own);
+      if (c.again) c = choose<double, V, true>(a, z, bias, lane, own);
     }
+    if (lane >= a.k) c.expert = -1;
     // the weights, lane j those of the j-th
     const bool some = c.expert >= 0;
     float s = 0.0f;
@@ -368,7 +450,7 @@ __global__ __launch_bounds__(kThreadsOf<V>) void route_kernel(const RouteArgs a)
       if (!a.renormalize) {
         m = z[0];
 #pragma unroll
-        for (int v = 1; v < V; ++v) m = z[v] > m ? z[v] : m;
+        for (int v = 1; v < V; ++v) m = larger(m, z[v]);
       }
       m = row_max(m);
       if (!a.renormalize && m > -inf()) {
@@ -419,85 +501,97 @@ __global__ __launch_bounds__(kThreadsOf<V>) void route_kernel(const RouteArgs a)
   write_rest(a, total, base, 0, 1);
 }
 
-// The pairs' order from the counts of every 64 tokens and the chosen experts.
-// Each workgroup sums all counts by itself (they are few and in L2), 16
+// The pairs' order from the counts of every a.group tokens and the chosen experts.
+// Each workgroup sums all counts by itself (they are few and in L2), eight
 // experts for a thread.
 __global__ __launch_bounds__(1024) void plan_kernel(const RouteArgs a) {
-  constexpr int kParts = kPlanTokens / kRouteTokens;
+  constexpr int kParts = kPlanTokens / 64;
+  // expert e's sums lie at (e % 8) * kStride + e / 8: threads of a wave add to
+  // neighbouring words
+  constexpr int kStride = kMaxExperts / 8 + 1;
   __shared__ uint64_t mask[kParts][kMaxExperts];
   __shared__ int total[kMaxExperts], before[kMaxExperts], base[kMaxExperts + 1];
+  __shared__ int all_sums[8 * kStride], low_sums[8 * kStride];
   const int tid = threadIdx.x;
-  const int wide = (a.experts + 15) & ~15, chunks = wide / 16;  // 1 .. 32 chunks of 16 experts
-  const int rows = (a.tokens + kRouteTokens - 1) / kRouteTokens;
-  const int own = blockIdx.x * kParts;  // rows before this workgroup's tokens
+  const int wide = (a.experts + 15) & ~15, words = wide / 8;  // 2 .. 64 words of 8 experts
+  const int rows = (a.tokens + a.group - 1) / a.group;
+  const int own = blockIdx.x * (kPlanTokens / a.group);  // rows before this workgroup's tokens
+  // this workgroup's pairs, kept from here to the end
+  constexpr int kPairs = kPlanTokens * kMaxChosen / 1024;
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanTokens * a.k;
+  const int count = static_cast<int>(min(static_cast<int64_t>(kPlanTokens), a.tokens - static_cast<int64_t>(blockIdx.x) * kPlanTokens)) * a.k;
+  int mine[kPairs], local[kPairs];
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    const int at = tid + i * 1024;
+    mine[i] = a.slots && at < count ? a.chosen[first + at] : -1;
+    local[i] = at / a.k;
+  }
   for (int e = tid; e < kMaxExperts; e += 1024) {
-    total[e] = before[e] = 0;
 #pragma unroll
     for (int q = 0; q < kParts; ++q) mask[q][e] = 0;
   }
+  for (int e = tid; e < 8 * kStride; e += 1024) all_sums[e] = low_sums[e] = 0;
   __syncthreads();
   {
-    // thread = (row, chunk); the sums of its rows as two 16-bit counters a word
-    const int per = 1024 / chunks;
-    const int chunk = tid % chunks, row = tid / chunks;
+    // thread = (row, word); its sums as 16-bit counters, two to a register
+    const int per = 1024 / words;
+    const int row = tid / words, word = tid - row * words;
     if (row < per) {
-      for (int start = 0; start < rows; start += per * 64) {  // 64 rows of 64 tokens fit 16 bits
-        uint32_t all[8], low[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) all[i] = low[i] = 0;
-        const int end = min(rows, start + per * 64);
-#pragma unroll 4
+      for (int start = 0; start < rows; start += per * 512) {  // 512 rows of at most 64 tokens fit 16 bits
+        uint32_t all[4] = {0, 0, 0, 0}, low[4] = {0, 0, 0, 0};
+        const int end = min(rows, start + per * 512);
+#pragma unroll 8
         for (int r = start + row; r < end; r += per) {
-          const uint4 u = *reinterpret_cast<const uint4*>(a.counts + static_cast<int64_t>(r) * wide + chunk * 16);
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+          const uint2 u = *reinterpret_cast<const uint2*>(a.counts + static_cast<int64_t>(r) * wide + word * 8);
+          const uint32_t keep = r < own ? 0x00ff00ffu : 0;
+          const uint32_t w[4] = {u.x & 0x00ff00ffu, (u.x >> 8) & 0x00ff00ffu, u.y & 0x00ff00ffu,
+                                 (u.y >> 8) & 0x00ff00ffu};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t even = w[i] & 0x00ff00ffu, odd = (w[i] >> 8) & 0x00ff00ffu;
-            all[2 * i] += even;
-            all[2 * i + 1] += odd;
-            if (r < own) {
-              low[2 * i] += even;
-              low[2 * i + 1] += odd;
-            }
+            all[i] += w[i];
+            low[i] += w[i] & keep;
           }
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int e = chunk * 16 + 4 * (i / 2) + i % 2;
-          if (all[i] & 0xffffu) atomicAdd(&total[e], static_cast<int>(all[i] & 0xffffu));
-          if (all[i] >> 16) atomicAdd(&total[e + 2], static_cast<int>(all[i] >> 16));
-          if (low[i] & 0xffffu) atomicAdd(&before[e], static_cast<int>(low[i] & 0xffffu));
-          if (low[i] >> 16) atomicAdd(&before[e + 2], static_cast<int>(low[i] >> 16));
+          const int n = i / 4 * 2 + i % 2, shift = i % 4 / 2 * 16;
+          const int x = all[n] >> shift & 0xffffu, y = low[n] >> shift & 0xffffu;
+          if (x) atomicAdd(&all_sums[i * kStride + word], x);
+          if (y) atomicAdd(&low_sums[i * kStride + word], y);
         }
       }
     }
   }
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kPlanTokens * a.k;
-  const int64_t last = min(first + kPlanTokens * a.k, static_cast<int64_t>(a.tokens) * a.k);
   if (a.slots) {
-    for (int64_t p = first + tid; p < last; p += 1024) {
-      const int e = a.chosen[p];
-      const int t = static_cast<int>(p - first) / a.k;
-      if (e >= 0)
-        atomicOr(reinterpret_cast<uint32_t*>(&mask[t / kRouteTokens][e]) + (t >> 5 & 1), 1u << (t & 31));
-    }
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i)
+      if (mine[i] >= 0)
+        atomicOr(reinterpret_cast<uint32_t*>(&mask[local[i] / 64][mine[i]]) + (local[i] >> 5 & 1), 1u << (local[i] & 31));
+  }
+  __syncthreads();
+  for (int e = tid; e < a.experts; e += 1024) {
+    total[e] = all_sums[(e & 7) * kStride + (e >> 3)];
+    before[e] = low_sums[(e & 7) * kStride + (e >> 3)];
   }
   __syncthreads();
   if (tid < 64) scan_rows(total, base, a.experts, a.align);
   __syncthreads();
   if (a.slots) {
-    for (int64_t p = first + tid; p < last; p += 1024) {
-      const int e = a.chosen[p];
-      const int t = static_cast<int>(p - first) / a.k;
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i) {
+      const int at = tid + i * 1024;
+      if (at >= count) break;
+      const int e = mine[i], t = local[i];
       int slot = -1;
       if (e >= 0) {
         slot = base[e] + before[e];
-        const int part = t / kRouteTokens;
+        const int part = t / 64;
         for (int q = 0; q < part; ++q) slot += __builtin_popcountll(mask[q][e]);
-        slot += __builtin_popcountll(mask[part][e] & ((uint64_t{1} << (t % kRouteTokens)) - 1));
-        a.pairs[slot] = static_cast<int32_t>(p);
+        slot += __builtin_popcountll(mask[part][e] & ((uint64_t{1} << (t % 64)) - 1));
+        a.pairs[slot] = static_cast<int32_t>(first + at);
       }
-      a.slots[p] = slot;
+      a.slots[first + at] = slot;
     }
   }
   write_rest(a, total, base, blockIdx.x, gridDim.x);
@@ -534,7 +628,7 @@ __global__ __launch_bounds__(256) void backward_kernel(const RouteBackwardArgs a
     load<V>(z, row, a.dtype, first, a.experts);
     float m = z[0], sum = 0.0f;
 #pragma unroll
-    for (int v = 1; v < V; ++v) m = z[v] > m ? z[v] : m;
+    for (int v = 1; v < V; ++v) m = larger(m, z[v]);
     m = row_max(m);
     if (m > -inf()) {
 #pragma unroll
@@ -612,30 +706,45 @@ __global__ __launch_bounds__(kMaxExperts) void balance_kernel(const BalanceArgs 
   a.loads[e] = 0;
 }
 
-template <int V>
-void launch_kernel(const RouteArgs& a, bool scores, uint32_t blocks, hipStream_t s) {
-  if (scores) {
-    route_kernel<V, true><<<blocks, kThreadsOf<V>, 0, s>>>(a);
+template <int V, int TOKENS>
+void launch_kernel(const RouteArgs& a, hipStream_t s) {
+  const uint32_t blocks = static_cast<uint32_t>((a.tokens + TOKENS - 1) / TOKENS);
+  if (a.bias || (a.groups > 1 && a.group_best > 1)) {
+    route_kernel<V, TOKENS, true><<<blocks, kThreadsOf<V, TOKENS>, 0, s>>>(a);
   } else {
-    route_kernel<V, false><<<blocks, kThreadsOf<V>, 0, s>>>(a);
+    route_kernel<V, TOKENS, false><<<blocks, kThreadsOf<V, TOKENS>, 0, s>>>(a);
   }
+}
+
+// 16 tokens in a workgroup while 64 leave compute units without one (5003 tokens
+// of 256 experts: 34 us against 63), 64 where the second kernel would have too
+// many counts to sum, and where one workgroup does it all.
+template <int V>
+void launch_tokens(RouteArgs& a, hipStream_t s) {
+  a.group = route_group(a.tokens, a.experts);
+  if constexpr (V <= 16) {
+    if (a.group == 16) {
+      launch_kernel<V, 16>(a, s);
+      return;
+    }
+  }
+  launch_kernel<V, 64>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
-  const uint32_t blocks = static_cast<uint32_t>((a.tokens + kRouteTokens - 1) / kRouteTokens);
-  const bool scores = a.bias || (a.groups > 1 && a.group_best > 1);
+hipError_t launch_route(const RouteArgs& args, hipStream_t s) {
+  RouteArgs a = args;
   if (a.experts <= 64) {
-    launch_kernel<4>(a, scores, blocks, s);
+    launch_tokens<4>(a, s);
   } else if (a.experts <= 128) {
-    launch_kernel<8>(a, scores, blocks, s);
+    launch_tokens<8>(a, s);
   } else if (a.experts <= 256) {
-    launch_kernel<16>(a, scores, blocks, s);
+    launch_tokens<16>(a, s);
   } else {
-    launch_kernel<32>(a, scores, blocks, s);
+    launch_tokens<32>(a, s);
   }
-  if (blocks > 1 && (a.slots || a.loads))
+  if (a.tokens > 64 && (a.slots || a.loads))
     plan_kernel<<<(a.tokens + kPlanTokens - 1) / kPlanTokens, 1024, 0, s>>>(a);
   return hipGetLastError();
 }

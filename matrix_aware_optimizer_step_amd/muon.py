@@ -546,17 +546,30 @@ class OptimizerStep:
     whose update rounds a little differently from ``AdamW``'s (a reciprocal, off
     by 1e-7 of the step, for the division).  The norm takes contiguous gradients
     only; without it Muon's may have rows further apart.
+
+    ``codes``: ``{key: name}`` or ``{key: [names of equal matrices]}``: after every
+    step the 8-bit codes of these parameters are made anew (an expert layer's
+    matrices as one batch, in the list's order); ``codes[key]`` is their
+    ``WeightCodes``, from the start.  ``balance``: the ``BalanceBias`` objects of the
+    model's routers, moved after every step (not by a step that is skipped).
     """
 
     def __init__(self, named_params, *, compute: int = L.MUON_BF16, muon_lr: float = 3e-4,
                  muon_weight_decay: float = 0.1, adam_lr: float = 3e-4, adam_betas=(0.9, 0.999),
                  adam_eps: float = 1e-8, adam_weight_decay: float = 0.1, is_muon=is_muon_param,
                  max_grad_norm: float | None = None, skip_nonfinite: bool = False, adam_state_bits: int = 32,
-                 seed: int = 0):
-        from .multi import AdamWMulti, GradClip  # multi imports this module's helpers
+                 seed: int = 0, codes=None, balance=()):
+        from .blocks import WeightCodes  # these import this module's helpers
+        from .multi import AdamWMulti, GradClip
         if adam_state_bits not in (8, 32):
             raise ValueError("adam_state_bits must be 8 or 32")
         named_params = list(named_params)
+        by_name = {name: p for name, p, _ in named_params}
+        for key, names in (codes or {}).items():
+            missing = [n for n in ([names] if isinstance(names, str) else names) if n not in by_name]
+            if missing:
+                raise ValueError(f"codes[{key!r}]: no parameter named {missing[0]!r}")
+        self.balance = list(balance)
         shapes = {}
         adam = {}
         self.routing = {}
@@ -576,6 +589,11 @@ class OptimizerStep:
                                  max_norm=math.inf if max_grad_norm is None else max_grad_norm,
                                  skip_nonfinite=skip_nonfinite)
             control = self.clip.control
+        for b in self.balance:
+            if control is not None and b.bias.device != control.device:
+                raise ValueError("a balance bias is on another device than the gradients")
+        self.codes = {key: WeightCodes(by_name[names] if isinstance(names, str) else [by_name[n] for n in names])
+                      for key, names in (codes or {}).items()}
         if shapes:
             groups = [([p for p, _ in v], [g for _, g in v]) for v in shapes.values()]
             self.muon = MuonStep(groups, compute=compute, lr=muon_lr, weight_decay=muon_weight_decay, control=control)
@@ -597,13 +615,19 @@ class OptimizerStep:
             self.muon.step(stream=stream)
         for group in self.adamw:
             group.step(stream=stream)
+        for w in self.codes.values():
+            w.refresh(stream)
+        for b in self.balance:
+            b.step(None if self.clip is None else self.clip.control, stream)
 
     def state_dict(self) -> dict:
         """Everything a resumed run needs besides the weights: the Muon
         momentum, every AdamW group's moments and step count, the control
-        block's counts and lr factor, the hyperparameters and the routing they
-        belong to."""
-        return {"routing": dict(self.routing), "muon": None if self.muon is None else self.muon.state_dict(),
+        block's counts and lr factor, the balance biases, the hyperparameters
+        and the routing they belong to.  The codes are not part of it: refresh
+        them (``codes[key].refresh()``) once the weights are loaded."""
+        return {"balance": [b.state_dict() for b in self.balance],
+                "routing": dict(self.routing), "muon": None if self.muon is None else self.muon.state_dict(),
                 "adamw": [g.state_dict() for g in self.adamw],
                 "control": None if self.clip is None else self.clip.control.state_dict()}
 
@@ -615,6 +639,9 @@ class OptimizerStep:
         parts += zip(self.adamw, state["adamw"])
         if self.clip is not None and state.get("control") is not None:
             parts.append((self.clip.control, state["control"]))
+        if len(state.get("balance", [])) != len(self.balance):
+            raise ValueError("the state was saved for another number of balance biases")
+        parts += zip(self.balance, state.get("balance", []))
         for own, saved in parts:  # all of them before any is changed
             own.check_state(saved)
         for own, saved in parts:

@@ -1,0 +1,29 @@
+"""Register and scratch budget of the expert kernels (CPU: hipcc cross-compiles
+for gfx950 with the library's own flags): no spilled vector registers, no
+scratch memory, none of the packed fp32 instructions that the build turns off,
+and the products on the matrix instructions they are meant to use."""
+
+import re
+
+import pytest
+
+from tests.test_multi_resources import assembly
+
+
+@pytest.mark.parametrize("source,kernels,most", [("block_codes.hip", 10, 128), ("route.hip", 20, 512),
+                                                 ("expert_sum.hip", 2, 64), ("block_gemm.hip", 30, 256)])
+def test_kernels_use_no_scratch(tmp_path, source, kernels, most):
+    text = assembly(tmp_path, source)
+    found = 0
+    for block in re.split(r"\n\s+- \.", text):
+        vals = {k: int(v) for k, v in re.findall(r"\.(private_segment_fixed_size|vgpr_spill_count|vgpr_count):\s+(\d+)",
+                                                   block)}
+        if "vgpr_count" not in vals:
+            continue
+        found += 1
+        assert vals["private_segment_fixed_size"] == vals["vgpr_spill_count"] == 0, vals
+        assert vals["vgpr_count"] <= most, vals
+    assert found == kernels
+    assert not re.search(r"\bv_pk_(add|mul|fma)_f32\b", text)
+    if source == "block_gemm.hip":
+        assert "v_mfma_f32_16x16x128_f8f6f4" in text and "v_mfma_f32_16x16x32_bf16" in text
