@@ -188,21 +188,34 @@ __device__ __forceinline__ int offset_at(const int32_t* offsets, int64_t i, int 
   return o < 0 ? 0 : o > most ? most : o;
 }
 
-// Which expert and which rows the m-tile `tile` of a list of segments is:
-// every segment is cut into tiles of BM rows by itself.  A wave scans the
-// segments, 64 at a time.  False: behind the last tile.
+// Segments of rows, each cut into tiles of BM rows by itself.  A wave scans the
+// segments, 64 at a time.
+template <int BM>
+__device__ __forceinline__ int segment_tiles(const BlockGemmArgs& a, int64_t e, int& lo, int& hi) {
+  lo = hi = 0;
+  if (e < a.count) {
+    lo = offset_at(a.offsets, e, a.M);
+    hi = offset_at(a.offsets, e + 1, a.M);
+  }
+  return hi > lo ? (hi - lo + BM - 1) / BM : 0;
+}
+// The tiles of all segments.
+template <int BM>
+__device__ __forceinline__ int count_rows(const BlockGemmArgs& a) {
+  int lo, hi, sum = 0;
+  for (int64_t e = threadIdx.x & 63; e < a.count; e += 64) sum += segment_tiles<BM>(a, e, lo, hi);
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+  return __builtin_amdgcn_readfirstlane(sum);
+}
+// Which segment and which rows the m-tile `tile` is.  False: behind the last.
 template <int BM>
 __device__ __forceinline__ bool find_rows(const BlockGemmArgs& a, int tile, int& expert, int& first, int& end) {
   const int lane = threadIdx.x & 63;
   int before = 0;
   for (int64_t e0 = 0; e0 < a.count; e0 += 64) {
-    const int64_t e = e0 + lane;
-    int lo = 0, hi = 0;
-    if (e < a.count) {
-      lo = offset_at(a.offsets, e, a.M);
-      hi = offset_at(a.offsets, e + 1, a.M);
-    }
-    const int mine = hi > lo ? (hi - lo + BM - 1) / BM : 0;
+    int lo, hi;
+    const int mine = segment_tiles<BM>(a, e0 + lane, lo, hi);
     int sum = mine;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
@@ -224,6 +237,7 @@ __device__ __forceinline__ bool find_rows(const BlockGemmArgs& a, int tile, int&
 }
 
 constexpr int kGroupRows = 8;  // tile rows that are walked together, column by column
+constexpr int kChunkCols = 4;  // REDUCE: tile columns of a chunk of tiles that one XCD takes
 
 // BM x BN tile, WM x WN waves of (BM/WM) x (BN/WN) each.  SB: B has a scale
 // for each row.
@@ -242,18 +256,36 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
-  // workgroup ids reach the 8 XCDs round-robin: each XCD takes a contiguous
-  // range of the tiles, so that tiles that share rows share its L2
-  const int total = static_cast<int>(a.total_tiles);
-  const int xcd = blockIdx.x & 7;
-  int t = (blockIdx.x >> 3) + xcd * (total >> 3) + (xcd < (total & 7) ? xcd : (total & 7));
-  const int per = a.tiles_m * a.tiles_n;
-  const int mat = t / per;
-  t -= mat * per;
-  const int span = kGroupRows * a.tiles_n;
-  const int grp = t / span, in = t - grp * span;
-  const int high = min(kGroupRows, a.tiles_m - grp * kGroupRows);
-  const int tj = in / high, ti = grp * kGroupRows + in - tj * high;
+  // Workgroup ids reach the 8 XCDs round-robin: each XCD takes a contiguous
+  // range of the tiles, so that tiles that share rows share its L2.  The range
+  // is of the tiles that there are: with segments of rows the launch has more.
+  // Segments of k have tiles of unequal length: there the XCDs take small
+  // chunks of every segment in turn, and their shares come out even.
+  const int xcd = blockIdx.x & 7, turn = blockIdx.x >> 3;
+  int mat, ti, tj;
+  if (a.mode == GEMM_REDUCE) {
+    const int high = min(kGroupRows, a.tiles_m), size = high * kChunkCols;
+    const int across = (a.tiles_n + kChunkCols - 1) / kChunkCols, down = (a.tiles_m + high - 1) / high;
+    const int chunk = turn / size * 8 + xcd, in = turn % size;
+    mat = chunk / (across * down);
+    const int c = chunk - mat * (across * down);
+    ti = c / across * high + in % high;
+    tj = c % across * kChunkCols + in / high;
+    if (mat >= a.count || ti >= a.tiles_m || tj >= a.tiles_n) return;
+  } else {
+    const int tiles_m = a.mode == GEMM_ROWS ? count_rows<BM>(a) : a.tiles_m;
+    const int per = tiles_m * a.tiles_n;
+    const int total = per * (a.mode == GEMM_ROWS ? 1 : static_cast<int>(a.count));
+    if (turn >= (total >> 3) + (xcd < (total & 7) ? 1 : 0)) return;
+    int t = turn + xcd * (total >> 3) + min(xcd, total & 7);
+    mat = t / per;
+    t -= mat * per;
+    const int span = kGroupRows * a.tiles_n;
+    const int grp = t / span, in = t - grp * span;
+    const int high = min(kGroupRows, tiles_m - grp * kGroupRows);
+    tj = in / high;
+    ti = grp * kGroupRows + in - tj * high;
+  }
 
   // the tile's rows [m0, m1) of A, the matrix of B and C, and its blocks of k
   int m0 = ti * BM, m1 = a.M, which = mat, kb0 = 0, nk = (a.K + 127) >> 7;
@@ -603,13 +635,20 @@ __global__ __launch_bounds__(64 * W) void few_rows_kernel(const BlockGemmArgs a)
 int64_t count_tiles(BlockGemmArgs& a, int bm, int bn) {
   a.tiles_n = (a.N + bn - 1) / bn;
   a.tiles_m = a.mode == GEMM_ROWS ? static_cast<int32_t>(a.M / bm + a.count) : (a.M + bm - 1) / bm;
-  a.total_tiles = static_cast<int64_t>(a.tiles_m) * a.tiles_n * (a.mode == GEMM_ROWS ? 1 : a.count);
-  return a.total_tiles;
+  return static_cast<int64_t>(a.tiles_m) * a.tiles_n * (a.mode == GEMM_ROWS ? 1 : a.count);
+}
+// Workgroups of a launch (gemm_kernel's numbering of the tiles).
+int64_t count_workgroups(BlockGemmArgs& a, int bm, int bn) {
+  const int64_t tiles = count_tiles(a, bm, bn);
+  if (a.mode != GEMM_REDUCE) return tiles;
+  const int64_t high = a.tiles_m < kGroupRows ? a.tiles_m : kGroupRows;
+  const int64_t chunks = (a.tiles_n + kChunkCols - 1) / kChunkCols * ((a.tiles_m + high - 1) / high) * a.count;
+  return (chunks + 7) / 8 * 8 * high * kChunkCols;
 }
 
 template <int BM, int BN, int WM, int WN, int STAGES, bool WIDE>
 void launch(BlockGemmArgs& a, hipStream_t s) {
-  const uint32_t g = static_cast<uint32_t>(count_tiles(a, BM, BN));
+  const uint32_t g = static_cast<uint32_t>(count_workgroups(a, BM, BN));
   if (a.square) {
     gemm_kernel<BM, BN, WM, WN, STAGES, false, WIDE><<<g, 64 * WM * WN, 0, s>>>(a);
   } else {

@@ -49,7 +49,6 @@ struct BlockGemmArgs {
   int32_t square;          // b's blocks are 128x128
   int32_t accumulate;
   int32_t tiles_m, tiles_n;  // set by the launcher
-  int64_t total_tiles;       // set by the launcher
 };
 hipError_t launch_block_gemm(const BlockGemmArgs& a, hipStream_t stream);
 
