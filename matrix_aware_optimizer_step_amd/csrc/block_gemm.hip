@@ -237,7 +237,7 @@ __device__ __forceinline__ bool find_rows(const BlockGemmArgs& a, int tile, int&
 }
 
 constexpr int kGroupRows = 8;  // tile rows that are walked together, column by column
-constexpr int kChunkCols = 4;  // REDUCE: tile columns of a chunk of tiles that one XCD takes
+constexpr int kChunkCols = 2;  // REDUCE: tile columns of a chunk of tiles that one XCD takes
 
 // BM x BN tile, WM x WN waves of (BM/WM) x (BN/WN) each.  SB: B has a scale
 // for each row.
