@@ -81,9 +81,12 @@ typedef u32x4 u32x4_any2 __attribute__((aligned(2)));
 // Large matrices go past the caches in both directions (nontemporal accesses):
 // 16384 x 4096 bf16 in both orders 66 us against 72.  Small ones stay, for the
 // product that reads them next.
+// (A matrix's address may come out of a table, and would be read by flat
+// accesses: it is global memory.)
 template <bool STREAM, typename T>
 __device__ __forceinline__ T read(const T* p) {
-  return STREAM ? __builtin_nontemporal_load(p) : *p;
+  const auto g = (__attribute__((address_space(1))) const T*)(p);
+  return STREAM ? __builtin_nontemporal_load(g) : *g;
 }
 template <bool STREAM, typename T>
 __device__ __forceinline__ void write(T* p, const T& v) {
@@ -107,7 +110,8 @@ __device__ __forceinline__ void load8(float* v, const char* p, int left) {
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (k < left) w[k / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[k]) << (16 * (k % 2));
+        if (k < left)
+          w[k / 2] |= static_cast<uint32_t>(read<STREAM>(reinterpret_cast<const uint16_t*>(p) + k)) << (16 * (k % 2));
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = __builtin_bit_cast(float, k % 2 ? w[k / 2] & 0xffff0000u : w[k / 2] << 16);
@@ -124,7 +128,7 @@ __device__ __forceinline__ void load8(float* v, const char* p, int left) {
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (k < left) v[k] = reinterpret_cast<const float*>(p)[k];
+        if (k < left) v[k] = read<STREAM>(reinterpret_cast<const float*>(p) + k);
     }
   }
 }

@@ -28,6 +28,7 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -108,40 +109,44 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){a, b}, bf16x2));
 }
 
+// Results lie in global memory, also where the address comes out of a table
+// (flat accesses otherwise), at the alignment of their elements.
+template <typename T>
+using Global = __attribute__((address_space(1))) T*;
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+typedef i32x4 i32x4_any __attribute__((aligned(2)));
+typedef i32x2 i32x2_any __attribute__((aligned(2)));
+
 // 16 bytes of a row of the result from column n on, `left` elements of them
 // inside the matrix.
 template <bool WIDE>
 __device__ __forceinline__ void store_run(char* row, int64_t n, int left, const float* v, int accumulate) {
   if (WIDE) {
-    float* p = reinterpret_cast<float*>(row) + n;
+    Global<float> p = (Global<float>)(reinterpret_cast<float*>(row) + n);
     if (left >= 4) {
-      float4 u = make_float4(v[0], v[1], v[2], v[3]);
-      if (accumulate) {
-        float4 o;
-        __builtin_memcpy(&o, p, 16);
-        u = make_float4(o.x + u.x, o.y + u.y, o.z + u.z, o.w + u.w);
-      }
-      __builtin_memcpy(p, &u, 16);  // at any alignment
+      f32x4 u = {v[0], v[1], v[2], v[3]};
+      if (accumulate) u += *(Global<const f32x4_any>)(p);
+      *(Global<f32x4_any>)(p) = u;
     } else {
 #pragma unroll
       for (int k = 0; k < 3; ++k)
         if (k < left) p[k] = accumulate ? p[k] + v[k] : v[k];
     }
   } else {
-    char* p = row + 2 * n;
+    Global<uint16_t> p = (Global<uint16_t>)(reinterpret_cast<uint16_t*>(row) + n);
     uint32_t u[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) u[k] = bf16_pair(v[2 * k], v[2 * k + 1]);
     if (left >= 8) {
-      __builtin_memcpy(p, u, 16);
+      *(Global<i32x4_any>)(p) = (i32x4){static_cast<int>(u[0]), static_cast<int>(u[1]), static_cast<int>(u[2]),
+                                        static_cast<int>(u[3])};
     } else {
 #pragma unroll
       for (int k = 0; k < 7; ++k)
-        if (k < left) reinterpret_cast<uint16_t*>(p)[k] = static_cast<uint16_t>(u[k / 2] >> (16 * (k % 2)));
+        if (k < left) p[k] = static_cast<uint16_t>(u[k / 2] >> (16 * (k % 2)));
     }
   }
 }
-
 // The same for four elements.
 template <bool WIDE>
 __device__ __forceinline__ void store_few(char* row, int64_t n, int left, const float* v, int accumulate) {
@@ -149,13 +154,14 @@ __device__ __forceinline__ void store_few(char* row, int64_t n, int left, const 
     store_run<true>(row, n, left, v, accumulate);
     return;
   }
+  Global<uint16_t> p = (Global<uint16_t>)(reinterpret_cast<uint16_t*>(row) + n);
   const uint32_t u[2] = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
   if (left >= 4) {
-    __builtin_memcpy(row + 2 * n, u, 8);
+    *(Global<i32x2_any>)(p) = (i32x2){static_cast<int>(u[0]), static_cast<int>(u[1])};
   } else {
 #pragma unroll
     for (int k = 0; k < 3; ++k)
-      if (k < left) reinterpret_cast<uint16_t*>(row)[n + k] = static_cast<uint16_t>(u[k / 2] >> (16 * (k % 2)));
+      if (k < left) p[k] = static_cast<uint16_t>(u[k / 2] >> (16 * (k % 2)));
   }
 }
 
@@ -509,12 +515,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
       char* row = C + m * a.c.ld * 4;
       f32x4 old[NT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) __builtin_memcpy(&old[j], row + 4 * (n_first + b_row<true>(j, 4 * g)), 16);
+      for (int j = 0; j < NT; ++j) old[j] = *(Global<const f32x4_any>)(row + 4 * (n_first + b_row<true>(j, 4 * g)));
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        old[j] += acc[i][j];
-        __builtin_memcpy(row + 4 * (n_first + b_row<true>(j, 4 * g)), &old[j], 16);
-      }
+      for (int j = 0; j < NT; ++j)
+        *(Global<f32x4_any>)(row + 4 * (n_first + b_row<true>(j, 4 * g))) = old[j] + acc[i][j];
     }
     return;
   }
