@@ -376,7 +376,7 @@ muon_status_t muon_expert_sum(const muon_batch_t* y, const int32_t* slots, const
 
 muon_status_t muon_expert_dot(const muon_batch_t* grad, const muon_batch_t* y, const int32_t* slots, int64_t k,
                               float* dots, void* stream) {
-  const muon_status_t st = check_sum(y, grad, "grad", slots, k, 1);
+  const muon_status_t st = check_sum(y, grad, "grad", slots, k, ceil_div(k, 4));
   if (st != MUON_OK) return st;
   if (!dots || !aligned(dots, 4)) return fail(MUON_ERR_INVALID_VALUE, "dots must be a 4-byte aligned device address");
   ExpertSumArgs a{};

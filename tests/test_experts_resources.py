@@ -11,7 +11,7 @@ from tests.test_multi_resources import assembly
 
 
 @pytest.mark.parametrize("source,kernels,most", [("block_codes.hip", 20, 128), ("route.hip", 20, 512),
-                                                 ("expert_sum.hip", 2, 64), ("block_gemm.hip", 30, 256)])
+                                                 ("expert_sum.hip", 4, 64), ("block_gemm.hip", 30, 256)])
 def test_kernels_use_no_scratch(tmp_path, source, kernels, most):
     text = assembly(tmp_path, source)
     found = 0
