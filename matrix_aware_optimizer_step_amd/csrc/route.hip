@@ -118,23 +118,35 @@ __device__ __forceinline__ void load(float* z, const char* row, int dtype, int f
   }
 }
 
+__device__ __forceinline__ float logit(const char* row, int dtype, int e) {
+  return dtype ? __builtin_bit_cast(float, static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[e]) << 16)
+               : reinterpret_cast<const float*>(row)[e];
+}
+
+// fp64 exponentials are not computed side by side: the registers.
+template <typename T>
+__device__ __forceinline__ void one_by_one() {
+  if (sizeof(T) == 8) __builtin_amdgcn_sched_barrier(0);
+}
+
 // What a token's 16 lanes found: lane j has the j-th best.
 struct Choice {
   int expert;    // -1: none
   float z, bias; // its logit and bias
   int found;     // lanes that hold a candidate: k, or more where some are as near as the k-th
-  bool near;     // the candidates' order, or who is among them, needs fp64
+  bool near;     // candidates are close to each other: their order, or who is among the k, needs fp64
   bool again;    // the whole token does
 };
 
 // The k best of a token.  T: type of the keys; SCORES: the keys are scores
-// (plus bias), else the logits.  `shared`: LDS floats of this token's own
+// (plus bias, `bias` in LDS, `widest` its largest magnitude), else the logits.
+// `row`: the token's logits in memory.  `shared`: LDS of this token's own
 // (kMaxExpertGroups + 2 * kLanes of T).
 template <typename T, int V, bool SCORES>
-__device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, const float* bias, int lane, T* shared) {
+__device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, const float* bias, float widest,
+                                         const char* row, int lane, T* shared) {
   const int first = lane * V;
   T key[V];
-  float widest = 0.0f;  // largest bias
   if (SCORES) {
     T scale = T(1), top = T(0);
     if (!a.sigmoid) {
@@ -147,19 +159,17 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, con
       for (int v = 0; v < V; ++v) {
         key[v] = exponential(T(z[v]) - top);
         sum += key[v];
+        one_by_one<T>();
       }
       scale = T(1) / row_sum(sum);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       key[v] = a.sigmoid ? sigmoid(T(z[v])) : key[v] * scale;
-      if (a.bias) {
-        key[v] += T(bias[v]);
-        widest = fmaxf(widest, fabsf(bias[v]));
-      }
+      if (a.bias) key[v] += T(bias[first + v]);
       if (z[v] == -inf()) key[v] = -T(inf());
+      one_by_one<T>();
     }
-    if (a.bias) widest = row_max(widest);
   } else {
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] = T(z[v]);
@@ -244,9 +254,7 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, con
   }
   Choice c;
   c.expert = -1;
-  c.z = c.bias = 0.0f;
   T before = T(0);
-  float z_before = 0.0f, b_before = 0.0f;
   int j = 0;
   for (;; ++j) {
     T best = key[0];
@@ -260,35 +268,27 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, con
       again = true;
       break;
     }
+    near = near || close;
     int at = V;
-    float zv = 0.0f, bv = 0.0f;
 #pragma unroll
-    for (int v = V - 1; v >= 0; --v)
-      if (key[v] == best) {
-        at = v;
-        zv = z[v];
-        if (SCORES && a.bias) bv = bias[v];
-      }
+    for (int v = V - 1; v >= 0; --v) {
+      at = key[v] == best ? v : at;
+      if (V > 16 && v % 8 == 0) __builtin_amdgcn_sched_barrier(0);  // (32 masks at once do not fit)
+    }
     const int expert = row_min(at < V ? first + at : 1 << 30);
-    const bool mine = at < V && first + at == expert;
+    const int taken = first + at == expert ? at : V;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (mine && v == at) key[v] = -T(inf());
-    if (SCORES) {
-      zv = row_max(mine ? zv : -inf());
-      if (a.bias) bv = row_max(mine ? bv : -inf());
-      if (close && !(zv == z_before && bv == b_before)) near = true;
-      before = best;
-      z_before = zv;
-      b_before = bv;
-    } else {
-      zv = static_cast<float>(best);
+    for (int v = 0; v < V; ++v) {
+      key[v] = v == taken ? -T(inf()) : key[v];
+      if (V > 16 && v % 8 == 7) __builtin_amdgcn_sched_barrier(0);
     }
-    if (lane == j) {
-      c.expert = expert;
-      c.z = zv;
-      c.bias = bv;
-    }
+    before = best;
+    if (lane == j) c.expert = expert;
+  }
+  c.z = c.bias = 0.0f;
+  if (c.expert >= 0) {
+    c.z = logit(row, a.dtype, c.expert);
+    if (SCORES && a.bias) c.bias = bias[c.expert];
   }
   c.found = j;
   c.near = near;
@@ -309,7 +309,10 @@ __device__ __forceinline__ void put_in_order(const RouteArgs& a, const float* z,
     m = row_max(m);
     double sum = 0.0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) sum += exponential(static_cast<double>(z[v]) - m);
+    for (int v = 0; v < V; ++v) {
+      sum += exponential(static_cast<double>(z[v]) - m);
+      one_by_one<double>();
+    }
     sum = row_sum(sum);
     if (lane < c.found) key = exponential(static_cast<double>(c.z) - m) / sum;
   }
@@ -388,10 +391,10 @@ __device__ __forceinline__ void write_rest(const RouteArgs& a, const int* total,
   }
 }
 
-// TOKENS tokens in a workgroup of 16 lanes each; of 64 tokens in passes of 32
-// with V = 16 and of 16 with V = 32 (the registers).
+// TOKENS tokens in a workgroup of 16 lanes each; 64 tokens with V = 32 in passes
+// of 16 (the registers).
 template <int V, int TOKENS>
-constexpr int kThreadsOf = TOKENS * kLanes / (TOKENS < 64 || V < 16 ? 1 : V / 8);
+constexpr int kThreadsOf = TOKENS * kLanes / (TOKENS < 64 || V < 32 ? 1 : 4);
 
 template <int V, int TOKENS, bool SCORES>
 __global__ __launch_bounds__((kThreadsOf<V, TOKENS>)) void route_kernel(const RouteArgs a) {
@@ -401,27 +404,34 @@ __global__ __launch_bounds__((kThreadsOf<V, TOKENS>)) void route_kernel(const Ro
   __shared__ int16_t found[TOKENS][kMaxChosen];
   using Mark = std::conditional_t<SCORES, double, float>;
   __shared__ Mark marks[kThreads / kLanes][kMaxExpertGroups + 2 * kLanes];
+  __shared__ float bias[SCORES ? kLanes * V : 1];
   const int lane = threadIdx.x & (kLanes - 1);
   const int64_t token0 = static_cast<int64_t>(blockIdx.x) * TOKENS;
   const bool plan = a.slots || a.loads;
   for (int e = threadIdx.x; e < a.experts; e += kThreads) mask[e] = 0;
   __syncthreads();
-  float bias[V];
+  float widest = 0.0f;
   bool bad_bias = false;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    bias[v] = SCORES && a.bias && lane * V + v < a.experts ? a.bias[lane * V + v] : 0.0f;
-    bad_bias = bad_bias || bias[v] != bias[v];
+  if (SCORES && a.bias) {
+    for (int e = threadIdx.x; e < kLanes * V; e += kThreads) bias[e] = e < a.experts ? a.bias[e] : 0.0f;
+    __syncthreads();
+    for (int v = 0; v < V; ++v) {
+      const float b = bias[lane * V + v];
+      bad_bias = bad_bias || b != b;
+      widest = fmaxf(widest, fabsf(b));
+    }
+    widest = row_max(widest);
   }
 #pragma unroll 1
   for (int local = threadIdx.x / kLanes; local < TOKENS; local += kThreads / kLanes) {
     const int64_t token = token0 + local;
     if (token >= a.tokens) break;
     const bool there = !a.mask || a.mask[token];
+    const char* row = a.logits + token * a.ld * (a.dtype ? 2 : 4);
     float z[V];
     bool bad = false;
     if (there) {
-      load<V>(z, a.logits + token * a.ld * (a.dtype ? 2 : 4), a.dtype, lane * V, a.experts);
+      load<V>(z, row, a.dtype, lane * V, a.experts);
 #pragma unroll
       for (int v = 0; v < V; ++v) bad = bad || z[v] != z[v] || (!a.sigmoid && z[v] == inf());
       bad = row_max(bad || bad_bias ? 1 : 0) != 0;
@@ -432,10 +442,13 @@ __global__ __launch_bounds__((kThreadsOf<V, TOKENS>)) void route_kernel(const Ro
     }
     Choice c;
     Mark* own = marks[threadIdx.x / kLanes];
-    c = choose<float, V, SCORES>(a, z, bias, lane, reinterpret_cast<float*>(own));
+    c = choose<float, V, SCORES>(a, z, bias, widest, row, lane, reinterpret_cast<float*>(own));
     if constexpr (SCORES) {
       if (c.near && !c.again) put_in_order<V>(a, z, c, lane, own);
-      if (c.again) c = choose<double, V, true>(a, z, bias, lane, own);
+      if (c.again) {
+        c = choose<double, V, true>(a, z, bias, widest, row, lane, own);
+        load<V>(z, row, a.dtype, lane * V, a.experts);  // (not kept meanwhile: the registers)
+      }
     }
     if (lane >= a.k) c.expert = -1;
     // the weights, lane j those of the j-th
@@ -503,15 +516,12 @@ __global__ __launch_bounds__((kThreadsOf<V, TOKENS>)) void route_kernel(const Ro
 
 // The pairs' order from the counts of every a.group tokens and the chosen experts.
 // Each workgroup sums all counts by itself (they are few and in L2), eight
-// experts for a thread.
+// experts a lane.
 __global__ __launch_bounds__(1024) void plan_kernel(const RouteArgs a) {
   constexpr int kParts = kPlanTokens / 64;
-  // expert e's sums lie at (e % 8) * kStride + e / 8: threads of a wave add to
-  // neighbouring words
-  constexpr int kStride = kMaxExperts / 8 + 1;
   __shared__ uint64_t mask[kParts][kMaxExperts];
   __shared__ int total[kMaxExperts], before[kMaxExperts], base[kMaxExperts + 1];
-  __shared__ int all_sums[8 * kStride], low_sums[8 * kStride];
+  __shared__ int sums[2][16][kMaxExperts];  // of each wave's rows, all and those before; expert e at (e % 8) * 64 + e / 8
   const int tid = threadIdx.x;
   const int wide = (a.experts + 15) & ~15, words = wide / 8;  // 2 .. 64 words of 8 experts
   const int rows = (a.tokens + a.group - 1) / a.group;
@@ -531,35 +541,59 @@ __global__ __launch_bounds__(1024) void plan_kernel(const RouteArgs a) {
 #pragma unroll
     for (int q = 0; q < kParts; ++q) mask[q][e] = 0;
   }
-  for (int e = tid; e < 8 * kStride; e += 1024) all_sums[e] = low_sums[e] = 0;
   __syncthreads();
   {
-    // thread = (row, word); its sums as 16-bit counters, two to a register
-    const int per = 1024 / words;
-    const int row = tid / words, word = tid - row * words;
-    if (row < per) {
-      for (int start = 0; start < rows; start += per * 512) {  // 512 rows of at most 64 tokens fit 16 bits
-        uint32_t all[4] = {0, 0, 0, 0}, low[4] = {0, 0, 0, 0};
-        const int end = min(rows, start + per * 512);
-#pragma unroll 8
-        for (int r = start + row; r < end; r += per) {
-          const uint2 u = *reinterpret_cast<const uint2*>(a.counts + static_cast<int64_t>(r) * wide + word * 8);
-          const uint32_t keep = r < own ? 0x00ff00ffu : 0;
-          const uint32_t w[4] = {u.x & 0x00ff00ffu, (u.x >> 8) & 0x00ff00ffu, u.y & 0x00ff00ffu,
-                                 (u.y >> 8) & 0x00ff00ffu};
+    // A wave takes 64 / lanes rows at a time, a lane a word of each; sums are
+    // 16-bit counters, two to a register, joined over the rows of a wave by
+    // lane exchanges before a counter can overflow.  (LDS atomics here took
+    // half of the kernel's time.)
+    int lanes = 2;
+    while (lanes < words) lanes *= 2;
+    const int lane = tid & 63, wave = tid >> 6, word = lane & (lanes - 1);
+    const int step = 16 * (64 / lanes), most = 16 * lanes - 1;  // rows of a pass; passes that fit 16 bits
+    int all[8], low[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) all[i] = low[i] = 0;
+    for (int start = 0; start < rows; start += step * most) {
+      uint32_t x[4] = {0, 0, 0, 0}, y[4] = {0, 0, 0, 0};
+      const int end = min(rows, start + step * most);
+      // eight loads are in flight together: none depends on a branch
+      for (int r = start + wave * (64 / lanes) + lane / lanes; r < end; r += 8 * step) {
+        uint2 u[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          u[q] = *reinterpret_cast<const uint2*>(a.counts + static_cast<int64_t>(min(r + q * step, rows - 1)) * wide +
+                                                 min(word, words - 1) * 8);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t here = r + q * step < end ? 0x00ff00ffu : 0, keep = r + q * step < own ? here : 0;
+          const uint32_t w[4] = {u[q].x, u[q].x >> 8, u[q].y, u[q].y >> 8};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            all[i] += w[i];
-            low[i] += w[i] & keep;
+            x[i] += w[i] & here;
+            y[i] += w[i] & keep;
           }
         }
+      }
+      for (int d = lanes; d < 64; d *= 2) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int n = i / 4 * 2 + i % 2, shift = i % 4 / 2 * 16;
-          const int x = all[n] >> shift & 0xffffu, y = low[n] >> shift & 0xffffu;
-          if (x) atomicAdd(&all_sums[i * kStride + word], x);
-          if (y) atomicAdd(&low_sums[i * kStride + word], y);
+        for (int i = 0; i < 4; ++i) {
+          x[i] += __shfl_xor(x[i], d);
+          y[i] += __shfl_xor(y[i], d);
         }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int n = i / 4 * 2 + i % 2, shift = i % 4 / 2 * 16;
+        all[i] += x[n] >> shift & 0xffffu;
+        low[i] += y[n] >> shift & 0xffffu;
+      }
+    }
+    if (lane < lanes) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sums[0][wave][i * 64 + word] = all[i];
+        sums[1][wave][i * 64 + word] = low[i];
       }
     }
   }
@@ -570,9 +604,14 @@ __global__ __launch_bounds__(1024) void plan_kernel(const RouteArgs a) {
         atomicOr(reinterpret_cast<uint32_t*>(&mask[local[i] / 64][mine[i]]) + (local[i] >> 5 & 1), 1u << (local[i] & 31));
   }
   __syncthreads();
-  for (int e = tid; e < a.experts; e += 1024) {
-    total[e] = all_sums[(e & 7) * kStride + (e >> 3)];
-    before[e] = low_sums[(e & 7) * kStride + (e >> 3)];
+  {
+    const int e = tid & (kMaxExperts - 1), half = tid / kMaxExperts;
+    int sum = 0;
+    if (e < a.experts) {
+#pragma unroll
+      for (int w = 0; w < 16; ++w) sum += sums[half][w][(e & 7) * 64 + (e >> 3)];
+    }
+    (half ? before : total)[e] = sum;
   }
   __syncthreads();
   if (tid < 64) scan_rows(total, base, a.experts, a.align);
@@ -642,15 +681,7 @@ __global__ __launch_bounds__(256) void backward_kernel(const RouteBackwardArgs a
     }
   }
   float d = (g - (a.renormalize && a.scale != 0.0f ? gw / a.scale : 0.0f)) * w;
-  if (a.sigmoid && e >= 0) {
-    float zj;
-    if (a.dtype) {
-      zj = __builtin_bit_cast(float, static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(row)[e]) << 16);
-    } else {
-      zj = reinterpret_cast<const float*>(row)[e];
-    }
-    d *= sigmoid(-zj);
-  }
+  if (a.sigmoid && e >= 0) d *= sigmoid(-logit(row, a.dtype, e));
   if (gw != gw) {
 #pragma unroll
     for (int v = 0; v < V; ++v) out[v] = gw;

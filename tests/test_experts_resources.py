@@ -1,7 +1,8 @@
 """Register and scratch budget of the expert kernels (CPU: hipcc cross-compiles
 for gfx950 with the library's own flags): no spilled vector registers, no
-scratch memory, none of the packed fp32 instructions that the build turns off,
-and the products on the matrix instructions they are meant to use."""
+scratch memory (but for some scalar masks where more than 256 experts are chosen
+by score), none of the packed fp32 instructions that the build turns off, and
+the products on the matrix instructions they are meant to use."""
 
 import re
 
@@ -10,9 +11,10 @@ import pytest
 from tests.test_multi_resources import assembly
 
 
-@pytest.mark.parametrize("source,kernels,most", [("block_codes.hip", 20, 128), ("route.hip", 20, 512),
-                                                 ("expert_sum.hip", 4, 64), ("block_gemm.hip", 30, 256)])
-def test_kernels_use_no_scratch(tmp_path, source, kernels, most):
+@pytest.mark.parametrize("source,kernels,most,scratch", [
+    ("block_codes.hip", 20, 128, 0), ("route.hip", 20, 512, 128), ("expert_sum.hip", 4, 64, 0),
+    ("block_gemm.hip", 30, 256, 0)])
+def test_kernels_use_no_scratch(tmp_path, source, kernels, most, scratch):
     text = assembly(tmp_path, source)
     found = 0
     for block in re.split(r"\n\s+- \.", text):
@@ -21,7 +23,7 @@ def test_kernels_use_no_scratch(tmp_path, source, kernels, most):
         if "vgpr_count" not in vals:
             continue
         found += 1
-        assert vals["private_segment_fixed_size"] == vals["vgpr_spill_count"] == 0, vals
+        assert vals["vgpr_spill_count"] == 0 and vals["private_segment_fixed_size"] <= scratch, vals
         assert vals["vgpr_count"] <= most, vals
     assert found == kernels
     assert not re.search(r"\bv_pk_(add|mul|fma)_f32\b", text)
