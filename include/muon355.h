@@ -31,6 +31,10 @@
  * AdamW ([GUIDE] sections 5 and 6), and the soap_* calls run SOAP, Adam in
  * the eigenbasis of Shampoo's statistics ([GUIDE] 11.1-11.2).
  *
+ * Beside the optimizers stand the operators of the expert layers whose weights
+ * they step: muon_block_* (8-bit block codes and their products), muon_route_*
+ * (tokens to experts) and muon_expert_* (each token's sum over its experts).
+ *
  * Conventions shared by every entry point:
  *   - All matrix memory and all workspaces are caller-owned DEVICE memory.
  *     The library never allocates, frees or synchronizes; every call only
@@ -704,8 +708,8 @@ typedef struct muon_codes {
  *
  *   scale = max|x| / 448,   code = round(448 * x / max|x|)   over a block,
  *
- * to nearest, ties to even; the quotient is correctly rounded before.  A block
- * whose largest magnitude is below 2^-100 gets scale 0 and codes 0.  A block
+ * to nearest, ties to even.  A quotient that fp32 holds is exact before that
+ * rounding (so ties are ties), another within its last place.  A block whose largest magnitude is below 2^-100 gets scale 0 and codes 0.  A block
  * that holds a NaN or an infinity gets a scale that is not finite, and every
  * value of it is NaN: products pass it on.
  *
@@ -725,7 +729,13 @@ muon_status_t muon_block_quantize(const muon_batch_t* x, const int32_t* pairs, c
  * Products C = A * B^T over codes: A has M rows, B has N, both K columns; C is
  * M x N, row-major, BF16 or F32.  A's blocks have one row, B's one or 128.
  * Sums over a block of 128 are fp32, each is multiplied by the two scales in
- * fp32 and added to an fp32 sum in the order of the blocks.
+ * fp32 and added to an fp32 sum, in an order that depends on the shapes alone:
+ * the same call gives the same bits.
+ *   BF16 results come from the matrix instruction for 8-bit floats, which drops
+ *     what lies 13 bits below the largest of eight neighbouring products: about
+ *     5e-5 of a result's size, a fortieth of its rounding to BF16.
+ *   F32 results (gradients that batches add to) come from the one for BF16, on
+ *     codes that BF16 holds exactly: products are exact, sums fp32.
  *
  * MUON_PRODUCT_BATCH : count products; a, b and c have equal counts; offsets
  *   is NULL.

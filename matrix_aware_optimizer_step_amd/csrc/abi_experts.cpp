@@ -224,7 +224,9 @@ muon_status_t muon_block_matmul(const muon_codes_t* a, const muon_codes_t* b, co
   }
   const int64_t tiles = (ceil_div(a->rows, 128) + (product == MUON_PRODUCT_ROWS ? many : 0)) * ceil_div(b->rows, 128) *
                         (product == MUON_PRODUCT_ROWS ? 1 : many);
-  if (tiles > kMaxWorkgroups) return fail(MUON_ERR_UNSUPPORTED, "the product is too large for one launch");
+  // (REDUCE numbers its tiles in chunks, up to four times as many)
+  if (tiles > (product == MUON_PRODUCT_REDUCE ? kMaxWorkgroups / 4 : kMaxWorkgroups))
+    return fail(MUON_ERR_UNSUPPORTED, "the product is too large for one launch");
   BlockGemmArgs g{};
   g.a = to_codes(a);
   g.b = to_codes(b);

@@ -11,6 +11,10 @@
 // fell to either side.
 //
 // Both kernels are bound by memory: bytes in plus one byte for each order out.
+// 16384 x 4096 bf16: one order 38 us (5.3 TB/s), the transposed one 48, both 60 to
+// 67 (4.0 to 4.5 TB/s), both with square blocks 54.  Workgroups that fetch their
+// next tile while they work on one were no faster (75), nor were fewer registers
+// for more waves (83).
 
 #include "block_internal.h"
 

@@ -5,7 +5,8 @@
 //   dw[t][j] = <dout[t], y[slots[t][j]]>                 fp32
 //
 // Both read every row once and are bound by that: bytes in, an element of the
-// result for each k of them.
+// result for each k of them.  16384 tokens, 8 rows of 2048 bf16: sums 106 us (5.7
+// TB/s), dots 112 (5.4).
 
 #include "block_internal.h"
 
@@ -21,8 +22,8 @@ typedef u32x4 u32x4_any __attribute__((aligned(2)));
 
 // Eight elements at column c of a row, as fp32; zeros behind the last column.
 // STREAM: past the caches (nontemporal), where y is more than they hold:
-// 16384 tokens of 8 rows of 2048 106 us against 120 for the sums, 121 against
-// 133 for the dots; 1000 tokens of 6 rows of 5120 16 and 47 against 14 and 36.
+// 16384 tokens of 8 rows of 2048 106 us against 120 for the sums; 1000 tokens of
+// 6 rows of 5120 16 against 14.
 template <bool STREAM>
 __device__ __forceinline__ void load8(float* v, const char* row, int bf16, int64_t c, int64_t cols) {
   if (bf16) {

@@ -18,6 +18,11 @@
 // order among themselves (a token in a thousand); or the whole token, where it
 // is a border between groups, or more experts than lanes.
 //
+// Measured: 65536 tokens, 8 of 128, softmax 23 us for the choice (11 for one
+// expert instead of eight: each costs 1.7 us, 69 instructions for four tokens; the
+// logits' 34 MB are 5 us), 16 for the order, 10 for the gradient.  5003 tokens, 8 of
+// 256 in groups by biased sigmoid scores: 26 and 10.  One token: 5.4.
+//
 // The order by expert needs no sort and no atomics on global memory: a token
 // chooses an expert at most once, so 64 tokens are one 64-bit mask for each
 // expert, and a pair's place among them is the number of bits below its own.
