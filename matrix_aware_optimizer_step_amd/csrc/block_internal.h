@@ -77,7 +77,7 @@ struct RouteArgs {
 };
 // Tokens of a run, whose counts are one row of the workspace.
 constexpr int32_t route_group(int64_t tokens, int64_t experts) {
-  return tokens <= 64 || tokens > 16384 || experts > 256 ? 64 : 16;
+  return tokens <= 64 || tokens > 16384 ? 64 : 16;
 }
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
 

@@ -6,7 +6,8 @@
 // and the order of the (token, expert) pairs by expert.
 //
 // A token is 16 lanes with V logits each, so that four tokens share a wave and
-// every reduction is four rotations inside a row of lanes.  The k best are
+// every reduction is four rotations inside a row of lanes; or 32 lanes, with one
+// exchange of two rows more (launch_route has the rule).  The k best are
 // taken one after the other: the largest key of all lanes, then the lowest
 // expert that has it.
 //
@@ -21,7 +22,7 @@
 // Measured: 65536 tokens, 8 of 128, softmax 23 us for the choice (11 for one
 // expert instead of eight: each costs 1.7 us, 69 instructions for four tokens; the
 // logits' 34 MB are 5 us), 16 for the order, 10 for the gradient.  5003 tokens, 8 of
-// 256 in groups by biased sigmoid scores: 26 and 10.  One token: 5.4.
+// 256 in groups by biased sigmoid scores: 15 and 10.  One token: 5.4.
 //
 // The order by expert needs no sort and no atomics on global memory: a token
 // chooses an expert at most once, so 64 tokens are one 64-bit mask for each
@@ -35,6 +36,7 @@ namespace muon {
 namespace {
 
 constexpr int kLanes = 16;
+constexpr int kMaxCandidates = 16;
 constexpr int kPlanTokens = 256;  // tokens of a workgroup of the second kernel
 
 // Keys of fp32 scores that are further apart than this are in the right order.
@@ -64,37 +66,58 @@ __device__ __forceinline__ double rotated(double x) {
   const uint32_t lo = rotated<CTRL>(static_cast<int>(u)), hi = rotated<CTRL>(static_cast<int>(u >> 32));
   return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
 }
+// x of two neighbouring rows of 16 lanes, in both: a the lower row's, b the upper
+// one's.
+__device__ __forceinline__ void pair_rows(int x, int& a, int& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void pair_rows(float x, float& a, float& b) {
+  int p, q;
+  pair_rows(__builtin_bit_cast(int, x), p, q);
+  a = __builtin_bit_cast(float, p);
+  b = __builtin_bit_cast(float, q);
+}
+__device__ __forceinline__ void pair_rows(double x, double& a, double& b) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, x);
+  int p[2], q[2];
+  pair_rows(static_cast<int>(u), p[0], q[0]);
+  pair_rows(static_cast<int>(u >> 32), p[1], q[1]);
+  __builtin_memcpy(&a, p, 8);
+  __builtin_memcpy(&b, q, 8);
+}
 // The larger one (no operand is a NaN: tokens that hold one are set apart).
 __device__ __forceinline__ float larger(float a, float b) { return __builtin_fmaxf(a, b); }
 __device__ __forceinline__ double larger(double a, double b) { return __builtin_fmax(a, b); }
 __device__ __forceinline__ int larger(int a, int b) { return max(a, b); }
-// Over a row of 16 lanes, in every one of them.
-template <typename T>
+// f over a row of 16 lanes, or over two of them, in every lane.
+template <int LANES, typename T, typename F>
+__device__ __forceinline__ T over_lanes(T x, F f) {
+  x = f(x, rotated<0x128>(x));
+  x = f(x, rotated<0x124>(x));
+  x = f(x, rotated<0x122>(x));
+  x = f(x, rotated<0x121>(x));
+  if (LANES == 16) return x;
+  T a, b;
+  pair_rows(x, a, b);
+  return f(a, b);
+}
+template <int LANES = kLanes, typename T>
 __device__ __forceinline__ T row_max(T x) {
-  x = larger(x, rotated<0x128>(x));
-  x = larger(x, rotated<0x124>(x));
-  x = larger(x, rotated<0x122>(x));
-  return larger(x, rotated<0x121>(x));
+  return over_lanes<LANES>(x, [](T a, T b) { return larger(a, b); });
 }
+template <int LANES>
 __device__ __forceinline__ int row_min(int x) {
-  x = min(x, rotated<0x128>(x));
-  x = min(x, rotated<0x124>(x));
-  x = min(x, rotated<0x122>(x));
-  return min(x, rotated<0x121>(x));
+  return over_lanes<LANES>(x, [](int a, int b) { return min(a, b); });
 }
-__device__ __forceinline__ uint32_t row_or(uint32_t u) {
-  int x = static_cast<int>(u);
-  x |= rotated<0x128>(x);
-  x |= rotated<0x124>(x);
-  x |= rotated<0x122>(x);
-  return static_cast<uint32_t>(x | rotated<0x121>(x));
+template <int LANES>
+__device__ __forceinline__ uint32_t row_or(uint32_t x) {
+  return static_cast<uint32_t>(over_lanes<LANES>(static_cast<int>(x), [](int a, int b) { return a | b; }));
 }
-template <typename T>
+template <int LANES = kLanes, typename T>
 __device__ __forceinline__ T row_sum(T x) {
-  x += rotated<0x128>(x);
-  x += rotated<0x124>(x);
-  x += rotated<0x122>(x);
-  return x + rotated<0x121>(x);
+  return over_lanes<LANES>(x, [](T a, T b) { return a + b; });
 }
 
 __device__ __forceinline__ float exponential(float x) { return expf(x); }
@@ -141,7 +164,7 @@ __device__ __forceinline__ void one_by_one() {
   if (sizeof(T) == 8) __builtin_amdgcn_sched_barrier(0);
 }
 
-// What a token's 16 lanes found: lane j has the j-th best.
+// What a token's lanes found: lane j has the j-th best.
 struct Choice {
   int expert;    // -1: none
   float z, bias; // its logit and bias
@@ -153,8 +176,8 @@ struct Choice {
 // The k best of a token.  T: type of the keys; SCORES: the keys are scores
 // (plus bias, `bias` in LDS, `widest` its largest magnitude), else the logits.
 // `row`: the token's logits in memory.  `shared`: LDS of this token's own
-// (kMaxExpertGroups + 2 * kLanes of T).
-template <typename T, int V, bool SCORES>
+// (kMaxExpertGroups + 2 * LANES of T).
+template <typename T, int V, int LANES, bool SCORES>
 __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, const float* bias, float widest,
                                          const char* row, int lane, T* shared) {
   const int first = lane * V;
@@ -170,7 +193,7 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, con
       float m = z[0];
 #pragma unroll
       for (int v = 1; v < V; ++v) m = larger(m, z[v]);
-      const T top = row_max(m);
+      const T top = row_max<LANES>(m);
       T sum = T(0);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -178,7 +201,7 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, con
         sum += key[v];
         one_by_one<T>();
       }
-      const T scale = T(1) / row_sum(sum);
+      const T scale = T(1) / row_sum<LANES>(sum);
 #pragma unroll
       for (int v = 0; v < V; ++v) key[v] *= scale;
     }
@@ -231,11 +254,11 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, con
           b2 = larger(b2, x < b1 ? x : b1);
           b1 = larger(b1, x);
         }
-        const T m1 = row_max(b1);
+        const T m1 = row_max<LANES>(b1);
         T score = m1;
         if (a.group_best > 1) {
-          const int who = row_min(b1 == m1 ? lane : kLanes);  // the lane whose best is the group's
-          const T m2 = row_max(lane == who ? b2 : b1);
+          const int who = row_min<LANES>(b1 == m1 ? lane : LANES);  // the lane whose best is the group's
+          const T m2 = row_max<LANES>(lane == who ? b2 : b1);
           if (m2 > -T(inf())) score = m1 + m2;
         }
         shared[g] = score;  // every lane writes the same value
@@ -247,7 +270,7 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, con
     // groups of 32, 25 us against 18)
     uint32_t kept = 0;
     T low = T(inf()), high = -T(inf());  // worst kept, best dropped
-    for (int g = lane; g < a.groups; g += kLanes) {
+    for (int g = lane; g < a.groups; g += LANES) {
       const T mark = shared[g];
       int ahead = 0;
 #pragma unroll 4
@@ -262,9 +285,9 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, con
         high = mark > high ? mark : high;
       }
     }
-    kept = row_or(kept);
-    low = -row_max(-low);
-    high = row_max(high);
+    kept = row_or<LANES>(kept);
+    low = -row_max<LANES>(-low);
+    high = row_max<LANES>(high);
     if (SCORES && high > -T(inf()) && low - high <= T(2 * margin(static_cast<float>(low), 2 * widest))) again = true;
     int g = g0, in = in0;
 #pragma unroll
@@ -284,28 +307,22 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, con
     T best = key[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) best = larger(best, key[v]);
-    best = row_max(best);
-    if (!(best > -T(inf()))) break;  // the same in all 16 lanes
+    best = row_max<LANES>(best);
+    if (!(best > -T(inf()))) break;  // the same in all lanes
     const bool close = SCORES && sizeof(T) == 4 && j > 0 && before - best <= T(margin(static_cast<float>(best), widest));
     if (j >= a.k && !close) break;
-    if (j == kLanes) {
+    if (j == kMaxCandidates) {
       again = true;
       break;
     }
     near = near || close;
     int at = V;
 #pragma unroll
-    for (int v = V - 1; v >= 0; --v) {
-      at = key[v] == best ? v : at;
-      if (V > 16 && v % 8 == 0) __builtin_amdgcn_sched_barrier(0);  // (32 masks at once do not fit)
-    }
-    const int expert = row_min(at < V ? first + at : 1 << 30);
+    for (int v = V - 1; v >= 0; --v) at = key[v] == best ? v : at;
+    const int expert = row_min<LANES>(at < V ? first + at : 1 << 30);
     const int taken = first + at == expert ? at : V;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      key[v] = v == taken ? -T(inf()) : key[v];
-      if (V > 16 && v % 8 == 7) __builtin_amdgcn_sched_barrier(0);
-    }
+    for (int v = 0; v < V; ++v) key[v] = v == taken ? -T(inf()) : key[v];
     before = best;
     if (lane == j) c.expert = expert;
   }
@@ -321,7 +338,7 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, con
 }
 
 // The candidates' order by their keys in fp64, one a lane.
-template <int V>
+template <int V, int LANES>
 __device__ __forceinline__ void put_in_order(const RouteArgs& a, const float* z, Choice& c, int lane, double* shared) {
   double key = -inf();
   if (a.sigmoid) {
@@ -330,20 +347,20 @@ __device__ __forceinline__ void put_in_order(const RouteArgs& a, const float* z,
     float m = z[0];
 #pragma unroll
     for (int v = 1; v < V; ++v) m = larger(m, z[v]);
-    m = row_max(m);
+    m = row_max<LANES>(m);
     double sum = 0.0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       sum += exponential(static_cast<double>(z[v]) - m);
       one_by_one<double>();
     }
-    sum = row_sum(sum);
+    sum = row_sum<LANES>(sum);
     if (lane < c.found) key = exponential(static_cast<double>(c.z) - m) / sum;
   }
   key += c.bias;
   int rank = 0;
   shared[lane] = key;
-  int* experts = reinterpret_cast<int*>(shared + kLanes);
+  int* experts = reinterpret_cast<int*>(shared + LANES);
   experts[lane] = c.expert;
   __builtin_amdgcn_wave_barrier();
   for (int o = 0; o < c.found; ++o) {
@@ -415,21 +432,21 @@ __device__ __forceinline__ void write_rest(const RouteArgs& a, const int* total,
   }
 }
 
-// TOKENS tokens in a workgroup of 16 lanes each; 64 tokens with V = 32 in passes
-// of 16 (the registers).
-template <int V, int TOKENS>
-constexpr int kThreadsOf = TOKENS * kLanes / (TOKENS < 64 || V < 32 ? 1 : 4);
+// TOKENS tokens in a workgroup, of LANES lanes each; 64 tokens of 32 lanes in
+// passes of 16 (the registers).
+template <int LANES, int TOKENS>
+constexpr int kThreadsOf = LANES * (LANES == 16 ? TOKENS : 16);
 
-template <int V, int TOKENS, bool SCORES>
-__global__ __launch_bounds__((kThreadsOf<V, TOKENS>)) void route_kernel(const RouteArgs a) {
-  constexpr int kThreads = kThreadsOf<V, TOKENS>;
+template <int V, int LANES, int TOKENS, bool SCORES>
+__global__ __launch_bounds__((kThreadsOf<LANES, TOKENS>)) void route_kernel(const RouteArgs a) {
+  constexpr int kThreads = kThreadsOf<LANES, TOKENS>;
   __shared__ uint64_t mask[kMaxExperts];
   __shared__ int total[kMaxExperts], base[kMaxExperts + 1];
   __shared__ int16_t found[TOKENS][kMaxChosen];
   using Mark = std::conditional_t<SCORES, double, float>;
-  __shared__ Mark marks[kThreads / kLanes][kMaxExpertGroups + 2 * kLanes];
-  __shared__ float bias[SCORES ? kLanes * V : 1];
-  const int lane = threadIdx.x & (kLanes - 1);
+  __shared__ Mark marks[kThreads / LANES][kMaxExpertGroups + 2 * LANES];
+  __shared__ float bias[SCORES ? LANES * V : 1];
+  const int lane = threadIdx.x & (LANES - 1);
   const int64_t token0 = static_cast<int64_t>(blockIdx.x) * TOKENS;
   const bool plan = a.slots || a.loads;
   for (int e = threadIdx.x; e < a.experts; e += kThreads) mask[e] = 0;
@@ -437,17 +454,17 @@ __global__ __launch_bounds__((kThreadsOf<V, TOKENS>)) void route_kernel(const Ro
   float widest = 0.0f;
   bool bad_bias = false;
   if (SCORES) {
-    for (int e = threadIdx.x; e < kLanes * V; e += kThreads) bias[e] = a.bias && e < a.experts ? a.bias[e] : 0.0f;
+    for (int e = threadIdx.x; e < LANES * V; e += kThreads) bias[e] = a.bias && e < a.experts ? a.bias[e] : 0.0f;
     __syncthreads();
     for (int v = 0; v < V; ++v) {
       const float b = bias[lane * V + v];
       bad_bias = bad_bias || b != b;
       widest = fmaxf(widest, fabsf(b));
     }
-    widest = row_max(widest);
+    widest = row_max<LANES>(widest);
   }
 #pragma unroll 1
-  for (int local = threadIdx.x / kLanes; local < TOKENS; local += kThreads / kLanes) {
+  for (int local = threadIdx.x / LANES; local < TOKENS; local += kThreads / LANES) {
     const int64_t token = token0 + local;
     if (token >= a.tokens) break;
     const bool there = !a.mask || a.mask[token];
@@ -458,19 +475,19 @@ __global__ __launch_bounds__((kThreadsOf<V, TOKENS>)) void route_kernel(const Ro
       load<V>(z, row, a.dtype, lane * V, a.experts);
 #pragma unroll
       for (int v = 0; v < V; ++v) bad = bad || z[v] != z[v] || (!a.sigmoid && z[v] == inf());
-      bad = row_max(bad || bad_bias ? 1 : 0) != 0;
+      bad = row_max<LANES>(bad || bad_bias ? 1 : 0) != 0;
     }
     if (!there || bad) {  // nothing is chosen (and the weights are NaN where something is not a number)
 #pragma unroll
       for (int v = 0; v < V; ++v) z[v] = -inf();
     }
     Choice c;
-    Mark* own = marks[threadIdx.x / kLanes];
-    c = choose<float, V, SCORES>(a, z, bias, widest, row, lane, reinterpret_cast<float*>(own));
+    Mark* own = marks[threadIdx.x / LANES];
+    c = choose<float, V, LANES, SCORES>(a, z, bias, widest, row, lane, reinterpret_cast<float*>(own));
     if constexpr (SCORES) {
-      if (c.near && !c.again) put_in_order<V>(a, z, c, lane, own);
+      if (c.near && !c.again) put_in_order<V, LANES>(a, z, c, lane, own);
       if (c.again) {
-        c = choose<double, V, true>(a, z, bias, widest, row, lane, own);
+        c = choose<double, V, LANES, true>(a, z, bias, widest, row, lane, own);
         load<V>(z, row, a.dtype, lane * V, a.experts);  // (not kept meanwhile: the registers)
       }
     }
@@ -489,18 +506,18 @@ __global__ __launch_bounds__((kThreadsOf<V, TOKENS>)) void route_kernel(const Ro
 #pragma unroll
         for (int v = 1; v < V; ++v) m = larger(m, z[v]);
       }
-      m = row_max(m);
+      m = row_max<LANES>(m);
       if (!a.renormalize && m > -inf()) {
         sum = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) sum += exponential(z[v] - m);
-        sum = row_sum(sum);
+        sum = row_sum<LANES>(sum);
       }
       if (some) s = exponential(c.z - m) / sum;
     }
     float w = a.scale * s;
     if (a.renormalize) {
-      const float sum = row_sum(s);
+      const float sum = row_sum<LANES>(s);
       w = sum > 0.0f ? a.scale * (s / sum) : 0.0f;
     }
     if (bad) w = __builtin_nanf("");
@@ -508,7 +525,7 @@ __global__ __launch_bounds__((kThreadsOf<V, TOKENS>)) void route_kernel(const Ro
       a.chosen[token * a.k + lane] = c.expert;
       a.weights[token * a.k + lane] = w;
     }
-    found[local][lane] = static_cast<int16_t>(c.expert);
+    if (lane < kMaxChosen) found[local][lane] = static_cast<int16_t>(c.expert);
     if (plan && some) atomicOr(reinterpret_cast<uint32_t*>(&mask[c.expert]) + (local >> 5), 1u << (local & 31));
   }
   if (!plan) return;
@@ -525,7 +542,7 @@ __global__ __launch_bounds__((kThreadsOf<V, TOKENS>)) void route_kernel(const Ro
   if (threadIdx.x < 64) scan_rows(total, base, a.experts, a.align);
   __syncthreads();
   if (a.slots && lane < a.k) {
-    for (int local = threadIdx.x / kLanes; local < a.tokens; local += kThreads / kLanes) {
+    for (int local = threadIdx.x / LANES; local < a.tokens; local += kThreads / LANES) {
       const int e = found[local][lane], p = local * a.k + lane;
       int slot = -1;
       if (e >= 0) {
@@ -761,43 +778,49 @@ __global__ __launch_bounds__(kMaxExperts) void balance_kernel(const BalanceArgs 
   a.loads[e] = 0;
 }
 
-template <int V, int TOKENS>
+bool by_score(const RouteArgs& a) { return a.bias || (a.groups > 1 && a.group_best > 1); }
+
+template <int V, int LANES, int TOKENS>
 void launch_kernel(const RouteArgs& a, hipStream_t s) {
   const uint32_t blocks = static_cast<uint32_t>((a.tokens + TOKENS - 1) / TOKENS);
-  if (a.bias || (a.groups > 1 && a.group_best > 1)) {
-    route_kernel<V, TOKENS, true><<<blocks, kThreadsOf<V, TOKENS>, 0, s>>>(a);
+  if (by_score(a)) {
+    route_kernel<V, LANES, TOKENS, true><<<blocks, kThreadsOf<LANES, TOKENS>, 0, s>>>(a);
   } else {
-    route_kernel<V, TOKENS, false><<<blocks, kThreadsOf<V, TOKENS>, 0, s>>>(a);
+    route_kernel<V, LANES, TOKENS, false><<<blocks, kThreadsOf<LANES, TOKENS>, 0, s>>>(a);
   }
 }
 
 // 16 tokens in a workgroup while 64 leave compute units without one (5003 tokens
 // of 256 experts: 34 us against 63), 64 where the second kernel would have too
 // many counts to sum, and where one workgroup does it all.
-template <int V>
-void launch_tokens(RouteArgs& a, hipStream_t s) {
-  a.group = route_group(a.tokens, a.experts);
-  if constexpr (V <= 16) {
-    if (a.group == 16) {
-      launch_kernel<V, 16>(a, s);
-      return;
-    }
-  }
-  launch_kernel<V, 64>(a, s);
+template <int V, int LANES>
+void launch_tokens(const RouteArgs& a, hipStream_t s) {
+  a.group == 16 ? launch_kernel<V, LANES, 16>(a, s) : launch_kernel<V, LANES, 64>(a, s);
 }
 
 }  // namespace
 
+// 16 lanes a token up to 256 experts, 32 above (512 experts, 5003 tokens: 11 us
+// against 32, with a bias 18 against 47; 65536: 72 against 70, 145 against 186).
+// With 256 experts and keys that are scores 32 as long as 16 leave a SIMD with two
+// waves or fewer (in groups, 500 tokens: 13 us against 18, 5003: 15 against 18, 16384:
+// 25 against 23).  A whole wave for a token was slower from 5003 tokens on at any
+// size (256 experts in groups: 22).
 hipError_t launch_route(const RouteArgs& args, hipStream_t s) {
   RouteArgs a = args;
+  a.group = route_group(a.tokens, a.experts);
   if (a.experts <= 64) {
-    launch_tokens<4>(a, s);
+    launch_tokens<4, 16>(a, s);
   } else if (a.experts <= 128) {
-    launch_tokens<8>(a, s);
+    launch_tokens<8, 16>(a, s);
   } else if (a.experts <= 256) {
-    launch_tokens<16>(a, s);
+    if (by_score(a) && a.group == 16 && a.tokens <= 8192) {
+      route_kernel<8, 32, 16, true><<<(a.tokens + 15) / 16, kThreadsOf<32, 16>, 0, s>>>(a);
+    } else {
+      launch_tokens<16, 16>(a, s);
+    }
   } else {
-    launch_tokens<32>(a, s);
+    launch_tokens<16, 32>(a, s);
   }
   if (a.tokens > 64 && (a.slots || a.loads))
     plan_kernel<<<(a.tokens + kPlanTokens - 1) / kPlanTokens, 1024, 0, s>>>(a);

@@ -12,7 +12,7 @@ from tests.test_multi_resources import assembly
 
 
 @pytest.mark.parametrize("source,kernels,most,scratch", [
-    ("block_codes.hip", 20, 128, 0), ("route.hip", 20, 512, 128), ("expert_sum.hip", 4, 64, 0),
+    ("block_codes.hip", 20, 128, 0), ("route.hip", 23, 256, 128), ("expert_sum.hip", 4, 64, 0),
     ("block_gemm.hip", 30, 256, 0)])
 def test_kernels_use_no_scratch(tmp_path, source, kernels, most, scratch):
     text = assembly(tmp_path, source)

@@ -156,6 +156,33 @@ def test_not_a_number(mx, score):
     check(mx, z[:5].contiguous(), 4, score=score, bias=bias.cuda())
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("tokens,experts,k", [(40, 400, 16), (300, 200, 8), (300, 512, 8)])
+def test_tokens_of_many_experts(mx, tokens, experts, k, score):
+    """Masks, infinities, NaN, ties and near keys where a token is more than 16 lanes (tokens beyond 64 and a bias for
+    200 experts, any call for 400)."""
+    z = logits(tokens, experts, F32, 9)
+    z[:, 7] = -math.inf
+    z[1] = -math.inf
+    z[2, 3:] = -math.inf
+    z[3, 150] = math.nan
+    z[4, experts - 1] = math.inf
+    z[5] = 0.25
+    z[6] = torch.randint(0, 3, (experts,), generator=torch.Generator().manual_seed(1)).float().cuda()
+    mask = torch.rand(tokens, generator=torch.Generator().manual_seed(2)) > 0.3
+    mask[1:7] = True
+    bias = (0.1 * torch.randn(experts, generator=torch.Generator().manual_seed(1))).cuda()
+    for kw in (dict(), dict(bias=bias), dict(bias=torch.zeros_like(bias)), dict(bias=bias, groups=4, top_groups=2),
+               dict(groups=8, top_groups=4), dict(groups=8, top_groups=1, group_best=1, bias=bias)):
+        check(mx, z, k, mask=mask, score=score, align=128, **kw)
+    z = logits(tokens, experts, F32, 5, 1.0)
+    z[1:] = z[0] + 1e-7 * torch.arange(1, tokens, device="cuda")[:, None]
+    s = O.scores(z[:1].double().cpu().numpy(), score)[0]
+    bias = torch.from_numpy((0.5 - s).astype(np.float32)).cuda()
+    check(mx, z, k, score=score, bias=bias)
+    check(mx, z, k, score=score, bias=bias, groups=4, top_groups=2)
+
+
 def test_strided_logits_and_without_order(mx):
     big = logits(90, 101, BF16, 1)
     z = big[3:80, 7:90]
