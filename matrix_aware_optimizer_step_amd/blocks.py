@@ -55,6 +55,16 @@ def _enqueue(device, stream, fresh, fn, *args) -> None:
         _record_on(_stream_object(stream), fresh)
 
 
+def _filled(t, value, stream):
+    """t, filled on the call's stream (results that no kernel computes)."""
+    if t.is_cuda:
+        with torch.cuda.device(t.device), torch.cuda.stream(_stream_object(stream)):
+            t.fill_(value)
+            _record_on(_stream_object(stream), [t])
+        return t
+    return t.fill_(value)
+
+
 class BlockCodes:
     """A matrix (or a batch of equal ones) as e4m3 codes with block scales.
 
@@ -280,7 +290,7 @@ def block_matmul(a: BlockCodes, b: BlockCodes, *, out: torch.Tensor | None = Non
     if c.numel() == 0:
         return c
     if a.cols == 0:
-        return c if accumulate else c.zero_()
+        return c if accumulate else _filled(c, 0, stream)
     _enqueue(a.device, stream, [c] if made else [], L.muon_block_matmul, a.desc, b.desc, _c_desc(c), None,
              L.PRODUCT_BATCH, int(bool(accumulate)))
     return c
@@ -326,7 +336,7 @@ def expert_grad(a: BlockCodes, b: BlockCodes, offsets: torch.Tensor, *, out: tor
     if c.numel() == 0:
         return c
     if a.cols == 0:
-        return c if accumulate else c.zero_()
+        return c if accumulate else _filled(c, 0, stream)
     _enqueue(a.device, stream, [c] if made else [], L.muon_block_matmul, a.desc, b.desc, _c_desc(c),
              offsets.data_ptr(), L.PRODUCT_REDUCE, int(bool(accumulate)))
     return c

@@ -7,14 +7,14 @@ matrices the optimizer step updates::
 
     r = route(logits, 8, bias=balance.bias, loads=balance.loads, align=128)
     a, at = quantize(x, pairs=(r.pairs, 8), order="both")  # rows by expert
-    y = expert_matmul(a, codes.q, r.offsets)
+    y = expert_matmul(a, codes.codes, r.offsets)
     out = expert_sum(y, r.slots, r.weights)
 
 and backward, from the gradient of ``out``::
 
     g, gt = quantize(grad, pairs=r.pairs, weights=r.weights, order="both")
     expert_grad(gt, at, r.offsets, out=weight_grads, accumulate=True)
-    grad_x = expert_sum(expert_matmul(g, codes.qt, r.offsets), r.slots)
+    grad_x = expert_sum(expert_matmul(g, codes.transposed, r.offsets), r.slots)
     grad_logits = route_backward(logits, r, expert_dot(grad, y, r.slots))
 
 Every call only enqueues kernels, on the current stream of its tensors' device
@@ -29,7 +29,7 @@ from dataclasses import dataclass
 import torch
 
 from . import _lib as L
-from .blocks import _enqueue, _matrix, _need, _same_device
+from .blocks import _enqueue, _filled, _matrix, _need, _same_device
 from .muon import dtype_code
 from .multi import StepControl, _settle
 
@@ -133,8 +133,8 @@ def route(logits: torch.Tensor, k: int, *, bias: torch.Tensor | None = None, sco
         if device.type != "cuda":
             raise RuntimeError("the tensors are not on a GPU (there is no CPU path)")
         if order:
-            found.pairs.fill_(NO_EXPERT)
-            found.offsets.zero_()
+            _filled(found.pairs, NO_EXPERT, stream)
+            _filled(found.offsets, 0, stream)
         return found
     desc = L.MuonRoute(logits.data_ptr(), _ld(logits), tokens, experts, k, dtype_code(logits), L.SCORES[score],
                        1 if renormalize else 0, groups, top_groups, group_best, align, scale)
@@ -197,7 +197,7 @@ def expert_sum(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | Non
     if tokens == 0 or shape[1] == 0:
         return out
     if y.shape[0] == 0:
-        return out.zero_()
+        return _filled(out, 0, stream)
     _enqueue(device, stream, (out,) if made else (), L.muon_expert_sum, desc, slots.data_ptr(),
              None if weights is None else weights.data_ptr(), k, od)
     return out
@@ -220,7 +220,7 @@ def expert_dot(grad: torch.Tensor, y: torch.Tensor, slots: torch.Tensor, *, out:
     if out.numel() == 0:
         return out
     if y.numel() == 0:
-        return out.zero_()
+        return _filled(out, 0, stream)
     _enqueue(device, stream, (out,) if made else (), L.muon_expert_dot, gd, yd, slots.data_ptr(), k, out.data_ptr())
     return out
 

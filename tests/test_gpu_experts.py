@@ -183,6 +183,29 @@ def test_tokens_of_many_experts(mx, tokens, experts, k, score):
     check(mx, z, k, score=score, bias=bias, groups=4, top_groups=2)
 
 
+def test_results_without_a_kernel_on_a_stream(mx):
+    """No tokens, no rows, no columns: the results are filled on the call's stream, not on the current one, which is
+    busy here until long after."""
+    z = torch.zeros(0, 6, device="cuda")
+    y, slots = torch.zeros(0, 9, device="cuda"), torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    grad = torch.zeros(4, 9, device="cuda")
+    a, b = mx.BlockCodes.empty(5, 0), mx.BlockCodes.empty(7, 0)
+    kept = torch.full((64, 512), 7.0, device="cuda")  # freed below: new results take memory that is not zero
+    torch.cuda.synchronize()
+    del kept
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        torch.cuda._sleep(20_000_000)
+        r = mx.route(z, 2, align=8, stream=stream)
+        out = mx.expert_sum(y, slots, stream=stream)
+        dots = mx.expert_dot(grad, y, slots, stream=stream)
+        c = mx.block_matmul(a, b, stream=stream)
+        with torch.cuda.stream(s):
+            assert (r.pairs.cpu() == -1).all() and r.pairs.numel() == 48 and not r.offsets.cpu().any()
+            assert not out.cpu().any() and not dots.cpu().any() and not c.cpu().any() and c.shape == (5, 7)
+        torch.cuda.synchronize()
+
+
 def test_strided_logits_and_without_order(mx):
     big = logits(90, 101, BF16, 1)
     z = big[3:80, 7:90]
