@@ -791,6 +791,7 @@ muon_status_t muon_block_matmul(const muon_codes_t* a, const muon_codes_t* b, co
 #define MUON_MAX_EXPERTS 512
 #define MUON_MAX_CHOSEN 16
 #define MUON_MAX_EXPERT_GROUPS 32
+#define MUON_MAX_ORDERED_TOKENS 4194304 /* of a call that writes the order or the loads */
 
 typedef enum muon_score { MUON_SCORE_SOFTMAX = 0, MUON_SCORE_SIGMOID = 1 } muon_score_t;
 

@@ -245,7 +245,9 @@ muon_status_t muon_block_matmul(const muon_codes_t* a, const muon_codes_t* b, co
 }
 
 int64_t muon_route_capacity(int64_t tokens, int64_t experts, int64_t k, int64_t align) {
-  return route_sizes_ok(tokens, experts, k, align) ? route_rows(tokens, experts, k, align) : 0;
+  return route_sizes_ok(tokens, experts, k, align) && tokens <= MUON_MAX_ORDERED_TOKENS
+             ? route_rows(tokens, experts, k, align)
+             : 0;
 }
 
 size_t muon_route_workspace(int64_t tokens, int64_t experts) {
@@ -266,6 +268,10 @@ muon_status_t muon_route(const muon_route_t* r, const float* bias, const uint8_t
   if (!aligned(bias, 4) || !aligned(chosen, 4) || !aligned(weights, 4) || !aligned(slots, 4) || !aligned(pairs, 4) ||
       !aligned(offsets, 4) || !aligned(loads, 4))
     return fail(MUON_ERR_INVALID_VALUE, "every array must be 4-byte aligned");
+  // the workgroup of every 256 tokens sums all counts: 137 GB out of L2 at this many of 128 experts
+  if ((slots || loads) && r->tokens > MUON_MAX_ORDERED_TOKENS)
+    return fail(MUON_ERR_UNSUPPORTED, "an order or loads of %lld tokens, more than %d", (long long)r->tokens,
+                MUON_MAX_ORDERED_TOKENS);
   const int64_t rows = route_rows(r->tokens, r->experts, r->k, r->align);
   if (slots && rows == 0) return fail(MUON_ERR_UNSUPPORTED, "the order has more than 2^31-1 rows");
   const size_t need = muon_route_workspace(r->tokens, r->experts);

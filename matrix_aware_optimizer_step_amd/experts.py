@@ -84,7 +84,7 @@ def _check(t, shape, dtype, what, device) -> None:
 def _sizes(tokens, experts, k, align, order):
     """Rows of the order, and 32-bit words of the workspace."""
     rows = L.muon_route_capacity(tokens, experts, k, align) if order else 0
-    _need(rows > 0 or not order, "align outside [1, 65536], or an order of more than 2^31-1 rows")
+    _need(rows > 0 or not order, "align outside [1, 65536], or an order of more than 2^22 tokens or 2^31-1 rows")
     return rows, -(-L.muon_route_workspace(tokens, experts) // 4)
 
 

@@ -132,6 +132,9 @@ def test_route_refuses():
     assert status_of(lambda: call(ws=FAKE + 4)) == WORKSPACE
     assert status_of(lambda: call(r=route_desc(tokens=(1 << 29) - 1, k=1, experts=512, ld=512, align=1 << 16),
                                   size=1 << 40)) == UNSUPPORTED
+    many = route_desc(tokens=(1 << 22) + 1)
+    assert status_of(lambda: call(r=many, size=1 << 40)) == UNSUPPORTED  # an order, or loads alone, of too many tokens
+    assert status_of(lambda: call(r=many, size=1 << 40, slots=None, pairs=None, offsets=None, loads=FAKE)) == UNSUPPORTED
     back = lambda chosen=FAKE, grad=FAKE, out=FAKE, ld=64: L.muon_route_backward(route_desc(), chosen, FAKE, grad, out, ld, 0)
     assert status_of(lambda: back(chosen=None)) == INVALID
     assert status_of(lambda: back(grad=None)) == INVALID
@@ -143,6 +146,7 @@ def test_capacity_and_workspace():
     assert L.muon_route_capacity(10, 64, 4, 1) == 40
     assert L.muon_route_capacity(10, 64, 4, 128) == -(-(40 + 64 * 127) // 128) * 128
     assert L.muon_route_capacity(0, 64, 4, 1) == 0 == L.muon_route_capacity(10, 64, 65, 1)
+    assert L.muon_route_capacity(1 << 22, 64, 4, 1) == 1 << 24 and L.muon_route_capacity((1 << 22) + 1, 64, 4, 1) == 0
     assert L.muon_route_workspace(0, 64) == 0 == L.muon_route_workspace(10, 513)
     assert L.muon_route_workspace(70, 100) == 5 * 112 and L.muon_route_workspace(1 << 20, 128) == (1 << 14) * 128
 
