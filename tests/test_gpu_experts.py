@@ -206,6 +206,29 @@ def test_results_without_a_kernel_on_a_stream(mx):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("experts", [3, 64])
+def test_order_of_a_million_tokens(mx, experts):
+    """More counts than the order's 16-bit counters take in one pass, from skewed tokens; the chosen are those of a
+    stable sort."""
+    tokens, k, align = (1 << 20) + 77, 2, 128
+    z = torch.randn(tokens, experts, generator=torch.Generator().manual_seed(4)) - 0.05 * torch.arange(experts)
+    r = mx.route(z.cuda(), k, align=align)
+    chosen = torch.sort(z, dim=1, descending=True, stable=True).indices[:, :k]  # (topk leaves the order of equals open)
+    assert torch.equal(r.experts.cpu().long(), chosen)
+    flat = chosen.flatten().numpy()
+    counts = np.bincount(flat, minlength=experts)
+    offsets = np.concatenate([[0], np.cumsum(-(-counts // align) * align)])
+    assert np.array_equal(r.offsets.cpu().numpy(), offsets)
+    order = np.argsort(flat, kind="stable")
+    first = np.concatenate([[0], np.cumsum(counts)])[:-1]
+    slots = np.empty(tokens * k, np.int64)
+    slots[order] = offsets[flat[order]] + np.arange(tokens * k) - first[flat[order]]
+    assert np.array_equal(r.slots.cpu().numpy().ravel(), slots)
+    pairs = np.full(r.pairs.numel(), -1, np.int64)
+    pairs[slots] = np.arange(tokens * k)
+    assert np.array_equal(r.pairs.cpu().numpy(), pairs)
+
+
 def test_strided_logits_and_without_order(mx):
     big = logits(90, 101, BF16, 1)
     z = big[3:80, 7:90]
