@@ -47,13 +47,15 @@ __device__ __forceinline__ uint32_t lds_address(const void* l) {
 // Global -> LDS copies of 16 or 4 bytes per lane: lane i's bytes at base + off
 // land at LDS address l + 16 i (4 i).  Inline asm, as the compiler would
 // otherwise wait for them at LDS reads that have nothing to do with them; the
-// kernels order them with wait_all() and a barrier.
+// kernels order them with wait_all_but() and a barrier.  The instruction reads
+// m0, which needs a wait state after its write (the compiler adds it to its own
+// instructions only).
 __device__ __forceinline__ void copy16(const char* base, uint32_t off, uint32_t l) {
-  asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(__builtin_amdgcn_readfirstlane(l))
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(__builtin_amdgcn_readfirstlane(l))
                : "memory");
 }
 __device__ __forceinline__ void copy4(const char* base, uint32_t off, uint32_t l) {
-  asm volatile("global_load_lds_dword %0, %1" ::"v"(off), "s"(base), "{m0}"(__builtin_amdgcn_readfirstlane(l))
+  asm volatile("s_nop 0\n\tglobal_load_lds_dword %0, %1" ::"v"(off), "s"(base), "{m0}"(__builtin_amdgcn_readfirstlane(l))
                : "memory");
 }
 // All LDS accesses of this wave are done and all but its N newest vector loads,

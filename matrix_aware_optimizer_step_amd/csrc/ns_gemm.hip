@@ -196,10 +196,11 @@ __device__ __forceinline__ int swizzle(int row, int c) {
 // vector load (vmcnt 0) in front of each later ds_read_b64_tr_b16, which
 // would make the k-major update wait for the next k-tile's copy in every
 // k-tile.  The kernel orders these copies itself (barrier_keep_vm); nothing
-// reads a register written by them.
+// reads a register written by them.  The instruction reads m0, which needs a
+// wait state after its write (the compiler adds it to its own instructions only).
 __device__ __forceinline__ void lds_dma16(const char* base, uint32_t off, char* l) {
   const uint32_t la = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) char*)(l)));
-  asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(__builtin_amdgcn_readfirstlane(la))
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "{m0}"(__builtin_amdgcn_readfirstlane(la))
                : "memory");
 }
 
