@@ -703,7 +703,8 @@ __global__ __launch_bounds__(256) void backward_kernel(const RouteBackwardArgs a
 #pragma unroll
   for (int v = 0; v < V; ++v) out[v] = 0.0f;
   const float gw = row_sum(e >= 0 ? g * w : w * 0.0f);  // (a NaN weight of a token that went nowhere stays)
-  if (!a.sigmoid && !a.renormalize) {
+  // (the logits of a token that went nowhere may be anything: they are not looked at)
+  if (!a.sigmoid && !a.renormalize && row_max(e >= 0 ? 1 : 0)) {
     float z[V];
     load<V>(z, row, a.dtype, first, a.experts);
     float m = z[0], sum = 0.0f;
