@@ -17,7 +17,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib as L
-from .muon import _record_on, _stream, _stream_object, batch, dtype_code
+from .muon import _made_on, _record_on, _stream, _stream_object, batch, dtype_code
 
 E4M3 = torch.float8_e4m3fn
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -40,7 +40,8 @@ def _same_device(device, t, name) -> None:
 
 def _enqueue(device, stream, fresh, fn, *args) -> None:
     """fn(*args, raw stream) with ``device`` current.  ``fresh``: tensors that
-    the call allocated, recorded on a stream that is not the current one."""
+    the call allocated, of the current stream's memory or of ``stream``'s: they
+    are used on both."""
     if device.type != "cuda":
         raise RuntimeError("the tensors are not on a GPU (there is no CPU path)")
     if device.index == torch.cuda.current_device():
@@ -48,19 +49,29 @@ def _enqueue(device, stream, fresh, fn, *args) -> None:
             fn(*args, _raw_stream(device.index))
         else:
             fn(*args, _stream(stream))
-            _record_on(_stream_object(stream), fresh)
+            _use(stream, fresh)
         return
     with torch.cuda.device(device):
         fn(*args, _raw_stream(device.index) if stream is None else _stream(stream))
-        _record_on(_stream_object(stream), fresh)
+        _use(stream, fresh)
+
+
+def _use(stream, tensors) -> None:
+    """Tensors of a call on ``stream``: the call's kernels write them there, and
+    what follows on the current stream reads them, each longer than the caller
+    may hold them.  The device is current."""
+    if stream is not None:
+        _record_on(_stream_object(stream), tensors)
+        _record_on(torch.cuda.current_stream(), tensors)
 
 
 def _filled(t, value, stream):
     """t, filled on the call's stream (results that no kernel computes)."""
     if t.is_cuda:
-        with torch.cuda.device(t.device), torch.cuda.stream(_stream_object(stream)):
-            t.fill_(value)
-            _record_on(_stream_object(stream), [t])
+        with torch.cuda.device(t.device):
+            with torch.cuda.stream(_stream_object(stream)):
+                t.fill_(value)
+            _use(stream, [t])
         return t
     return t.fill_(value)
 
@@ -183,8 +194,9 @@ def quantize(x, *, block_rows: int = 1, order: str = "rows", pairs: torch.Tensor
         _need(weights is None, "weights need pairs")
     fresh = []
     if out is None:
-        q = None if order == "cols" else BlockCodes.empty(rows, cols, block_rows, count, device)
-        qt = None if order == "rows" else BlockCodes.empty(cols, rows, block_rows, count, device)
+        q, qt = _made_on(stream, device, lambda: (
+            None if order == "cols" else BlockCodes.empty(rows, cols, block_rows, count, device),
+            None if order == "rows" else BlockCodes.empty(cols, rows, block_rows, count, device)))
         fresh = [t for one in (q, qt) if one is not None for t in (one.codes, one.scales)]
     else:
         q, qt = out if order == "both" else (None, out) if order == "cols" else (out, None)
@@ -240,11 +252,11 @@ def _matrix(t, what) -> L.MuonBatch:
                        dtype_code(t), 0)
 
 
-def _result(out, shape, dtype, accumulate, device):
+def _result(out, shape, dtype, accumulate, device, stream):
     """(the result's tensor, whether it was allocated here)."""
     if out is None:
         _need(not accumulate, "accumulate needs out")
-        return torch.empty(shape, dtype=dtype, device=device), True
+        return _made_on(stream, device, lambda: torch.empty(shape, dtype=dtype, device=device)), True
     if tuple(out.shape) != shape:
         raise ValueError(f"out must be {shape}, not {tuple(out.shape)}")
     _need(out.stride(-1) == 1 or out.shape[-1] <= 1, "out must be row-major (last stride 1)")
@@ -286,7 +298,7 @@ def block_matmul(a: BlockCodes, b: BlockCodes, *, out: torch.Tensor | None = Non
     _check_operands(a, b)
     _need(a.codes.dim() == b.codes.dim() and a.count == b.count, "a and b must be two matrices or two equal batches")
     shape = (a.rows, b.rows) if a.codes.dim() == 2 else (a.count, a.rows, b.rows)
-    c, made = _result(out, shape, dtype, accumulate, a.device)
+    c, made = _result(out, shape, dtype, accumulate, a.device, stream)
     if c.numel() == 0:
         return c
     if a.cols == 0:
@@ -309,7 +321,7 @@ def expert_matmul(a: BlockCodes, b: BlockCodes, offsets: torch.Tensor, *, out: t
     _need(a.codes.dim() == 2 and b.codes.dim() == 3, "a must be one matrix and b a batch")
     _check_offsets(offsets, a.device)
     _need(offsets.numel() == b.count + 1, "offsets must be one more than the experts")
-    c, made = _result(out, (a.rows, b.rows), dtype, accumulate, a.device)
+    c, made = _result(out, (a.rows, b.rows), dtype, accumulate, a.device, stream)
     if c.numel() == 0:
         return c
     _need(a.cols > 0, "no columns")
@@ -332,7 +344,7 @@ def expert_grad(a: BlockCodes, b: BlockCodes, offsets: torch.Tensor, *, out: tor
     _check_operands(a, b)
     _need(a.codes.dim() == 2 and b.codes.dim() == 2, "a and b must be one matrix each")
     _check_offsets(offsets, a.device)
-    c, made = _result(out, (offsets.numel() - 1, a.rows, b.rows), dtype, accumulate, a.device)
+    c, made = _result(out, (offsets.numel() - 1, a.rows, b.rows), dtype, accumulate, a.device, stream)
     if c.numel() == 0:
         return c
     if a.cols == 0:

@@ -30,7 +30,7 @@ import torch
 
 from . import _lib as L
 from .blocks import _enqueue, _filled, _matrix, _need, _same_device
-from .muon import dtype_code
+from .muon import _made_on, dtype_code
 from .multi import StepControl, _settle
 
 NO_EXPERT = -1
@@ -122,8 +122,9 @@ def route(logits: torch.Tensor, k: int, *, bias: torch.Tensor | None = None, sco
     # one buffer: experts, slots, pairs, offsets, and a workspace on a multiple of 16 bytes
     n = tokens * k
     end = -(-(2 * n + rows + experts + 1) // 4) * 4 if order else -(-n // 4) * 4
-    ints = torch.empty(end + ws, dtype=torch.int32, device=device)
-    weights = torch.empty((tokens, k), dtype=torch.float32, device=device)
+    ints, weights = _made_on(stream, device, lambda: (
+        torch.empty(end + ws, dtype=torch.int32, device=device),
+        torch.empty((tokens, k), dtype=torch.float32, device=device)))
     found = Routing(ints.as_strided((tokens, k), (k, 1)), weights,
                     ints.as_strided((tokens, k), (k, 1), n) if order else None,
                     ints.as_strided((rows,), (1,), 2 * n) if order else None,
@@ -158,7 +159,7 @@ def route_backward(logits: torch.Tensor, routing: Routing, grad_weights: torch.T
     _check(grad_weights, shape, torch.float32, "grad_weights", device)
     made = out is None
     if made:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=device)
+        out = _made_on(stream, device, lambda: torch.empty(logits.shape, dtype=logits.dtype, device=device))
     else:
         _need(out.shape == logits.shape and out.dtype == logits.dtype and (out.stride(1) == 1 or out.shape[1] <= 1),
               "out must have the logits' shape and type and last stride 1")
@@ -189,7 +190,7 @@ def expert_sum(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | Non
         _check(weights, (tokens, k), torch.float32, "weights", device)
     shape, made = (tokens, y.shape[1]), out is None
     if made:
-        out = torch.empty(shape, dtype=dtype or y.dtype, device=device)
+        out = _made_on(stream, device, lambda: torch.empty(shape, dtype=dtype or y.dtype, device=device))
     elif tuple(out.shape) != shape:
         raise ValueError(f"out must be {shape}, not {tuple(out.shape)}")
     _same_device(device, out, "out")
@@ -214,7 +215,7 @@ def expert_dot(grad: torch.Tensor, y: torch.Tensor, slots: torch.Tensor, *, out:
     _same_device(device, grad, "grad")
     made = out is None
     if made:
-        out = torch.empty((tokens, k), dtype=torch.float32, device=device)
+        out = _made_on(stream, device, lambda: torch.empty((tokens, k), dtype=torch.float32, device=device))
     else:
         _check(out, (tokens, k), torch.float32, "out", device)
     if out.numel() == 0:

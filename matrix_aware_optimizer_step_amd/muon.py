@@ -110,6 +110,16 @@ def _record_on(stream, tensors) -> None:
             t.record_stream(stream)
 
 
+def _made_on(stream, device, make):
+    """What ``make()`` allocates, as memory of the stream that a call runs on.
+    A block that the allocator takes back from the current stream may still be
+    in use by kernels queued there, which the call's stream does not wait for."""
+    if stream is None or torch.device(device).type != "cuda":
+        return make()
+    with torch.cuda.device(device), torch.cuda.stream(_stream_object(stream)):
+        return make()
+
+
 def _owned(batches) -> list:
     return [t for b in batches if b is not None for t in b.owned]
 

@@ -61,3 +61,60 @@ def test_gradient_of_rows_that_are_not_numbers_without_a_mask(mx, renormalize, s
     r = mx.route(z, 4, score=score, renormalize=renormalize)
     got = mx.route_backward(z, r, torch.ones(6, 4).cuda())
     assert got[1].isnan().all() and not got[2].any() and got[[0, 3, 4, 5]].isfinite().all()
+
+
+# ------------------------------------------------------------ streams
+
+def owner(t):
+    """The stream whose memory a tensor lies in."""
+    at = t.data_ptr()
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= at < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("no memory of the allocator")
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_results_are_memory_of_the_calls_stream(mx, handle):
+    """A block that the current stream's queued kernels still use must not go to a call on another stream."""
+    s = torch.cuda.Stream()
+    stream = s.cuda_stream if handle else s
+    x, w = matrix(200, 256, BF16, 1), matrix(96, 256, BF16, 2)
+    z = torch.randn(200, 8, device="cuda")
+    b3 = mx.quantize(torch.stack([w, w, w, w, w, w, w, w]), block_rows=128)
+    torch.cuda.synchronize()
+    q, qt = mx.quantize(x, order="both", stream=stream)
+    b = mx.quantize(w, block_rows=128, stream=stream)
+    c = mx.block_matmul(q, b, stream=stream)
+    r = mx.route(z, 2, align=128, stream=stream)
+    a, at = mx.quantize(x, pairs=(r.pairs, 2), order="both", stream=stream)
+    y = mx.expert_matmul(a, b3, r.offsets, stream=stream)
+    dw = mx.expert_grad(at, at, r.offsets, stream=stream)
+    out = mx.expert_sum(y, r.slots, r.weights, stream=stream)
+    dots = mx.expert_dot(out, y, r.slots, stream=stream)
+    dz = mx.route_backward(z, r, dots, stream=stream)
+    none = mx.route(z[:0], 2, align=8, stream=stream)
+    nothing = mx.expert_sum(y[:0], r.slots, stream=stream)
+    zeros = mx.block_matmul(mx.BlockCodes.empty(5, 0), mx.BlockCodes.empty(7, 0), stream=stream)
+    made = [q.codes, q.scales, qt.codes, qt.scales, b.codes, c, r.experts, r.weights, a.codes, at.scales, y, dw, out, dots,
+            dz, none.pairs, nothing, zeros]
+    assert {owner(t) for t in made} == {s.cuda_stream} and owner(x) == torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
+    assert torch.equal(c, mx.block_matmul(mx.quantize(x), mx.quantize(w, block_rows=128)))
+
+
+def test_results_of_another_stream_outlive_their_use_on_the_current_one(mx):
+    """Dropped while the current stream still reads it: its memory must not go to the other stream's next call."""
+    x = matrix(512, 2048, BF16, 1)
+    side = torch.cuda.Stream()
+    want = mx.quantize(x).codes.view(torch.uint8).clone()
+    torch.cuda.synchronize()
+    q = mx.quantize(x, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda._sleep(50_000_000)
+    got = q.codes.view(torch.uint8).clone()
+    del q
+    with torch.cuda.stream(side):
+        junk = [torch.full((512, 2048), 3, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and len(junk) == 8
