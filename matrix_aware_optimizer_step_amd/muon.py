@@ -176,7 +176,7 @@ def orthogonalize_grouped(ins, outs, sumsqs=None, steps: int = 5, coeffs=QUINTIC
     if ws is None:
         need = L.muon_orthogonalize_grouped_workspace([b.count for b in bi], [b.rows for b in bi],
                                                       [b.cols for b in bi], compute)
-        ws = workspace(need, device)
+        ws = workspace(need, device or bi[0].keep[-1].device)
     a, b, c = coeffs
     sp = None if sumsqs is None else [s.data_ptr() if s is not None else 0 for s in sumsqs]
     L.muon_orthogonalize_grouped([x.desc for x in bi], sp, [x.desc for x in bo], steps, a, b, c, eps, compute,
