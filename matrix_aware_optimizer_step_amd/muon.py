@@ -120,6 +120,11 @@ def _made_on(stream, device, make):
         return make()
 
 
+def _workspace(nbytes: int, device, stream) -> torch.Tensor:
+    """The workspace of a call on ``stream``."""
+    return _made_on(stream, device, lambda: workspace(nbytes, device))
+
+
 def _owned(batches) -> list:
     return [t for b in batches if b is not None for t in b.owned]
 
@@ -131,7 +136,7 @@ def momentum(grad, mom, nout, sumsq: torch.Tensor, beta: float = 0.95, nesterov:
     need = L.muon_momentum_workspace(g.count, g.rows, g.cols)
     own_ws = ws is None
     if ws is None:
-        ws = workspace(need, sumsq.device)
+        ws = _workspace(need, sumsq.device, stream)
     L.muon_momentum(g.desc, m.desc, n.desc if n else None, sumsq.data_ptr(), beta, nesterov,
                     ws.data_ptr(), ws.numel(), _stream(stream))
     _record_on(_stream_object(stream), ([ws] if own_ws else []) + _owned([g, m, n]))
@@ -147,7 +152,7 @@ def momentum_grouped(grads, moms, nouts, sumsqs, beta: float = 0.95, nesterov: b
     own_ws = ws is None
     if ws is None:
         need = L.muon_momentum_grouped_workspace([b.count for b in bg], [b.rows for b in bg], [b.cols for b in bg])
-        ws = workspace(need, sumsqs[0].device)
+        ws = _workspace(need, sumsqs[0].device, stream)
     L.muon_momentum_grouped([b.desc for b in bg], [b.desc for b in bm], None if bn is None else [b.desc for b in bn],
                             [s.data_ptr() for s in sumsqs], beta, nesterov, ws.data_ptr(), ws.numel(), _stream(stream))
     _record_on(_stream_object(stream), ([ws] if own_ws else []) + _owned(bg + bm + (bn or [])))
@@ -160,7 +165,8 @@ def orthogonalize(inp, out, sumsq: torch.Tensor | None = None, steps: int = 5, c
     own_ws = ws is None
     if ws is None:
         need = L.muon_orthogonalize_workspace(i.count, i.rows, i.cols, compute)
-        ws = workspace(need, device or (sumsq.device if sumsq is not None else i.keep[-1].device))
+        where = device or (sumsq.device if sumsq is not None else i.keep[-1].device)
+        ws = _workspace(need, where, stream)
     a, b, c = coeffs
     L.muon_orthogonalize(i.desc, sumsq.data_ptr() if sumsq is not None else None, o.desc, steps, a, b, c,
                          eps, compute, ws.data_ptr(), ws.numel(), _stream(stream))
@@ -176,7 +182,7 @@ def orthogonalize_grouped(ins, outs, sumsqs=None, steps: int = 5, coeffs=QUINTIC
     if ws is None:
         need = L.muon_orthogonalize_grouped_workspace([b.count for b in bi], [b.rows for b in bi],
                                                       [b.cols for b in bi], compute)
-        ws = workspace(need, device or bi[0].keep[-1].device)
+        ws = _workspace(need, device or bi[0].keep[-1].device, stream)
     a, b, c = coeffs
     sp = None if sumsqs is None else [s.data_ptr() if s is not None else 0 for s in sumsqs]
     L.muon_orthogonalize_grouped([x.desc for x in bi], sp, [x.desc for x in bo], steps, a, b, c, eps, compute,

@@ -14,7 +14,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib as L
-from .muon import _owned, _record_on, _stream, _stream_object, batch, workspace
+from .muon import _owned, _record_on, _stream, _stream_object, _workspace, batch, workspace
 
 # Adam's defaults ("LLM Optimizers", section 6); 0.9 for the statistics as
 # reported for the SOAP-Muon records ("初探优化器（一）", 7.2); refresh
@@ -62,7 +62,7 @@ def qr(a, q, ws: torch.Tensor | None = None, stream=None) -> None:
     need = L.soap_qr_workspace(ba.count, ba.rows)
     own_ws = ws is None
     if ws is None:
-        ws = workspace(need, bq.keep[-1].device)
+        ws = _workspace(need, bq.keep[-1].device, stream)
     L.soap_qr(ba.desc, bq.desc, ws.data_ptr(), ws.numel(), _stream(stream))
     _record_on(_stream_object(stream), ([ws] if own_ws else []) + _owned([ba, bq]))
 
@@ -74,7 +74,7 @@ def refresh(mbar, Lstat=None, Rstat=None, QL=None, QR=None, ws: torch.Tensor | N
     need = L.soap_refresh_workspace(bm.count, bm.rows, bm.cols, Lstat is not None, Rstat is not None)
     own_ws = ws is None
     if ws is None:
-        ws = workspace(need, bm.keep[-1].device)
+        ws = _workspace(need, bm.keep[-1].device, stream)
     L.soap_refresh(*map(_desc, bs), ws.data_ptr(), ws.numel(), _stream(stream))
     _record_on(_stream_object(stream), ([ws] if own_ws else []) + _owned(bs))
 
@@ -88,7 +88,7 @@ def refresh_grouped(mbars, Lstats, Rstats, QLs, QRs, ws: torch.Tensor | None = N
     if ws is None:
         need = L.soap_refresh_grouped_workspace([b.count for b in bm], [b.rows for b in bm], [b.cols for b in bm],
                                                 [x is not None for x in Lstats], [x is not None for x in Rstats])
-        ws = workspace(need, bm[0].keep[-1].device)
+        ws = _workspace(need, bm[0].keep[-1].device, stream)
     L.soap_refresh_grouped([_desc(b) for b in bl], [_desc(b) for b in br], [_desc(b) for b in bql],
                            [_desc(b) for b in bqr], [b.desc for b in bm], ws.data_ptr(), ws.numel(), _stream(stream))
     _record_on(_stream_object(stream), ([ws] if own_ws else []) + _owned(bm + bl + br + bql + bqr))
@@ -102,7 +102,7 @@ def precondition(grad, mbar, vbar, out, step: int, QL=None, QR=None, beta1: floa
     need = L.soap_precondition_workspace(bg.count, bg.rows, bg.cols)
     own_ws = ws is None
     if ws is None:
-        ws = workspace(need, bg.keep[-1].device)
+        ws = _workspace(need, bg.keep[-1].device, stream)
     L.soap_precondition(*map(_desc, bs), step, beta1, beta2, eps, ws.data_ptr(), ws.numel(), _stream(stream))
     _record_on(_stream_object(stream), ([ws] if own_ws else []) + _owned(bs))
 
@@ -117,7 +117,7 @@ def precondition_grouped(grads, mbars, vbars, outs, step: int, QLs, QRs, beta1: 
     if ws is None:
         need = L.soap_precondition_grouped_workspace([b.count for b in bg], [b.rows for b in bg],
                                                      [b.cols for b in bg])
-        ws = workspace(need, bg[0].keep[-1].device)
+        ws = _workspace(need, bg[0].keep[-1].device, stream)
     L.soap_precondition_grouped([b.desc for b in bg], [_desc(b) for b in bl], [_desc(b) for b in br],
                                 [b.desc for b in bm], [b.desc for b in bv], [b.desc for b in bo], step, beta1, beta2,
                                 eps, ws.data_ptr(), ws.numel(), _stream(stream))
