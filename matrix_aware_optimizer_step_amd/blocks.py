@@ -17,6 +17,7 @@ from __future__ import annotations
 import torch
 
 from . import _lib as L
+from .multi import _OnDevice
 from .muon import _made_on, _record_on, _stream, _stream_object, batch, dtype_code
 
 E4M3 = torch.float8_e4m3fn
@@ -213,7 +214,7 @@ def quantize(x, *, block_rows: int = 1, order: str = "rows", pairs: torch.Tensor
     return (q, qt) if order == "both" else q if qt is None else qt
 
 
-class WeightCodes:
+class WeightCodes(_OnDevice):
     """The codes of a weight, or of several equal ones (an expert layer's), kept
     in both orders and made anew from the weights by ``refresh()``.
 
@@ -230,17 +231,17 @@ class WeightCodes:
         _need(self.batch.rows > 0 and self.batch.cols > 0 and self.batch.count > 0, "no weights")
         count = None if isinstance(weights, torch.Tensor) and weights.dim() == 2 else self.batch.count
         device = first.device
-        self.device = device
         self.codes = BlockCodes.empty(self.batch.rows, self.batch.cols, L.CODE_BLOCK, count, device)
         self.transposed = BlockCodes.empty(self.batch.cols, self.batch.rows, L.CODE_BLOCK, count, device)
+        self._own(device, [t for q in (self.codes, self.transposed) for t in (q.codes, q.scales)] + self.batch.owned)
         self.refresh()
         torch.cuda.current_stream(device).synchronize()  # any stream may use them from here on
 
     def refresh(self, stream=None) -> None:
         """Enqueues ``muon_block_quantize`` of the weights as they are then."""
-        kept = [self.codes.codes, self.codes.scales, self.transposed.codes, self.transposed.scales]
-        _enqueue(self.device, stream, kept + self.batch.owned, L.muon_block_quantize, self.batch.desc, None, None, 1,
-                 self.codes.desc, self.transposed.desc)
+        raw = self._on(stream)
+        self._call(self._here(), L.muon_block_quantize, self.batch.desc, None, None, 1, self.codes.desc,
+                   self.transposed.desc, raw)
 
 
 def _matrix(t, what) -> L.MuonBatch:

@@ -31,7 +31,7 @@ import torch
 from . import _lib as L
 from .blocks import _enqueue, _filled, _matrix, _need, _same_device
 from .muon import _made_on, dtype_code
-from .multi import StepControl, _settle
+from .multi import StepControl, _OnDevice, _settle
 
 NO_EXPERT = -1
 
@@ -226,7 +226,7 @@ def expert_dot(grad: torch.Tensor, y: torch.Tensor, slots: torch.Tensor, *, out:
     return out
 
 
-class BalanceBias:
+class BalanceBias(_OnDevice):
     """The bias that keeps a router's experts evenly loaded, and the loads it
     goes by.
 
@@ -243,14 +243,19 @@ class BalanceBias:
         self.rate = float(rate)
         self.bias = torch.zeros(experts, dtype=torch.float32, device=device)
         self.loads = torch.zeros(experts, dtype=torch.int32, device=device)
-        _settle(self.bias.device)
+        self._control = None  # the one of the last step
+        self._own(self.bias.device, [self.bias, self.loads])
 
     def step(self, control: StepControl | None = None, stream=None) -> None:
-        device = self.bias.device
-        if control is not None and control.device != device:
+        if control is not None and control.device != self.device:
             raise ValueError("control is on another device than the bias")
-        _enqueue(device, stream, [self.bias, self.loads], L.muon_balance_update, self.bias.data_ptr(),
-                 self.loads.data_ptr(), self.bias.numel(), self.rate, None if control is None else control.data_ptr())
+        if control is not None and control is not self._control:
+            self._control = control
+            self._buffers = [self.bias, self.loads, control.block]
+            self._seen.clear()
+        raw = self._on(stream)
+        self._call(self._here(), L.muon_balance_update, self.bias.data_ptr(), self.loads.data_ptr(), self.bias.numel(),
+                   self.rate, None if control is None else control.data_ptr(), raw)
 
     def state_dict(self) -> dict:
         return {"bias": self.bias.to("cpu", copy=True), "loads": self.loads.to("cpu", copy=True), "rate": self.rate}

@@ -118,3 +118,46 @@ def test_results_of_another_stream_outlive_their_use_on_the_current_one(mx):
         junk = [torch.full((512, 2048), 3, dtype=torch.uint8, device="cuda") for _ in range(8)]
     torch.cuda.synchronize()
     assert torch.equal(got, want) and len(junk) == 8
+
+
+@pytest.mark.parametrize("explicit", [True, False])
+def test_dropped_codes_and_biases_outlive_their_kernels(mx, explicit):
+    """WeightCodes and BalanceBias, and the control block that a bias follows, are dropped while their kernels still wait
+    on a side stream: their memory must not go to new tensors before these ran."""
+    ws = [matrix(256, 512, BF16, s) for s in range(4)]
+    codes, bias, control = mx.WeightCodes(ws), mx.BalanceBias(512, rate=0.5), mx.StepControl("cuda")
+    sizes = [t.untyped_storage().nbytes() for t in (codes.codes.codes, codes.codes.scales, codes.batch.owned[0],
+                                                    bias.bias, bias.loads, control.block)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+        if not explicit:
+            codes.refresh()
+            bias.step(control)
+    if explicit:
+        codes.refresh(stream=side)
+        bias.step(control, stream=side)
+    del codes, bias, control
+    junk = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(24)]
+    torch.cuda.synchronize()
+    assert all((t == 7).all() for t in junk)
+
+
+def test_a_dropped_step_with_codes_on_a_side_stream(mx):
+    w = [matrix(128, 256, F32, s) for s in range(3)]
+    g = [0.01 * torch.randn_like(t) for t in w]
+    bias = mx.BalanceBias(256, rate=0.5)
+    opt = mx.OptimizerStep([(f"layers.{i}.w", a, b) for i, (a, b) in enumerate(zip(w, g))], max_grad_norm=1.0,
+                           codes={"w": [f"layers.{i}.w" for i in range(3)]}, balance=[bias])
+    sizes = [t.untyped_storage().nbytes() for t in (opt.codes["w"].codes.codes, opt.codes["w"].codes.scales,
+                                                    opt.codes["w"].batch.owned[0], bias.bias, bias.loads)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+        opt.step()
+    del opt, bias
+    junk = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(24)]
+    torch.cuda.synchronize()
+    assert all((t == 7).all() for t in junk)
