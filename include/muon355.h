@@ -718,8 +718,8 @@ typedef struct muon_codes {
  *         times weights[pairs[i]] when `weights` is not NULL, and zeros where
  *         pairs[i] < 0 (rows sent to experts, as muon_route lists them).
  *         x->count must be 1, block_rows 1; q has n rows and qt n columns.
- *         A pair behind x's last row gives zeros too.  Without pairs, k is 1
- *         and weights NULL.
+ *         A pair behind x's last row gives zeros too, and x may have no rows
+ *         at all (0, base NULL).  Without pairs, k is 1 and weights NULL.
  * q, qt : either may be NULL; equal counts and block_rows.
  */
 muon_status_t muon_block_quantize(const muon_batch_t* x, const int32_t* pairs, const float* weights, int64_t k,

@@ -161,7 +161,15 @@ extern "C" {
 muon_status_t muon_block_quantize(const muon_batch_t* x, const int32_t* pairs, const float* weights, int64_t k,
                                   const muon_codes_t* q, const muon_codes_t* qt, void* stream) {
   muon_status_t st;
-  if ((st = check_dense(x, "x")) != MUON_OK) return st;
+  muon_batch_t one;  // x without rows (every pair is behind them): nothing of it is read
+  if (x && x->rows == 0 && pairs) {
+    one = *x;
+    one.rows = 1;
+    one.base = const_cast<int32_t*>(pairs);
+    if ((st = check_dense(&one, "x")) != MUON_OK) return st;
+  } else if ((st = check_dense(x, "x")) != MUON_OK) {
+    return st;
+  }
   if (!q && !qt) return fail(MUON_ERR_INVALID_VALUE, "q and qt are both NULL");
   if (q && (st = check_codes(q, "q")) != MUON_OK) return st;
   if (qt && (st = check_codes(qt, "qt")) != MUON_OK) return st;

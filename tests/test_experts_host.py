@@ -1,8 +1,12 @@
-"""CPU checks of the expert operators' host side: whose memory a call's results are."""
+"""CPU checks of the expert operators' host side: whose memory a call's results
+are, what the calls accept."""
 
+import pytest
 import torch
 
+from matrix_aware_optimizer_step_amd import _lib as L
 from matrix_aware_optimizer_step_amd import muon as mu
+from tests import test_experts_binding as B
 
 
 class Within:
@@ -30,3 +34,19 @@ def test_memory_is_made_within_the_calls_stream(monkeypatch):
     assert mu._made_on(s, device, lambda: list(entered)) == [("device", device), ("stream", s)] and not entered
     assert mu._made_on(None, device, lambda: list(entered)) == []              # the current stream
     assert mu._made_on(s, torch.device("cpu"), lambda: list(entered)) == []
+
+
+def test_pairs_of_a_matrix_without_rows():
+    """An empty batch's order still has rows of -1: quantize passes them on, and the library takes x without rows there
+    only."""
+    def refused(x, pairs, **kw):
+        with pytest.raises(L.MuonError) as e:
+            L.muon_block_quantize(x, pairs, None, 1, B.codes(rows=7, cols=200, **kw), None, 0)
+        return e.value.status, str(e.value)
+
+    # (nothing here reaches a launch: the codes are refused after x has been accepted)
+    status, text = refused(B.dense(0, 200, base=None), B.FAKE, reserved=1)
+    assert status == B.INVALID and "q: reserved" in text
+    assert "x: 0 x 200" in refused(B.dense(0, 200, base=None), None)[1]
+    assert "x: ld" in refused(B.dense(0, 200, base=None, ld=100), B.FAKE)[1]
+    assert "codes' shape" in refused(B.dense(0, 199, base=None), B.FAKE)[1]

@@ -161,3 +161,62 @@ def test_a_dropped_step_with_codes_on_a_side_stream(mx):
     junk = [torch.full((n,), 7, dtype=torch.uint8, device="cuda") for n in sizes for _ in range(24)]
     torch.cuda.synchronize()
     assert all((t == 7).all() for t in junk)
+
+
+# ------------------------------------------------------------ empty batches
+
+@pytest.mark.parametrize("on_stream", [False, True])
+@pytest.mark.parametrize("align", [1, 8, 128])
+def test_a_layer_of_no_tokens(mx, align, on_stream):
+    """An empty micro-batch goes through the whole layer, forward and backward, and adds nothing."""
+    experts, k, width, outs = 5, 2, 200, 136
+    side = torch.cuda.Stream() if on_stream else None
+    w = mx.WeightCodes(torch.randn(experts, outs, width, device="cuda"))
+    x, z = torch.empty(0, width, dtype=BF16, device="cuda"), torch.empty(0, experts, device="cuda")
+    grad = torch.empty(0, outs, dtype=BF16, device="cuda")
+    loads = torch.zeros(experts, dtype=I32, device="cuda")
+    dw = torch.ones(experts, outs, width, device="cuda")
+    junk = torch.full((1 << 22,), 0x55, dtype=torch.uint8, device="cuda")  # what new memory would hold
+    torch.cuda.synchronize()
+    del junk
+    kw = dict(stream=side)
+    r = mx.route(z, k, align=align, loads=loads, **kw)
+    a, at = mx.quantize(x, pairs=(r.pairs, k), order="both", **kw)
+    rows = -(-experts * (align - 1) // align) * align
+    assert r.pairs.numel() == rows and (a.rows, a.cols, at.rows, at.cols) == (rows, width, width, rows)
+    y = mx.expert_matmul(a, w.codes, r.offsets, **kw)
+    out = mx.expert_sum(y, r.slots, r.weights, **kw)
+    g, gt = mx.quantize(grad, pairs=r.pairs, weights=r.weights, order="both", **kw)
+    mx.expert_grad(gt, at, r.offsets, out=dw, accumulate=True, **kw)
+    fresh = mx.expert_grad(gt, at, r.offsets, **kw)
+    dx = mx.expert_sum(mx.expert_matmul(g, w.transposed, r.offsets, **kw), r.slots, **kw)
+    dz = mx.route_backward(z, r, mx.expert_dot(grad, y, r.slots, **kw), **kw)
+    torch.cuda.synchronize()
+    assert (out.shape, dx.shape, dz.shape) == ((0, outs), (0, width), (0, experts)) and not loads.any()
+    assert (dw == 1).all() and not fresh.any()
+    for q in (a, at, g, gt):  # rows of -1 are zeros, the padding too
+        whole = q.codes.as_strided((q.rows, -(-q.cols // 128) * 128), q.codes.stride())
+        assert not raw(whole).any() and not q.scales.any()
+
+
+def test_zero_rows_for_pairs_into_given_codes(mx):
+    x = torch.empty(0, 300, device="cuda")
+    pairs = torch.full((7,), -1, dtype=I32, device="cuda")
+    q, qt = mx.BlockCodes.empty(7, 300), mx.BlockCodes.empty(300, 7)
+    wide = q.codes.as_strided((7, 384), (384, 1))
+    for t in (wide.view(torch.uint8), qt.codes.as_strided((300, 128), (128, 1)).view(torch.uint8)):
+        t.fill_(0x55)
+    q.scales.fill_(5.0)
+    qt.scales.fill_(5.0)
+    mx.quantize(x, pairs=pairs, order="both", out=(q, qt))
+    assert not raw(wide).any() and not q.scales.any() and not qt.scales.any()
+    assert not raw(qt.codes.as_strided((300, 128), (128, 1))).any()
+    # codes inside a wider buffer: what lies around them stays
+    big = torch.full((9, 640), 0x55, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    scales = torch.full((3, 10), 5.0, device="cuda")
+    part = mx.BlockCodes(big[1:8, 128:428], scales[:, 2:9])
+    mx.quantize(x, pairs=pairs, out=part)
+    left = raw(big)
+    assert not left[1:8, 128:512].any() and (left[[0, 8]] == 0x55).all()
+    assert (left[:, :128] == 0x55).all() and (left[:, 512:] == 0x55).all()
+    assert not scales[:, 2:9].any() and (scales[:, :2] == 5).all() and (scales[:, 9] == 5).all()
