@@ -66,12 +66,17 @@ def _use(stream, tensors) -> None:
         _record_on(torch.cuda.current_stream(), tensors)
 
 
-def _filled(t, value, stream):
-    """t, filled on the call's stream (results that no kernel computes)."""
+def _filled(t, value, stream, offsets=None):
+    """t, filled on the call's stream (results that no kernel computes); with
+    ``offsets`` its rows from the first of them to the last."""
     if t.is_cuda:
         with torch.cuda.device(t.device):
             with torch.cuda.stream(_stream_object(stream)):
-                t.fill_(value)
+                if offsets is None:
+                    t.fill_(value)
+                else:
+                    row = torch.arange(t.shape[0], device=t.device)
+                    t.masked_fill_(((row >= offsets[0]) & (row < offsets[-1]))[:, None], value)
             _use(stream, [t])
         return t
     return t.fill_(value)
@@ -325,7 +330,8 @@ def expert_matmul(a: BlockCodes, b: BlockCodes, offsets: torch.Tensor, *, out: t
     c, made = _result(out, (a.rows, b.rows), dtype, accumulate, a.device, stream)
     if c.numel() == 0:
         return c
-    _need(a.cols > 0, "no columns")
+    if a.cols == 0:
+        return c if accumulate else _filled(c, 0, stream, None if made else offsets)
     _enqueue(a.device, stream, [c] if made else [], L.muon_block_matmul, a.desc, b.desc, _c_desc(c),
              offsets.data_ptr(), L.PRODUCT_ROWS, int(bool(accumulate)))
     return c

@@ -220,3 +220,15 @@ def test_zero_rows_for_pairs_into_given_codes(mx):
     assert not left[1:8, 128:512].any() and (left[[0, 8]] == 0x55).all()
     assert (left[:, :128] == 0x55).all() and (left[:, 512:] == 0x55).all()
     assert not scales[:, 2:9].any() and (scales[:, :2] == 5).all() and (scales[:, 9] == 5).all()
+
+
+def test_products_of_no_columns(mx):
+    a, b = mx.BlockCodes.empty(6, 0), mx.BlockCodes.empty(7, 0, 128, 3)
+    o = torch.tensor([1, 3, 3, 5], dtype=I32).cuda()
+    for dtype in (F32, BF16):
+        assert not mx.expert_matmul(a, b, o, dtype=dtype)[1:5].any()
+        out = torch.full((6, 7), 4.0, dtype=dtype, device="cuda")
+        got = mx.expert_matmul(a, b, o, out=out)
+        assert got is out and not out[1:5].any() and (out[[0, 5]] == 4).all()  # rows of no expert stay
+    out = torch.full((6, 7), 4.0, device="cuda")
+    assert (mx.expert_matmul(a, b, o, out=out, accumulate=True) == 4).all()
