@@ -743,8 +743,10 @@ muon_status_t muon_block_quantize(const muon_batch_t* x, const int32_t* pairs, c
  *   offsets[e+1]-1 of C are those rows of A times B[e]^T.  Rows behind
  *   offsets[E] are left as they were.
  * MUON_PRODUCT_REDUCE: c holds E matrices, a and b one.  C[e] is the product
- *   over columns offsets[e] .. offsets[e+1]-1 alone; the offsets are multiples
- *   of 128 (the last one may be K).  An expert without columns gets zeros.
+ *   over columns offsets[e] .. offsets[e+1]-1 alone.  An expert without columns
+ *   gets zeros.  Offsets that are multiples of 128 are best: an expert that
+ *   starts or ends inside a block of columns shares that block's scales with
+ *   its neighbour, its NaN among them, and the block is read for both.
  *   A and B are codes of transposes here: C is a gradient of weights,
  *   rows(A) = outputs, rows(B) = inputs, columns = rows of activations.
  *

@@ -342,8 +342,9 @@ def expert_grad(a: BlockCodes, b: BlockCodes, offsets: torch.Tensor, *, out: tor
     """Every expert's weight gradient: C[e] = A[:, o_e:o_(e+1)] B[:, o_e:o_(e+1)]^T.
 
     ``a`` [outputs, rows] and ``b`` [inputs, rows] are codes of the transposes (of
-    the outputs' gradients and of the inputs, rows as ``offsets`` divides them,
-    each expert starting on a multiple of 128: ``route(align=128)``).  The result is
+    the outputs' gradients and of the inputs, rows as ``offsets`` divides them;
+    ``route(align=128)`` starts each expert on a block of its own, otherwise two
+    experts may share a block's scales).  The result is
     [experts, outputs, inputs]; ``accumulate`` adds to a float32 ``out``, which may
     be the gradient buffers that an optimizer step reads.  An expert without
     rows gets zeros, or stays as it is.

@@ -305,13 +305,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
 
   // the tile's rows [m0, m1) of A, the matrix of B and C, and its blocks of k
   int m0 = ti * BM, m1 = a.M, which = mat, kb0 = 0, nk = (a.K + 127) >> 7;
+  int cut_from = 0, cut_to = 128;  // the columns that count, from those of the first block to those of the last
   if (a.mode == GEMM_ROWS) {
     if (!find_rows<BM>(a, ti, which, m0, m1)) return;
   } else if (a.mode == GEMM_REDUCE) {
-    const int lo = offset_at(a.offsets, mat, a.K) >> 7, hi = (offset_at(a.offsets, mat + 1, a.K) + 127) >> 7;
-    kb0 = lo;
-    nk = hi > lo ? hi - lo : 0;
+    const int lo = offset_at(a.offsets, mat, a.K), hi = offset_at(a.offsets, mat + 1, a.K);
+    kb0 = lo >> 7;
+    nk = hi > lo ? ((hi + 127) >> 7) - kb0 : 0;
     if (nk == 0 && a.accumulate) return;
+    cut_from = lo & 127;
+    cut_to = hi - ((kb0 + nk - 1) << 7);
   }
   const int n0 = tj * BN;
   const int64_t amat = a.mode == GEMM_BATCH ? mat : 0, bmat = a.mode == GEMM_REDUCE ? 0 : which;
@@ -398,6 +401,21 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
       sa_next[i] = *reinterpret_cast<const float*>(s + a_scale + 64 * i);
       if (!SB) sa_next[i] *= sb;
     }
+  };
+  // A segment of k may start or end inside a block: A's codes there that belong
+  // to its neighbours become zeros, in LDS before a wave reads them for good.  (Where
+  // its borders are those of blocks this is two comparisons a tile; 16384 tokens,
+  // 8 of 128, 768 x 2048, added: 748 us with borders of blocks, 756 without.  Masks on the
+  // fragments inside the loop cost 30 registers and, at 128 x 128, scratch memory.)
+  auto cut = [&](uint32_t stage, int from, int to) __attribute__((always_inline)) {
+#pragma unroll 1
+    for (int x = threadIdx.x; x < BM * 32; x += 64 * NW) {  // four codes of a row
+      const int row = x >> 5, at = 4 * (x & 31);
+      const int lo = min(max(from - at, 0), 4), hi = max(min(max(to - at, 0), 4), lo);
+      *reinterpret_cast<uint32_t*>(smem + stage + row * 128 + (((at >> 4) ^ a_swizzle(row)) << 4) + (at & 15)) &=
+          static_cast<uint32_t>((uint64_t{1} << 8 * hi) - (uint64_t{1} << 8 * lo));
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   };
   auto add = [&](int i, int j) {  // a tile's sums, times their scales
 #pragma unroll
@@ -500,6 +518,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
     } else {
       wait_all_but<0>();
     }
+    if (cut_from > 0 || (nk == 1 && cut_to < 128)) cut(0, cut_from, nk == 1 ? cut_to : 128);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       read_a(smem, i);
@@ -509,6 +528,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
     set_b(0);
     read_scales(smem + ss);
     for (int kt = 0; kt + 1 < nk; ++kt) block(kt, std::false_type{});
+    if (nk > 1 && cut_to < 128) {  // what the last step has read of it is read again
+      cut(cs, 0, cut_to);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        read_a(smem + cs, i);
+        set_a(i);
+      }
+    }
     block(nk - 1, std::true_type{});
   }
 

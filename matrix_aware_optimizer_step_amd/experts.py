@@ -100,7 +100,7 @@ def route(logits: torch.Tensor, k: int, *, bias: torch.Tensor | None = None, sco
     (1 or 2) best, and the ``top_groups`` best stay.  ``mask`` (bool [tokens]): False
     sends a token nowhere (padding).  A logit of -inf takes its expert out.
     ``align``: each expert's rows are rounded up to a multiple of it (128 where
-    ``expert_grad`` follows).  ``loads`` (int32 [experts]): each expert's tokens are
+    ``expert_grad`` follows, so that no two experts share a block).  ``loads`` (int32 [experts]): each expert's tokens are
     added to it.  ``order=False`` leaves the order by expert out.
     """
     _check_logits(logits)

@@ -232,3 +232,56 @@ def test_products_of_no_columns(mx):
         assert got is out and not out[1:5].any() and (out[[0, 5]] == 4).all()  # rows of no expert stay
     out = torch.full((6, 7), 4.0, device="cuda")
     assert (mx.expert_matmul(a, b, o, out=out, accumulate=True) == 4).all()
+
+
+# ------------------------------------------------------------ gradients over segments anywhere
+
+SEGMENTS = [([5], 0, 0), ([5, 0, 130, 0, 1, 70], 0, 0), ([100, 27, 1, 300], 3, 77), ([0, 0, 0], 130, 200), ([1] * 40, 0, 9),
+            ([64, 64, 128, 129, 127, 0, 1], 1, 1), ([1, 600], 127, 0)]
+
+
+@pytest.mark.parametrize("lengths,lead,tail", SEGMENTS)
+@pytest.mark.parametrize("m,n", [(96, 200), (300, 129)])
+def test_expert_gradients_of_any_segments(mx, m, n, lengths, lead, tail):
+    """Segments that start and end inside a block of 128 rows (an order of align=1): each expert's rows alone count."""
+    at = [lead]
+    for length in lengths:
+        at.append(at[-1] + length)
+    rows = at[-1] + tail
+    a, b = mx.quantize(matrix(rows, m, F32, 1), order="cols"), mx.quantize(matrix(rows, n, F32, 2), order="cols")
+    va, vb = of(a), of(b)
+    offsets = torch.tensor(at, dtype=I32).cuda()
+    base = torch.randn(len(lengths), m, n, generator=torch.Generator().manual_seed(1)).cuda()
+    added = base.clone()
+    mx.expert_grad(a, b, offsets, out=added, accumulate=True)
+    fresh, low = mx.expert_grad(a, b, offsets), mx.expert_grad(a, b, offsets, dtype=BF16)
+    for e in range(len(lengths)):
+        lo, hi = at[e], at[e + 1]
+        if hi == lo:
+            assert torch.equal(added[e], base[e]) and not fresh[e].any() and not low[e].any()
+            continue
+        # rounding: a segment meets at most one block more than its length fills
+        want, size, lost = O.product(np.pad(va, ((0, 0), (0, 8)))[:, lo:hi], np.pad(vb, ((0, 0), (0, 8)))[:, lo:hi])
+        # the instruction's eight products are those of the whole rows: of the segment's, or of zeros
+        first, last = lo // 8 * 8, -(-hi // 8) * 8
+        inside = (np.arange(first, last) >= lo) & (np.arange(first, last) < hi)
+        lost = O.product((np.pad(va, ((0, 0), (0, 8)))[:, first:last] * inside),
+                         (np.pad(vb, ((0, 0), (0, 8)))[:, first:last] * inside))[2]
+        check_product(fresh[e], want, size, lost, hi - lo + 128)
+        check_product(low[e], want, size, lost, hi - lo + 128)
+        check_product(added[e], want, size, lost, hi - lo + 128, base[e].double().cpu().numpy())
+
+
+def test_expert_gradients_of_an_order_without_alignment(mx):
+    """route() as it is by default, and the gradient over its order."""
+    tokens, experts, k, width, outs = 300, 7, 2, 130, 90
+    x, grad = matrix(tokens, width, BF16, 3), matrix(tokens, outs, BF16, 4)
+    r = mx.route(torch.randn(tokens, experts, generator=torch.Generator().manual_seed(5)).cuda(), k)
+    _, xt = mx.quantize(x, pairs=(r.pairs, k), order="both")
+    _, gt = mx.quantize(grad, pairs=r.pairs, weights=r.weights, order="both")
+    got = mx.expert_grad(gt, xt, r.offsets)
+    va, vb, at = of(gt), of(xt), r.offsets.tolist()
+    for e in range(experts):
+        lo, hi = at[e], at[e + 1]
+        want, size, lost = O.product(va[:, lo:hi], vb[:, lo:hi])
+        check_product(got[e], want, size, lost, hi - lo + 128)
