@@ -816,7 +816,7 @@ typedef struct muon_route {
 /* Rows of the order: tokens*k + experts*(align-1), rounded up to a multiple of
  * align; 0 for arguments that muon_route refuses. */
 int64_t muon_route_capacity(int64_t tokens, int64_t experts, int64_t k, int64_t align);
-/* Bytes of device workspace of muon_route. */
+/* Bytes of device workspace of muon_route; enough for fewer tokens or experts too. */
 size_t muon_route_workspace(int64_t tokens, int64_t experts);
 
 /*

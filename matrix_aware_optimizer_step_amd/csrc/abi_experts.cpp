@@ -260,8 +260,11 @@ int64_t muon_route_capacity(int64_t tokens, int64_t experts, int64_t k, int64_t 
 
 size_t muon_route_workspace(int64_t tokens, int64_t experts) {
   if (!route_sizes_ok(tokens, experts, 1, 1)) return 0;
-  // the counts of every 16 or 64 tokens, a byte each
-  const size_t bytes = static_cast<size_t>(ceil_div(tokens, route_group(tokens, experts)) * (ceil_div(experts, 16) * 16));
+  // the counts of every 16 or 64 tokens, a byte each; never less than fewer tokens need
+  const int64_t few = tokens < kMostInRunsOf16 ? tokens : kMostInRunsOf16;
+  const int64_t runs = ceil_div(tokens, route_group(tokens, experts));
+  const int64_t before = ceil_div(few, route_group(few, experts));
+  const size_t bytes = static_cast<size_t>((runs > before ? runs : before) * (ceil_div(experts, 16) * 16));
   return bytes < 256 ? 256 : bytes;
 }
 

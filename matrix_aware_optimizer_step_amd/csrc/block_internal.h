@@ -76,9 +76,8 @@ struct RouteArgs {
   float scale;
 };
 // Tokens of a run, whose counts are one row of the workspace.
-constexpr int32_t route_group(int64_t tokens, int64_t experts) {
-  return tokens <= 64 || tokens > 16384 ? 64 : 16;
-}
+constexpr int64_t kMostInRunsOf16 = 16384;
+constexpr int32_t route_group(int64_t tokens, int64_t) { return tokens <= 64 || tokens > kMostInRunsOf16 ? 64 : 16; }
 hipError_t launch_route(const RouteArgs& a, hipStream_t stream);
 
 struct RouteBackwardArgs {

@@ -50,3 +50,17 @@ def test_pairs_of_a_matrix_without_rows():
     assert "x: 0 x 200" in refused(B.dense(0, 200, base=None), None)[1]
     assert "x: ld" in refused(B.dense(0, 200, base=None, ld=100), B.FAKE)[1]
     assert "codes' shape" in refused(B.dense(0, 199, base=None), B.FAKE)[1]
+
+
+def test_a_workspace_is_enough_for_fewer_tokens():
+    for experts in (1, 64, 100, 128, 512):
+        sizes = [L.muon_route_workspace(t, experts) for t in (1, 63, 64, 65, 1000, 16383, 16384, 16385, 20000, 65535, 65536,
+                                                                65537, 1 << 20)]
+        assert sizes == sorted(sizes)
+    assert L.muon_route_workspace(16385, 128) == L.muon_route_workspace(16384, 128) == 1024 * 128
+    assert L.muon_route_workspace(16385, 127) <= L.muon_route_workspace(16385, 129)
+    need = L.muon_route_workspace(16385, 128)
+    with pytest.raises(L.MuonError) as e:
+        L.muon_route(B.route_desc(tokens=16385, experts=128, ld=128), None, None, B.FAKE, B.FAKE, None, None, None, None,
+                     B.FAKE, need - 1, 0)
+    assert e.value.status == B.WORKSPACE
