@@ -292,7 +292,7 @@ __device__ __forceinline__ Choice choose(const RouteArgs& a, const float* z, con
     int g = g0, in = in0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if (!(kept >> g & 1u) || first + v >= a.experts) key[v] = -T(inf());
+      if (!(kept >> (g & 31) & 1u) || first + v >= a.experts) key[v] = -T(inf());  // (g: a group up to the last expert)
       if (++in == size) {
         in = 0;
         ++g;

@@ -63,6 +63,19 @@ def test_gradient_of_rows_that_are_not_numbers_without_a_mask(mx, renormalize, s
     assert got[1].isnan().all() and not got[2].any() and got[[0, 3, 4, 5]].isfinite().all()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,top,k", [(32, 5, 3), (64, 31, 16), (96, 2, 6), (160, 7, 8), (480, 32, 16)])
+def test_as_many_groups_as_there_may_be(mx, experts, top, k, score):
+    """32 groups of 1 to 15 experts: lanes behind the last expert belong to no group."""
+    z = torch.randn(100, experts, generator=torch.Generator().manual_seed(experts)).cuda()
+    bias = (0.1 * torch.randn(experts, generator=torch.Generator().manual_seed(1))).cuda()
+    for kw in (dict(), dict(bias=bias), dict(group_best=1)):
+        r = mx.route(z, k, groups=32, top_groups=top, score=score, **kw)
+        ref = dict(kw, bias=bias.double().cpu().numpy()) if "bias" in kw else kw
+        want, _ = X.route(z.double().cpu().numpy(), k, groups=32, top_groups=top, score=score, **ref)
+        assert np.array_equal(r.experts.cpu().numpy(), want)
+
+
 # ------------------------------------------------------------ streams
 
 def owner(t):
