@@ -298,3 +298,61 @@ def test_expert_gradients_of_an_order_without_alignment(mx):
         lo, hi = at[e], at[e + 1]
         want, size, lost = O.product(va[:, lo:hi], vb[:, lo:hi])
         check_product(got[e], want, size, lost, hi - lo + 128)
+
+
+# ------------------------------------------------------------ ties of codes
+
+def ties():
+    """Rows of 128 fp32 values with 24-bit significands: the first is the largest, 28 m, and 448 x / max|x| of each other
+    one lies exactly half-way between two codes."""
+    rng = np.random.default_rng(0)
+    odd, rows = np.arange(17, 32, 2), []
+    for r in range(256):
+        m = float(rng.integers(1 << 18, (1 << 24) // 31) | 1)
+        t = np.concatenate([odd * 2.0 ** (e - 1) for e in range(-6, 5)] + [(2 * np.arange(8) + 1) * 2.0 ** -10])
+        t = rng.permutation(t[t < 448])[:127]
+        t = np.concatenate([[448.0], t, np.zeros(127 - len(t))]) * rng.choice([-1.0, 1.0], 128)
+        rows.append(t)
+        rows[-1] = (t, m * 2.0 ** float(rng.integers(-90, 90)))
+    unit = np.stack([t for t, _ in rows])
+    factor = np.array([f for _, f in rows])[:, None]
+    return unit, factor
+
+
+def half_to_even(unit):
+    whole = np.floor(np.abs(unit) / O.step(unit))
+    even = np.where(np.abs(unit) / O.step(unit) % 1 == 0.5, whole + whole % 2, np.abs(unit) / O.step(unit))
+    return np.copysign(even * O.step(unit), unit)
+
+
+@pytest.mark.parametrize("order", ["rows", "cols", "both"])
+def test_ties_of_long_significands_go_to_even(mx, order):
+    unit, factor = ties()
+    x = (unit * factor / 16).astype(np.float32)
+    assert np.array_equal(x.astype(np.float64), unit * factor / 16)  # all of them floats, and 448 x / max is unit
+    want = half_to_even(unit)
+    if order != "cols":
+        q = mx.quantize(torch.from_numpy(x).cuda(), order=order)
+        q = q[0] if order == "both" else q
+        assert np.array_equal(O.TABLE[raw(q.codes)], want)
+    if order != "rows":  # the same blocks as columns
+        q = mx.quantize(torch.from_numpy(x.T.copy()).cuda(), order=order)
+        q = q[1] if order == "both" else q
+        assert np.array_equal(O.TABLE[raw(q.codes)], want)
+    if order == "rows":  # one block of 128 x 128
+        same = np.concatenate([unit[:1], unit[1:128]])
+        block = (same * factor[0] / 16).astype(np.float32)
+        q = mx.quantize(torch.from_numpy(block).cuda(), block_rows=128)
+        assert np.array_equal(O.TABLE[raw(q.codes)], half_to_even(same))
+
+
+@pytest.mark.parametrize("order", ["rows", "both"])
+def test_ties_of_weighted_bf16_rows_go_to_even(mx, order):
+    unit, factor = ties()
+    unit = np.where(np.abs(unit) >= 2.0 ** -6, unit, 0.0)
+    pairs = torch.arange(256, dtype=I32).cuda()
+    w = torch.from_numpy(factor.astype(np.float32)).cuda()
+    x = torch.from_numpy(unit / 16).to(BF16)
+    assert np.array_equal(x.double().numpy(), unit / 16)
+    q = mx.quantize(x.cuda(), pairs=pairs, weights=w, order=order)
+    assert np.array_equal(O.TABLE[raw((q[0] if order == "both" else q).codes)], half_to_even(unit))
