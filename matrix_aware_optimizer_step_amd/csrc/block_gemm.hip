@@ -549,13 +549,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void gemm_kernel(const BlockGemmAr
     for (int i = 0; i < MT; ++i) {
       const int m = m0 + arow + i * 16;
       if (m >= m1) continue;
-      char* row = C + m * a.c.ld * 4;
+      char* row = C + m * a.c.ld * 4 + static_cast<int64_t>(n_first) * 4;
       f32x4 old[NT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) old[j] = *(Global<const f32x4_any>)(row + 4 * (n_first + b_row<true>(j, 4 * g)));
+      for (int j = 0; j < NT; ++j) old[j] = *(Global<const f32x4_any>)(row + 4 * b_row<true>(j, 4 * g));
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        *(Global<f32x4_any>)(row + 4 * (n_first + b_row<true>(j, 4 * g))) = old[j] + acc[i][j];
+      for (int j = 0; j < NT; ++j) *(Global<f32x4_any>)(row + 4 * b_row<true>(j, 4 * g)) = old[j] + acc[i][j];
     }
     return;
   }

@@ -356,3 +356,23 @@ def test_ties_of_weighted_bf16_rows_go_to_even(mx, order):
     assert np.array_equal(x.double().numpy(), unit / 16)
     q = mx.quantize(x.cuda(), pairs=pairs, weights=w, order=order)
     assert np.array_equal(O.TABLE[raw((q[0] if order == "both" else q).codes)], half_to_even(unit))
+
+
+# ------------------------------------------------------------ columns past 32 bits of bytes
+
+def test_a_result_of_more_than_2_31_bytes_a_row_accumulates(mx):
+    """Column offsets in bytes pass 32 bits: 66 GiB of codes, all but the last rows zeros."""
+    n = (1 << 29) + 300
+    a = mx.quantize(torch.ones(1, 128, device="cuda"))
+    codes = torch.zeros(n, 128, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    few = mx.quantize(torch.arange(1, 401, dtype=F32, device="cuda")[:, None].expand(400, 128).contiguous())
+    codes[-400:] = few.codes
+    scales = torch.zeros(1, n, device="cuda")
+    scales[:, -400:] = few.scales
+    out = torch.ones(1, n, device="cuda")
+    mx.block_matmul(a, mx.BlockCodes(codes, scales), out=out, accumulate=True)
+    want = 1 + 128.0 * torch.arange(1, 401, device="cuda")
+    assert torch.all((out[0, -400:] - want).abs() <= 1e-5 * want)
+    assert bool((out[0, :-400] == 1).all())
+    del codes, scales, out
+    torch.cuda.empty_cache()
