@@ -34,6 +34,7 @@ from .muon import _made_on, dtype_code
 from .multi import StepControl, _OnDevice, _settle
 
 NO_EXPERT = -1
+_MOST = torch.finfo(torch.float32).max
 
 
 @dataclass
@@ -226,6 +227,13 @@ def expert_dot(grad: torch.Tensor, y: torch.Tensor, slots: torch.Tensor, *, out:
     return out
 
 
+def _rate(x) -> float:
+    x = float(x)
+    if not 0.0 <= x <= _MOST:  # (the library takes a float)
+        raise ValueError("rate must be finite and >= 0")
+    return x
+
+
 class BalanceBias(_OnDevice):
     """The bias that keeps a router's experts evenly loaded, and the loads it
     goes by.
@@ -240,7 +248,7 @@ class BalanceBias(_OnDevice):
     def __init__(self, experts: int, rate: float = 1e-3, device="cuda"):
         if not 1 <= experts <= L.MAX_EXPERTS:
             raise ValueError(f"experts outside [1, {L.MAX_EXPERTS}]")
-        self.rate = float(rate)
+        self.rate = _rate(rate)
         self.bias = torch.zeros(experts, dtype=torch.float32, device=device)
         self.loads = torch.zeros(experts, dtype=torch.int32, device=device)
         self._control = None  # the one of the last step
@@ -265,10 +273,13 @@ class BalanceBias(_OnDevice):
         for key, own in (("bias", self.bias), ("loads", self.loads)):
             if key not in state or state[key].shape != own.shape:
                 raise ValueError("the state was saved for another number of experts")
+        if "rate" not in state:
+            raise ValueError("the state was saved for something else than a balance bias")
+        _rate(state["rate"])
 
     def load_state_dict(self, state: dict) -> None:
         self.check_state(state)
         self.bias.copy_(state["bias"])
         self.loads.copy_(state["loads"])
-        self.rate = float(state["rate"])
+        self.rate = _rate(state["rate"])
         _settle(self.bias.device)

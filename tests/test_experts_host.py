@@ -4,6 +4,7 @@ are, what the calls accept."""
 import pytest
 import torch
 
+import matrix_aware_optimizer_step_amd as mx
 from matrix_aware_optimizer_step_amd import _lib as L
 from matrix_aware_optimizer_step_amd import muon as mu
 from tests import test_experts_binding as B
@@ -64,3 +65,22 @@ def test_a_workspace_is_enough_for_fewer_tokens():
         L.muon_route(B.route_desc(tokens=16385, experts=128, ld=128), None, None, B.FAKE, B.FAKE, None, None, None, None,
                      B.FAKE, need - 1, 0)
     assert e.value.status == B.WORKSPACE
+
+
+def test_a_rate_is_checked_before_a_step_begins():
+    """The library refuses such a rate too, but only once the step's other updates are on their way."""
+    for bad in (-0.1, float("nan"), float("inf"), 1e39):
+        with pytest.raises(ValueError, match="rate"):
+            mx.BalanceBias(4, bad, "cpu")
+    own, other = mx.BalanceBias(4, 0.5, "cpu"), mx.BalanceBias(4, 0.25, "cpu")
+    other.bias.fill_(1.0)
+    for change in (lambda s: s.pop("rate"), lambda s: s.update(rate=-1.0), lambda s: s.update(rate=float("nan"))):
+        state = other.state_dict()
+        change(state)
+        with pytest.raises(ValueError):
+            own.check_state(state)
+        with pytest.raises(ValueError):
+            own.load_state_dict(state)
+        assert not own.bias.any() and own.rate == 0.5  # nothing was loaded
+    own.load_state_dict(other.state_dict())
+    assert (own.bias == 1).all() and own.rate == 0.25
