@@ -709,14 +709,15 @@ typedef struct muon_codes {
  *   scale = max|x| / 448,   code = round(448 * x / max|x|)   over a block,
  *
  * to nearest, ties to even.  A quotient that fp32 holds is exact before that
- * rounding (so ties are ties), another within its last place.  A block whose largest magnitude is below 2^-100 gets scale 0 and codes 0.  A block
- * that holds a NaN or an infinity gets a scale that is not finite, and every
- * value of it is NaN: products pass it on.
+ * rounding (so ties are ties), another within its last place.  A block whose
+ * largest magnitude is below 2^-100 gets scale 0 and codes 0.  A block that
+ * holds a NaN or an infinity gets a scale that is not finite, and every value
+ * of it is NaN: products pass it on.
  *
  * x     : BF16 or F32, any alignment of its elements; read only.
  * pairs : NULL, or device int32[n]: row i of the codes is row pairs[i] / k of x,
- *         times weights[pairs[i]] when `weights` is not NULL, and zeros where
- *         pairs[i] < 0 (rows sent to experts, as muon_route lists them).
+ *         times weights[pairs[i]] (rounded to fp32) when `weights` is not
+ *         NULL, and zeros where pairs[i] < 0 (rows sent to experts, as muon_route lists them).
  *         x->count must be 1, block_rows 1; q has n rows and qt n columns.
  *         A pair behind x's last row gives zeros too, and x may have no rows
  *         at all (0, base NULL).  Without pairs, k is 1 and weights NULL.
@@ -732,8 +733,11 @@ muon_status_t muon_block_quantize(const muon_batch_t* x, const int32_t* pairs, c
  * fp32 and added to an fp32 sum, in an order that depends on the shapes alone:
  * the same call gives the same bits.
  *   BF16 results come from the matrix instruction for 8-bit floats, which drops
- *     what lies 13 bits below the largest of eight neighbouring products: about
- *     5e-5 of a result's size, a fortieth of its rounding to BF16.
+ *     what lies 13 bits below the largest of eight neighbouring products: less
+ *     than 2^-10 of it in all.  Where the products' signs are mixed at random
+ *     that is about 5e-5 of a result's size, a fortieth of its rounding to BF16;
+ *     a result that is small because its products cancel may lose more of its
+ *     own size (take F32 where that matters).
  *   F32 results (gradients that batches add to) come from the one for BF16, on
  *     codes that BF16 holds exactly: products are exact, sums fp32.
  *
@@ -780,8 +784,8 @@ muon_status_t muon_block_matmul(const muon_codes_t* a, const muon_codes_t* b, co
  * without a bias, in one group or with group_best 1, they are the logits.
  * A logit of -inf takes its expert out; where fewer than k are left the rest
  * of chosen is -1 with weight 0, and so is a token whose mask is 0.  A token
- * with a NaN (or +inf under softmax, or with a NaN bias) goes nowhere: -1, and its weights are
- * NaN, which muon_expert_sum passes on.
+ * with a NaN (or +inf under softmax, or with a NaN bias) goes nowhere: -1, and
+ * its weights are NaN, which muon_expert_sum passes on.
  *
  * The order of the (token, j) pairs by expert: expert e's rows are
  * offsets[e] .. offsets[e+1]-1, in the order of the tokens, each expert's rounded up
@@ -837,8 +841,9 @@ muon_status_t muon_route(const muon_route_t* r, const float* bias, const uint8_t
  * Gradient of the logits from the gradient of the weights, with chosen and
  * weights as muon_route wrote them for the same description (its groups, bias
  * and mask only chose).  grad_logits: [tokens, experts] of the logits' type,
- * ld_grad elements between tokens, written whole.  A NaN in a token's weights or their
- * gradients makes its row NaN.
+ * ld_grad elements between tokens, written whole.  A NaN in a token's weights,
+ * or in the gradient of one that has an expert, makes its row NaN.  A token
+ * without experts and with weights 0 gets zeros, whatever its logits are.
  */
 muon_status_t muon_route_backward(const muon_route_t* r, const int32_t* chosen, const float* weights,
                                   const float* grad_weights, void* grad_logits, int64_t ld_grad, void* stream);
@@ -858,7 +863,8 @@ muon_status_t muon_balance_update(float* bias, int32_t* loads, int64_t experts, 
  * of weights[t*k+j] * y[slots[t*k+j]], in fp32, rounded once (BF16 or F32,
  * whichever y has).  A slot that is negative or behind y's last row counts as
  * a row of zeros.  weights may be NULL (ones).  y and out: one matrix each,
- * equal cols; out has a row for each token.  k: 1 .. MUON_MAX_CHOSEN.
+ * equal cols; out has a row for each token and must not overlap y.
+ * k: 1 .. MUON_MAX_CHOSEN.
  */
 muon_status_t muon_expert_sum(const muon_batch_t* y, const int32_t* slots, const float* weights, int64_t k,
                               const muon_batch_t* out, void* stream);

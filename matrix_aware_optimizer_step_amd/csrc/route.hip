@@ -16,12 +16,18 @@
 // their best) they are compared as they are.  Where they are scores, rounded
 // to fp32, keys that lie within the rounding of each other and decide something
 // are computed again in fp64: the few experts in question, one a lane, put in
-// order among themselves (a token in a thousand); or the whole token, where it
-// is a border between groups, or more experts than lanes.
+// order among themselves; or the whole token, where it is a border between
+// groups, or more than 16 experts.  That is a token in a thousand where scores
+// and biases are spread, and most of them where many keys are equal or next to
+// each other: 5003 tokens of 128 experts take 8 to 9 us with random biases, 8 to
+// 14 with multiples of 1e-3 (as the bias's steps make them), and 18 where biases
+// are equal and most scores vanish (logits of +-16); of 256 in groups 14 to 15,
+// 15 to 31 and 31.
 //
-// Measured: 65536 tokens, 8 of 128, softmax 23 us for the choice (11 for one
-// expert instead of eight: each costs 1.7 us, 69 instructions for four tokens; the
-// logits' 34 MB are 5 us), 16 for the order, 10 for the gradient.  5003 tokens, 8 of
+// Measured: 65536 tokens, 8 of 128, softmax 30 us for the choice under the profiler
+// (each of the eight costs 69 instructions for four tokens; the logits' 34 MB are
+// 5 us), 11 for the order, 10 for the gradient (14 where it is not renormalised and
+// reads the logits).  5003 tokens, 8 of
 // 256 in groups by biased sigmoid scores: 15 and 10.  One token: 5.4.
 //
 // The order by expert needs no sort and no atomics on global memory: a token
@@ -557,7 +563,8 @@ __global__ __launch_bounds__((kThreadsOf<LANES, TOKENS>)) void route_kernel(cons
 
 // The pairs' order from the counts of every a.group tokens and the chosen experts.
 // Each workgroup sums all counts by itself (they are few and in L2), eight
-// experts a lane.
+// experts a lane.  That is quadratic in the tokens, and why the ABI layer refuses
+// more than 2^22 of them.
 __global__ __launch_bounds__(1024) void plan_kernel(const RouteArgs a) {
   constexpr int kParts = kPlanTokens / 64;
   __shared__ uint64_t mask[kParts][kMaxExperts];
