@@ -101,8 +101,9 @@ def route(logits: torch.Tensor, k: int, *, bias: torch.Tensor | None = None, sco
     (1 or 2) best, and the ``top_groups`` best stay.  ``mask`` (bool [tokens]): False
     sends a token nowhere (padding).  A logit of -inf takes its expert out.
     ``align``: each expert's rows are rounded up to a multiple of it (128 where
-    ``expert_grad`` follows, so that no two experts share a block).  ``loads`` (int32 [experts]): each expert's tokens are
-    added to it.  ``order=False`` leaves the order by expert out.
+    ``expert_grad`` follows, so that no two experts share a block).  ``loads``
+    (int32 [experts]): each expert's tokens are added to it.  ``order=False``
+    leaves the order by expert out.
     """
     _check_logits(logits)
     tokens, experts = logits.shape
@@ -183,7 +184,8 @@ def _check_slots(slots, device) -> None:
 def expert_sum(y: torch.Tensor, slots: torch.Tensor, weights: torch.Tensor | None = None, *,
                out: torch.Tensor | None = None, dtype=None, stream=None) -> torch.Tensor:
     """Each token's sum of weights[t, j] * y[slots[t, j]] (weights None: ones),
-    in fp32, rounded once to ``dtype`` (None: y's).  A slot of -1 adds nothing."""
+    in fp32, rounded once to ``dtype`` (None: y's).  A slot of -1 adds nothing
+    (a NaN weight is passed on).  ``out`` must not overlap y."""
     desc, device = _matrix(y, "y"), y.device
     _check_slots(slots, device)
     tokens, k = slots.shape
