@@ -20,7 +20,7 @@
 // rows of a fragment's read cover all 64 banks (no conflict is counted).
 //
 // Measured: 8192 x 14336 x 4096 into bf16 442 to 485 us (2.0 to 2.2 PFLOP/s,
-// by the box's clock; a plain 8-bit product with one scale runs in the library
+// by the card's clock; a plain 8-bit product with one scale runs in the library
 // in 382), 8192^3 443 (2.5; 355).  The matrix pipes are busy 57 % of the time.
 // Without the copies the loop is 17 % faster, without the scales' multiply-adds
 // 7 %, without the results' stores 13 % at K = 4096.  Prefetching lines into L2,
