@@ -716,11 +716,13 @@ typedef struct muon_codes {
  *
  * x     : BF16 or F32, any alignment of its elements; read only.
  * pairs : NULL, or device int32[n]: row i of the codes is row pairs[i] / k of x,
- *         times weights[pairs[i]] (rounded to fp32) when `weights` is not
- *         NULL, and zeros where pairs[i] < 0 (rows sent to experts, as muon_route lists them).
+ *         times weights[pairs[i]] when `weights` is not NULL, and zeros where
+ *         pairs[i] < 0 (rows sent to experts, as muon_route lists them).
  *         x->count must be 1, block_rows 1; q has n rows and qt n columns.
  *         A pair behind x's last row gives zeros too, and x may have no rows
  *         at all (0, base NULL).  Without pairs, k is 1 and weights NULL.
+ *         A row's weight falls out of the quotients of its own blocks (q); the
+ *         scales and the blocks of qt are those of products rounded to fp32.
  * q, qt : either may be NULL; equal counts and block_rows.
  */
 muon_status_t muon_block_quantize(const muon_batch_t* x, const int32_t* pairs, const float* weights, int64_t k,

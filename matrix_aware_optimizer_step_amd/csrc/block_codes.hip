@@ -65,8 +65,8 @@ __device__ __forceinline__ float quotient(float a, float rest, float b, float r)
 // took 10 % of the time of both orders.)  LONG: the values may have 24
 // significant bits, which times 0.875 are up to 27: what its product loses
 // joins the remainder (16384 x 4096 in both orders: fp32 84 us against 83
-// without, bf16 rows gathered and weighted 91 against 87).  Values that are bf16
-// lose nothing.
+// without, bf16 rows gathered and weighted, whose columns are such products, 91
+// against 87).  Values that are bf16 lose nothing.
 template <bool LONG>
 struct Divisor {
   float d, r;
@@ -84,6 +84,22 @@ struct Divisor {
 __device__ __forceinline__ float scale_of(float top) {
   return top < kTiny ? 0.0f : quotient(top, kTop, 1.0f / kTop);
 }
+
+// A block of one row times its weight w: the weight falls out of the quotients,
+// so the codes are the row's own (a tie stays one, which products rounded to
+// fp32 lose), with w's sign.  Not where the block is zeros or not finite by its
+// weight, or too small without it: the products' there.
+struct Weighted {
+  float all;     // the largest product
+  float factor;  // the values' on their way to the codes
+  float top;     // what the codes' values are at most
+  __device__ __forceinline__ Weighted(float most, float w) {
+    all = __builtin_fabsf(most * w);
+    const bool falls_out = most >= kTiny && all >= kTiny && all < __builtin_inff();
+    factor = falls_out ? __builtin_copysignf(1.0f, w) : w;
+    top = falls_out ? most : all;
+  }
+};
 
 // Four quotients as codes, to nearest, ties to even.
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
@@ -202,16 +218,21 @@ __global__ __launch_bounds__(kThreads) void rows_kernel(const QuantizeArgs a) {
     if (block * kCodeBlock >= a.cols) return;
     float top = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      if (PAIRS) v[b][k] *= w;
-      top = max_abs(top, v[b][k]);
-    }
+    for (int k = 0; k < 8; ++k) top = max_abs(top, v[b][k]);
     top = row_max(top);
-    const Divisor<!BF16 || PAIRS> div(top);
+    float all = top;
+    if (PAIRS) {
+      const Weighted x(top, w);
+      all = x.all;
+      top = x.top;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[b][k] *= x.factor;
+    }
+    const Divisor<!BF16> div(top);
     const u32x2 u = {encode4(div(v[b][0]), div(v[b][1]), div(v[b][2]), div(v[b][3])),
                      encode4(div(v[b][4]), div(v[b][5]), div(v[b][6]), div(v[b][7]))};
     write<STREAM>(reinterpret_cast<u32x2*>(out + block * kCodeBlock + 8 * lane), u);
-    if (lane == 0) scales[block * a.q.scale_ld] = scale_of(top);
+    if (lane == 0) scales[block * a.q.scale_ld] = scale_of(all);
   }
 }
 
@@ -231,17 +252,14 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(const QuantizeArgs a) {
   const char* base = matrix(a.x, mat);
   const int64_t c = c0 + 8 * tc;
   const int left = static_cast<int>(a.cols - c < 8 ? a.cols - c : 8);
-  float v[8][8];
+  float v[8][8], w[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t r = r0 + 8 * tr + i;
-    float w = 1.0f;
-    const char* src = r < a.rows ? source<BF16, PAIRS>(a, base, static_cast<int>(r), w) : nullptr;
+    w[i] = 1.0f;
+    const char* src = r < a.rows ? source<BF16, PAIRS>(a, base, static_cast<int>(r), w[i]) : nullptr;
     if (src && left > 0) {
       load8<BF16, STREAM>(v[i], src + c * (BF16 ? 2 : 4), left);
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (PAIRS) v[i][k] *= w;
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) v[i][k] = 0.0f;
@@ -276,17 +294,33 @@ __global__ __launch_bounds__(kThreads) void tile_kernel(const QuantizeArgs a) {
         for (int k = 0; k < 8; ++k) top = max_abs(top, v[i][k]);
         top = row_max(top);
       }
-      const Divisor<!BF16 || PAIRS> div(top);
+      float most = top, f = 1.0f;
+      if (PAIRS) {
+        const Weighted x(top, w[i]);
+        most = x.all;
+        top = x.top;
+        f = x.factor;
+      }
+      const Divisor<!BF16> div(top);
+      auto code4 = [&](const float* p) {
+        return PAIRS ? encode4(div(p[0] * f), div(p[1] * f), div(p[2] * f), div(p[3] * f))
+                     : encode4(div(p[0]), div(p[1]), div(p[2]), div(p[3]));
+      };
       if (r < a.rows) {
-        const u32x2 u = {encode4(div(v[i][0]), div(v[i][1]), div(v[i][2]), div(v[i][3])),
-                         encode4(div(v[i][4]), div(v[i][5]), div(v[i][6]), div(v[i][7]))};
+        const u32x2 u = {code4(v[i]), code4(v[i] + 4)};
         write<STREAM>(reinterpret_cast<u32x2*>(q + r * a.q.ld + c), u);
         if (!SQUARE && tc == 0)
-          a.q.scales[mat * a.q.scale_stride + bx * a.q.scale_ld + r] = scale_of(top);
+          a.q.scales[mat * a.q.scale_stride + bx * a.q.scale_ld + r] = scale_of(most);
       }
     }
   }
   if (!qt) return;
+  if (PAIRS) {  // a column's values have weights of their own
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[i][k] *= w[i];
+  }
   float top[8];
   if (!SQUARE) {
 #pragma unroll

@@ -376,3 +376,55 @@ def test_a_result_of_more_than_2_31_bytes_a_row_accumulates(mx):
     assert bool((out[0, :-400] == 1).all())
     del codes, scales, out
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------ weighted rows
+
+@pytest.mark.parametrize("order", ["rows", "both"])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_rows_weight_falls_out_of_its_own_blocks_codes(mx, dtype, order):
+    """code = round(448 w x / max|w x|): whatever the weight, a positive one gives the codes of the row alone, ties
+    among them, and a negative one their opposites."""
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(200, 300, generator=g).to(dtype)
+    x[3] = 0.0
+    x[4, 128:256] = 2.0 ** -99  # a whole block near the smallest
+    w = torch.randn(200, 1, generator=g) * torch.exp2(torch.randint(-20, 20, (200, 1), generator=g).float())
+    pairs = torch.arange(200, dtype=I32)
+    alone = mx.quantize(x.cuda())
+    got = mx.quantize(x.cuda(), pairs=pairs.cuda(), weights=w.cuda(), order=order)
+    got = got[0] if order == "both" else got
+    want = O.TABLE[raw(alone.codes)] * np.sign(w.numpy())
+    top = (x.abs().float() * w.abs()).numpy()  # products rounded to fp32, as the scale takes them
+    scale = O.tops(top.astype(np.float64), 1)
+    scale[scale < O.TINY] = 0.0
+    want = np.where(O.spread(scale, want.shape, 1) == 0, 0.0, want)
+    keep = np.ones(200, dtype=bool)
+    keep[4] = False  # its block's codes are zeros or those of the rounded products
+    assert np.array_equal(O.TABLE[raw(got.codes)][keep], want[keep])
+    assert np.array_equal(got.scales.cpu().numpy(), scale.astype(np.float32) / np.float32(448.0))
+
+
+@pytest.mark.parametrize("order", ["rows", "cols", "both"])
+def test_weights_out_of_range(mx, order):
+    """Weights of zero, not numbers, infinities, and such that take a row's values out of the range at either end."""
+    x = torch.randn(12, 128, generator=torch.Generator().manual_seed(1))
+    x[:, 5] = 0.0
+    x[8:10] *= 2.0 ** -110  # below the smallest block by itself
+    x[10] *= 2.0 ** 100
+    w = torch.tensor([1.0, 0.0, math.nan, math.inf, -math.inf, 2.0 ** -120, -0.0, -2.0, 2.0 ** 60, 1.0, 2.0 ** 100, 2.0 ** -40])
+    got = mx.quantize(x.cuda(), pairs=torch.arange(12, dtype=I32).cuda(), weights=w[:, None].cuda(), order=order)
+    rows = None if order == "cols" else (got[0] if order == "both" else got)
+    cols = None if order == "rows" else (got[1] if order == "both" else got)
+    if rows is not None:
+        v = rows.float().cpu()
+        assert v[[2, 3, 4, 10]].isnan().all()                      # (2^100 times 2^100 is no float)
+        assert not v[[1, 5, 6, 9]].any() and not rows.scales[0, [1, 5, 6, 9]].any()
+        for r in (0, 7, 8, 11):
+            true = x[r].double() * w[r].double()
+            top = true.abs().max()
+            assert (v[r].double() - true).abs().max() <= top * 2.0 ** -4 and v[r].isfinite().all()
+            assert abs(rows.scales[0, r].item() - top.item() / 448.0) <= top.item() / 448.0 * 2.0 ** -22
+    if cols is not None:  # a column's block holds all the rows
+        v = cols.float().cpu()
+        assert v.isnan().all()
